@@ -45,12 +45,20 @@ enum KernelId {
     kPagedRelease,
     kSentencePenalty,
     kSentenceReps,
+    kTokensRope,  // the order of CacheKernel (rkv_internal.h)
+    kTokensAppend,
+    kTokensQ4Append,
+    kQ4Read,
+    kAttention,
+    kAttentionQ4,
+    kAttentionCombine,
     kNumKernels
 };
 const char* const kKernelNames[kNumKernels] = {
     "key_stats", "importance", "importance_tc", "gram_tc", "gram_simt", "select", "gather",
     "identity_idx", "compact", "variant", "key_stats_paged", "compact_paged", "paged_release",
-    "sentence_penalty", "sentence_reps"};
+    "sentence_penalty", "sentence_reps", "rope", "paged_append", "q4_append", "q4_read",
+    "attention", "attention_q4", "attention_combine"};
 
 // ---------------------------------------------------------------- timing --
 // Events belong to the context they were created in, and a stream records
@@ -1044,6 +1052,31 @@ int rkv_paged_compress(const rkv_paged_desc* desc, void* K_pool, void* V_pool,
         });
     return e == cudaSuccess ? RKV_OK : RKV_ERR_CUDA;
 }
+
+}  // extern "C"
+
+namespace rkv {
+
+cudaError_t timed_cache(CacheKernel kernel, cudaStream_t s,
+                        cudaError_t (*launch)(const void*, cudaStream_t), const void* arg) {
+    return timed(kTokensRope + (int)kernel, s, [&] { return launch(arg, s); });
+}
+
+int check_paged_call(const rkv_paged_desc* d, const int32_t* table, PagedIn* pg) {
+    rkv_desc flat{};
+    const int rc = check_paged_desc(d, &flat);
+    if (rc) return rc;
+    pg->table = table;
+    pg->max_blocks = d->max_blocks_per_seq;
+    pg->log2bs = log2_exact(d->block_size);
+    pg->H = d->num_kv_heads;
+    pg->num_blocks = d->num_blocks;
+    return RKV_OK;
+}
+
+}  // namespace rkv
+
+extern "C" {
 
 int rkv_sentence_penalty(const rkv_sentences* sent, void* stream) {
     if (!sent) return RKV_ERR_INVALID_ARG;

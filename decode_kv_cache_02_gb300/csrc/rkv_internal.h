@@ -196,6 +196,104 @@ cudaError_t launch_variant(int64_t P, int N, int n_obs, const VariantIn& v, floa
 // records kDevErrTimeout in st after the wait limit (~1 s).
 cudaError_t launch_wait_timeout(DeviceStatus* st, cudaStream_t s);
 
+// Rows of heads of new tokens (rkv_rows with the element type left open).
+struct RowsView {
+    void* data = nullptr;
+    int64_t seq = 0, tok = 0, head = 0;  // strides in elements
+    int heads = 0;
+};
+
+// The four arrays of a 4-bit cache: codes (head_dim / 2 bytes a row) and
+// (scale, low) bf16 pairs (head_dim / 32 a row).
+struct Q4Pools {
+    uint8_t* k_codes = nullptr;
+    uint32_t* k_scales = nullptr;
+    uint8_t* v_codes = nullptr;
+    uint32_t* v_scales = nullptr;
+};
+
+// New tokens on their way to a cache, or through the rotation alone (table ==
+// nullptr): see rkv_rope_apply, rkv_paged_append, rkv_q4_append.
+struct TokenArgs {
+    int dtype = 0, d = 0;
+    int rot = 0;  // 0: no rotation
+    int interleaved = 0, inverse = 0;
+    float factor = 1.f;
+    uint64_t turns[RKV_MAX_ROT_DIM / 2];
+    int64_t num_tokens = 0, per_seq = 1;
+    const int32_t* positions = nullptr;
+    RowsView q, out_q, k, out_k, v;
+    // append
+    PagedIn pg;
+    int64_t num_seqs = 0;
+    const int32_t* lens = nullptr;
+    const int32_t* cu = nullptr;
+    void* k_pool = nullptr;
+    void* v_pool = nullptr;
+    bool q4 = false;
+    Q4Pools q4p;
+    DeviceStatus* status = nullptr;
+};
+cudaError_t launch_tokens(const TokenArgs& a, cudaStream_t s);
+
+struct Q4ReadArgs {
+    int dtype = 0, d = 0;
+    PagedIn pg;
+    int64_t num_seqs = 0;
+    const int32_t* lens = nullptr;
+    const int32_t* first = nullptr;
+    int n_rows = 0;
+    Q4Pools p;
+    void* out_k = nullptr;
+    void* out_v = nullptr;
+    DeviceStatus* status = nullptr;
+};
+cudaError_t launch_q4_read(const Q4ReadArgs& a, cudaStream_t s);
+
+// One attention call over a paged cache (bf16, fp32 or 4-bit).
+struct AttnArgs {
+    int dtype = 0, d = 0, G = 1;
+    bool q4 = false;
+    int n_new = 1, max_rows = 0;
+    int64_t num_seqs = 0;
+    PagedIn pg;
+    const void* k = nullptr;  // pools (unused with q4)
+    const void* v = nullptr;
+    Q4Pools q4p;
+    RowsView q, out;
+    const int32_t* lens = nullptr;
+    float scale = 1.f;
+    float* lse = nullptr;
+    float* partial = nullptr;  // attn_plan().partial_floats of scratch
+    DeviceStatus* status = nullptr;
+};
+// How a call is cut: row groups of `rows` queries per KV head, each
+// sequence's rows in chunks of `chunk`, at most `splits` of them.
+struct AttnPlan {
+    int rows = 8, groups = 1, chunk = 0, splits = 1;
+    int64_t ctas = 0;
+    size_t partial_floats = 0;
+};
+AttnPlan attn_plan(const AttnArgs& a);
+cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
+cudaError_t launch_attention_combine(const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
+
+// Runs `launch` with the library's timing and tracing around it (kernel: an
+// index of rkv_kernel_name).
+enum CacheKernel {
+    kCacheRope = 0,
+    kCacheAppend,
+    kCacheQ4Append,
+    kCacheQ4Read,
+    kCacheAttn,
+    kCacheAttnQ4,
+    kCacheAttnCombine
+};
+cudaError_t timed_cache(CacheKernel kernel, cudaStream_t s,
+                        cudaError_t (*launch)(const void*, cudaStream_t), const void* arg);
+// The paged descriptor's checks (an RKV_* code) and the table it describes.
+int check_paged_call(const rkv_paged_desc* d, const int32_t* table, PagedIn* pg);
+
 // rkv_compress_ex; with clear_status the workspace's device error word is
 // cleared (enqueued) once the arguments have passed every check; with lanes
 // the step may take the two-partition schedule (rkv_set_overlap), whose first

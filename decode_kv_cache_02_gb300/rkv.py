@@ -29,7 +29,9 @@ EXPORTED = [
     "rkv_score_ex", "rkv_paged_workspace_size", "rkv_paged_freed_per_seq", "rkv_paged_compress",
     "rkv_sentence_reps", "rkv_sentence_penalty", "rkv_selftest_wait_timeout",
     "rkv_noalloc_device_status", "rkv_noalloc_selftest_wait_timeout", "rkv_set_overlap",
-    "rkv_trace_enable", "rkv_trace_read",
+    "rkv_trace_enable", "rkv_trace_read", "rkv_rope_init", "rkv_rope_init_freqs",
+    "rkv_rope_apply", "rkv_paged_append", "rkv_q4_append", "rkv_q4_read",
+    "rkv_attention_workspace_size", "rkv_paged_attention", "rkv_q4_attention",
 ]
 RKV_MAX_POOL_WINDOW = 255
 RKV_ERR_DEVICE = 6
@@ -136,6 +138,30 @@ class _PagedDesc(ctypes.Structure):
                 ("max_blocks_per_seq", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("seq_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _RopeConfig(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("attn_factor", ctypes.c_double)]
+
+
+class _RopePlan(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("attn_factor", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("turns", ctypes.c_uint64 * 64)]
+
+
+class _Q4Cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -211,6 +237,32 @@ def load(path: str | None = None):
         lib.rkv_compress_noalloc.argtypes = [dp, vp, vp, vp, i32, i32, i32, f32, i32, f32, vp,
                                              vp, vp, vp]
         lib.rkv_compress_noalloc.restype = i32
+        rows, rope, q4 = (ctypes.POINTER(_Rows), ctypes.POINTER(_RopePlan),
+                          ctypes.POINTER(_Q4Cache))
+        lib.rkv_rope_init.argtypes = [ctypes.POINTER(_RopeConfig), rope]
+        lib.rkv_rope_init.restype = i32
+        lib.rkv_rope_init_freqs.argtypes = [i32, i32, ctypes.POINTER(ctypes.c_double),
+                                            ctypes.c_double, rope]
+        lib.rkv_rope_init_freqs.restype = i32
+        lib.rkv_rope_apply.argtypes = [rope, i32, i32, i64, i64, vp, i32, i32, rows, rows, i32,
+                                       rows, rows, vp]
+        lib.rkv_rope_apply.restype = i32
+        lib.rkv_paged_append.argtypes = [pdp, rope, vp, vp, vp, vp, i64, i32, vp, vp, rows, rows,
+                                         rows, rows, vp, vp]
+        lib.rkv_paged_append.restype = i32
+        lib.rkv_q4_append.argtypes = [pdp, rope, q4, vp, vp, i64, i32, vp, vp, rows, rows, rows,
+                                      rows, vp, vp]
+        lib.rkv_q4_append.restype = i32
+        lib.rkv_q4_read.argtypes = [pdp, q4, vp, vp, vp, i32, vp, vp, vp, vp]
+        lib.rkv_q4_read.restype = i32
+        lib.rkv_attention_workspace_size.argtypes = [pdp, i32, i32]
+        lib.rkv_attention_workspace_size.restype = sz
+        lib.rkv_paged_attention.argtypes = [pdp, i32, rows, vp, vp, vp, vp, i32, f32, rows, vp,
+                                            vp, sz, vp]
+        lib.rkv_paged_attention.restype = i32
+        lib.rkv_q4_attention.argtypes = [pdp, i32, rows, q4, vp, vp, i32, f32, rows, vp, vp, sz,
+                                         vp]
+        lib.rkv_q4_attention.restype = i32
         lib.rkv_kernel_name.argtypes = [i32]
         lib.rkv_kernel_name.restype = ctypes.c_char_p
         _lib = lib
@@ -486,7 +538,7 @@ def rkv_timing_enable(on: bool = True):
 def rkv_timing_read(reset: bool = True) -> dict:
     """{kernel name: (total ms, launches)} of the timed launches so far."""
     lib = load()
-    n = 16
+    n = 64
     ms = (ctypes.c_double * n)()
     cnt = (ctypes.c_int64 * n)()
     k = lib.rkv_timing_read(ms, cnt, n, 1 if reset else 0)

@@ -300,6 +300,165 @@ int rkv_paged_compress(const rkv_paged_desc* desc, void* K_pool, void* V_pool,
                        const rkv_variant* variant, int32_t* out_idx, int32_t* out_freed,
                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------ the cache in use --
+ * What a decode loop does with a paged cache between two compressions:
+ * rotate the new tokens' queries and keys by their positions, write the new
+ * rows through the block table (as they are, or at 4 bits), and attend over
+ * the rows.  After a compression a row of the cache is no longer its token's
+ * position, so the calls take the positions (int32 [tokens]) apart from the
+ * rows (lens).
+ *
+ * lens [num_seqs] int32: the rows in use of each sequence, counted with the
+ * tokens the call brings: the append writes rows lens[s] - n_s .. lens[s] - 1
+ * and the attention that follows reads rows 0 .. lens[s] - 1.
+ *
+ * New tokens come as rows of heads (rkv_rows): value d of head h of token j
+ * at data[j * token_stride + h * head_stride + d], or, in calls with the same
+ * number of tokens for every sequence, of token i of sequence s at
+ * data[s * seq_stride + i * token_stride + h * head_stride + d].  Strides
+ * count elements; data and every stride used are multiples of 16 bytes, so a
+ * slice of a fused projection is taken as it is. */
+typedef struct {
+    void* data;
+    int64_t seq_stride;   /* unused where tokens are numbered through */
+    int64_t token_stride;
+    int64_t head_stride;
+} rkv_rows;
+
+/* Rotary positions.  Pair i (0 <= i < rot_dim / 2) of a head is turned by
+ * pos * f_i:  (x, x') -> m (x cos - x' sin, x' cos + x sin), the pair being
+ * elements (i, i + rot_dim / 2) or, interleaved, (2i, 2i + 1); elements past
+ * rot_dim pass through.  f_i = base^(-2i / rot_dim), and for long contexts
+ *   LINEAR    f_i / factor
+ *   NTK       the base becomes base * factor^(rot_dim / (rot_dim - 2))
+ *   BY_PARTS  with t_i = original_len * f_i / (2 pi) turns over the trained
+ *             length and g = (t_i - low) / (high - low) cut to [0, 1]:
+ *             f_i (g + (1 - g) / factor)
+ * m = attn_factor (1 leaves lengths alone).  The plan is host memory, made
+ * once: it holds each f_i as a 64-bit fixed-point part of a turn, so pos * f_i
+ * is reduced exactly whatever the position (the angle is off by less than
+ * 2^-22 turns at position 2^31, by less than 2^-24 below 2^27). */
+enum {
+    RKV_ROPE_NONE = 0,
+    RKV_ROPE_LINEAR = 1,
+    RKV_ROPE_NTK = 2,
+    RKV_ROPE_BY_PARTS = 3
+};
+#define RKV_MAX_ROT_DIM 128
+typedef struct {
+    int32_t rot_dim;      /* even, 2 .. RKV_MAX_ROT_DIM                       */
+    int32_t interleaved;  /* 0 or 1                                           */
+    int32_t scaling;      /* RKV_ROPE_*                                       */
+    double base;          /* > 0                                              */
+    double factor;        /* > 0                                              */
+    double original_len;  /* > 0 for BY_PARTS                                 */
+    double low, high;     /* low < high for BY_PARTS                          */
+    double attn_factor;   /* m, finite                                        */
+} rkv_rope_config;
+typedef struct {
+    int32_t rot_dim;
+    int32_t interleaved;
+    float attn_factor;
+    int32_t reserved;
+    uint64_t turns[RKV_MAX_ROT_DIM / 2]; /* f_i / (2 pi) in units of 2^-64 turn */
+} rkv_rope_plan;
+
+/* Fill a plan from a configuration, or from rot_dim / 2 angles per position
+ * (radians, finite) of the caller's own.  Host only. */
+int rkv_rope_init(const rkv_rope_config* config, rkv_rope_plan* plan);
+int rkv_rope_init_freqs(int rot_dim, int interleaved, const double* freqs, double attn_factor,
+                        rkv_rope_plan* plan);
+
+/* out = the rows of q (q_heads per token) and, unless k is NULL, of k
+ * (k_heads per token) turned by their tokens' positions; inverse != 0 turns
+ * by the opposite angles, which is the gradient's map (the transpose).
+ * num_tokens tokens, tokens_per_seq of them (a divisor of num_tokens) per
+ * sequence for seq_stride.  An output may be its input (same pointer and
+ * strides); other overlaps are RKV_ERR_ALIAS.  fp32 arithmetic, one rounding. */
+int rkv_rope_apply(const rkv_rope_plan* plan, int dtype, int head_dim, int64_t num_tokens,
+                   int64_t tokens_per_seq, const int32_t* positions, int inverse, int q_heads,
+                   const rkv_rows* q, const rkv_rows* out_q, int k_heads, const rkv_rows* k,
+                   const rkv_rows* out_k, void* stream);
+
+/* Append to a paged cache (rkv_paged_desc; dtype is that of the pools and of
+ * k, v, q).  With cu_tokens NULL every sequence brings new_per_seq tokens
+ * (num_tokens = num_seqs * new_per_seq); otherwise sequence s brings tokens
+ * cu_tokens[s] .. cu_tokens[s + 1] - 1 ([num_seqs + 1] int32 on the device,
+ * ascending from 0), num_tokens bounds cu_tokens[num_seqs], and tokens past it
+ * (padding) are neither read nor written.  k and v have num_kv_heads heads.
+ * With a rope, k is turned by positions (NULL: by the rows it is written to);
+ * q (num_kv_heads * gqa_group heads; may be NULL) is turned the same way, or
+ * copied without a rope, into out_q (which may be q).  Rows outside the table
+ * and ids that name no block are recorded as a device error in `workspace`
+ * (NULL: not recorded; else 256-byte aligned, only its error word is used)
+ * and not written.  Two tokens of a call must not share a row of the pool.
+ * Nothing else of the pools changes. */
+int rkv_paged_append(const rkv_paged_desc* desc, const rkv_rope_plan* rope, void* K_pool,
+                     void* V_pool, const int32_t* block_table, const int32_t* lens,
+                     int64_t num_tokens, int new_per_seq, const int32_t* cu_tokens,
+                     const int32_t* positions, const rkv_rows* k, const rkv_rows* v,
+                     const rkv_rows* q, const rkv_rows* out_q, void* workspace, void* stream);
+
+/* A paged cache held in 4 bits.  Each row of head_dim values is stored in
+ * groups of 32 neighbours as x ~ scale * code + low:
+ *   low   the largest bf16 that is not above the group's smallest value,
+ *   scale the smallest bf16 that is not below (largest - low) / 15,
+ *   code  the whole number nearest to (x - low) * r, r the fp32 nearest to
+ *         1 / scale (0 where the scale is below 2^-126); halves go to even.
+ * A group that holds a NaN or an infinity, or whose range passes the largest
+ * float, reads as NaN.  codes [num_blocks, num_kv_heads, block_size,
+ * head_dim / 2] bytes: with W = head_dim / 32, 16-bit word g * W + w of a row
+ * holds values 32 w + 4 g .. 32 w + 4 g + 3 (lowest bits first), so that a
+ * lane's share of every group lies together.  scales [num_blocks,
+ * num_kv_heads, block_size, W, 2] bf16: (scale, low).  Codes are 16-byte
+ * aligned, scales too. */
+typedef struct {
+    void* k_codes;
+    void* k_scales;
+    void* v_codes;
+    void* v_scales;
+} rkv_q4_cache;
+
+/* rkv_paged_append into a 4-bit cache (desc->dtype: that of k, v and q). */
+int rkv_q4_append(const rkv_paged_desc* desc, const rkv_rope_plan* rope,
+                  const rkv_q4_cache* cache, const int32_t* block_table, const int32_t* lens,
+                  int64_t num_tokens, int new_per_seq, const int32_t* cu_tokens,
+                  const int32_t* positions, const rkv_rows* k, const rkv_rows* v,
+                  const rkv_rows* q, const rkv_rows* out_q, void* workspace, void* stream);
+
+/* Rows of a 4-bit cache as values: row first[s] + i (first NULL: i) of
+ * sequence s and head h, i < n_rows, to out_K and out_V
+ * [num_seqs * num_kv_heads, n_rows, head_dim] (desc->dtype; either may be
+ * NULL), the layout rkv_score and rkv_compress take.  Rows at or past lens[s]
+ * are not written. */
+int rkv_q4_read(const rkv_paged_desc* desc, const rkv_q4_cache* cache,
+                const int32_t* block_table, const int32_t* lens, const int32_t* first,
+                int n_rows, void* out_K, void* out_V, void* workspace, void* stream);
+
+/* Attention of the newest n_new (1 .. RKV_MAX_NEW_TOKENS) tokens of every
+ * sequence over its cache: token t sees rows j <= lens[s] - n_new + t,
+ *   out[s, t, head] = sum_j p_j V_j,  p = softmax_j(scale * q . K_j)
+ * with query heads h * gqa_group .. of KV head h.  A token that sees no row
+ * (lens[s] < n_new, or 0) gets zeros.  lse, unless NULL, receives
+ * log(sum_j exp(scale * q . K_j)) [num_seqs, n_new, heads] fp32 (-inf where
+ * nothing is seen).  Rows at or past lens[s] may hold anything.  max_rows (1
+ * .. the table's rows) bounds lens; a larger lens[s] is recorded as a device
+ * error and cut to it, a negative one likewise to 0, and rows whose id names
+ * no block are recorded and skipped.  Sums, the softmax's statistics and the
+ * output before its one rounding are fp32; bf16 and 4-bit caches round the
+ * probabilities to bf16 for the second product.
+ * q, out: rkv_rows by sequence and token (bf16 for 4-bit caches). */
+#define RKV_MAX_NEW_TOKENS 64
+size_t rkv_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int max_rows);
+int rkv_paged_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
+                        const void* K_pool, const void* V_pool, const int32_t* block_table,
+                        const int32_t* lens, int max_rows, float scale, const rkv_rows* out,
+                        float* lse, void* workspace, size_t workspace_bytes, void* stream);
+int rkv_q4_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
+                     const rkv_q4_cache* cache, const int32_t* block_table,
+                     const int32_t* lens, int max_rows, float scale, const rkv_rows* out,
+                     float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 /* The selection alone: for scores Z [P, n] (fp32), out_idx [P, budget] as
  * rkv_compress would produce it (top budget-n_obs of the candidates
  * 0..n-n_obs-1 by Z, ties to the larger index, then the n_obs observation
