@@ -5,68 +5,65 @@ As in ``rkv``: tensor metadata is checked here, outputs the caller did not pass
 are allocated, raw pointers and the stream go to the library, and there is no
 fallback.  Calls run on the device of their tensors and, unless ``stream`` is
 given, on that device's current stream.
+
+These calls run for every layer of every token, and a decode step's kernels
+take a few microseconds, so the common case (tensors on the current device, the
+current stream) takes no context manager, and descriptors are packed bytes.
 """
 from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
-from .rkv import (RKV_DTYPE_BF16, RKV_DTYPE_FP32, _PagedDesc, _Q4Cache, _RopeConfig, _RopePlan,
-                  _Rows, _check, load)
+from .rkv import (RKV_DTYPE_BF16, RKV_DTYPE_FP32, _Q4Cache, _RopeConfig, _RopePlan, _check, load)
 
 RKV_MAX_NEW_TOKENS = 64
 _DTYPE = {torch.bfloat16: RKV_DTYPE_BF16, torch.float32: RKV_DTYPE_FP32}
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
-_byref = ctypes.byref
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+_pack_rows = struct.Struct("@Pqqq").pack      # rkv_rows
+_pack_desc = struct.Struct("@q7i4x").pack     # rkv_paged_desc
+_pack_q4 = struct.Struct("@4P").pack          # rkv_q4_cache
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-class _Call:
-    """The device and stream of a call: entered, its device is current and
-    what is allocated belongs to its stream."""
-
-    __slots__ = ("device", "stream", "_dev", "_str")
-
-    def __init__(self, t: torch.Tensor, stream):
-        if not t.is_cuda:
-            raise ValueError("the tensors must be CUDA tensors")
-        self.device, self.stream = t.device, stream
-        self._dev = self._str = None
-
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self._dev = torch.cuda.device(self.device)
-            self._dev.__enter__()
-        if self.stream is not None:
-            if self.stream.device != self.device:
-                self.__exit__()
-                raise ValueError("stream and tensors must be on one device")
-            self._str = torch.cuda.stream(self.stream)
-            self._str.__enter__()
-            return self.stream.cuda_stream
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self._str is not None:
-            self._str.__exit__(None, None, None)
-            self._str = None
-        if self._dev is not None:
-            self._dev.__exit__(None, None, None)
-            self._dev = None
-        return False
+def _elsewhere(fn, t: torch.Tensor, stream, *args, **kw):
+    """fn on another stream, or on tensors of another device than the current
+    one: what it allocates belongs to that stream."""
+    if not t.is_cuda:
+        raise ValueError("the tensors must be CUDA tensors")
+    if stream is not None and stream.device != t.device:
+        raise ValueError("stream and tensors must be on one device")
+    with torch.cuda.device(t.device):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
 
 
-def _same_device(ref: torch.Tensor, **tensors):
-    dev = ref.device
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}")
+def _away(t: torch.Tensor, stream) -> bool:
+    return stream is not None or not t.is_cuda or t.get_device() != _current_device()
 
 
-def _int32(t, name: str, shape):
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+def _ints(t, name: str, dev: int, *shape) -> int:
+    """The address of a contiguous int32 tensor."""
+    if t.dtype != _I32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 {list(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the other tensors")
+    return t.data_ptr()
+
+
+def _token_ints(t, name: str, dev: int, tokens: int) -> int:
+    if t.dtype != _I32 or t.numel() != tokens or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32, one per token")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the other tensors")
+    return t.data_ptr()
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -76,35 +73,38 @@ def _dtype(t: torch.Tensor) -> int:
     return c
 
 
-def _rows(t: torch.Tensor, name: str, heads, d: int, dtype, tokens: int, per_seq: int) -> _Rows:
+def _rows(t, name: str, dev: int, heads, d: int, dtype, tokens: int, per_seq: int) -> bytes:
     """The rows of [tokens, heads, d] or [seqs, per_seq, heads, d], strides as
-    they are."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
+    they are, as an rkv_rows."""
     sh, st = t.shape, t.stride()
-    if t.dim() == 4:
-        ok = sh[0] * sh[1] == tokens and sh[1] == per_seq
-        seq, tok = st[0], st[1]
-    elif t.dim() == 3:
-        ok, seq, tok = sh[0] == tokens, per_seq * st[0], st[0]
+    if len(sh) == 4:
+        seqs, n, h, e = sh
+        ok = n == per_seq and seqs * n == tokens
+        seq, tok, head, one = st
+    elif len(sh) == 3:
+        n, h, e = sh
+        ok = n == tokens
+        tok, head, one = st
+        seq = per_seq * tok
     else:
-        ok, seq, tok = False, 0, 0
-    if not ok or sh[-2] != heads or sh[-1] != d:
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {d}] or "
-                         f"[{tokens // max(per_seq, 1)}, {per_seq}, {heads}, {d}]")
-    if st[-1] != 1 and d > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    return _Rows(t.data_ptr(), seq, tok, st[-2])
+        ok, h, e, one = False, 0, 0, 1
+    if not ok or h != heads or e != d or t.dtype != dtype or one != 1:
+        raise ValueError(f"{name} must be {dtype} [{tokens}, {heads}, {d}] or [{tokens // max(per_seq, 1)}, "
+                         f"{per_seq}, {heads}, {d}] with a contiguous last dimension")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the other tensors")
+    return _pack_rows(t.data_ptr(), seq, tok, head)
 
 
-def _workspace(ws, name="workspace"):
+def _workspace(ws, dev: int):
+    """(address, bytes) of a workspace; its error word needs 256 bytes."""
     if ws is None:
         return None, 0
-    if not ws.is_cuda or not ws.is_contiguous() or ws.dtype != torch.uint8:
-        raise ValueError(f"{name} must be a contiguous CUDA uint8 tensor")
-    if ws.numel() < 256:
-        raise ValueError(f"{name} must hold at least 256 bytes")
-    return ws.data_ptr(), ws.numel()
+    n = ws.numel()
+    if ws.dtype != _U8 or n < 256 or not ws.is_contiguous() or ws.get_device() != dev:
+        raise ValueError("workspace must be a contiguous uint8 tensor of at least 256 bytes on the "
+                         "device of the other tensors")
+    return ws.data_ptr(), n
 
 
 # ------------------------------------------------------------------ rotary --
@@ -122,24 +122,23 @@ class RopePlan:
                  low: float = 1.0, high: float = 32.0, attn_factor: float = 1.0, freqs=None):
         if scaling not in _SCALING:
             raise ValueError(f"scaling must be one of {sorted(_SCALING)}")
-        self._c = _RopePlan()
+        c = _RopePlan()
         if freqs is not None:
             f = [float(x) for x in freqs]
             if 2 * len(f) != int(rot_dim):
                 raise ValueError("freqs must hold rot_dim / 2 angles")
             arr = (ctypes.c_double * max(len(f), 1))(*f)
             rc = load().rkv_rope_init_freqs(int(rot_dim), 1 if interleaved else 0, arr,
-                                            float(attn_factor), _byref(self._c))
+                                            float(attn_factor), ctypes.byref(c))
             _check(rc, "rkv_rope_init_freqs")
         else:
-            c = _RopeConfig(int(rot_dim), 1 if interleaved else 0, _SCALING[scaling], float(base),
-                            float(factor), float(original_len), float(low), float(high),
-                            float(attn_factor))
-            _check(load().rkv_rope_init(_byref(c), _byref(self._c)), "rkv_rope_init")
-
-    @property
-    def rot_dim(self) -> int:
-        return self._c.rot_dim
+            cfg = _RopeConfig(int(rot_dim), 1 if interleaved else 0, _SCALING[scaling], float(base),
+                              float(factor), float(original_len), float(low), float(high),
+                              float(attn_factor))
+            _check(load().rkv_rope_init(ctypes.byref(cfg), ctypes.byref(c)), "rkv_rope_init")
+        self._c = c
+        self._packed = bytes(c)
+        self.rot_dim = int(rot_dim)
 
 
 def rkv_rope_apply(rope: RopePlan, positions, q, k=None, out_q=None, out_k=None,
@@ -147,102 +146,104 @@ def rkv_rope_apply(rope: RopePlan, positions, q, k=None, out_q=None, out_k=None,
     """q (and k) [tokens, heads, d] or [seqs, n, heads, d] turned by positions
     (int32, one per token); inverse=True turns back, the map of the gradients.
     Outputs may be the inputs.  Returns out_q, or (out_q, out_k) with k."""
-    with _Call(q, stream) as s:
-        _same_device(q, k=k, positions=positions, out_q=out_q, out_k=out_k)
-        if q.dim() not in (3, 4):
-            raise ValueError("q must be [tokens, heads, d] or [seqs, n, heads, d]")
-        d, hq = q.shape[-1], q.shape[-2]
-        per = q.shape[1] if q.dim() == 4 else q.shape[0]
-        tokens = q.shape[0] * q.shape[1] if q.dim() == 4 else q.shape[0]
-        if positions.dtype != torch.int32 or positions.numel() != tokens \
-                or not positions.is_contiguous():
-            raise ValueError("positions must be contiguous int32, one per token")
-        dt = _dtype(q)
-        if out_q is None:
-            out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        rq = _rows(q, "q", hq, d, q.dtype, tokens, per)
-        ro = _rows(out_q, "out_q", hq, d, q.dtype, tokens, per)
-        rk = rko = None
-        hk = 0
-        if k is not None:
-            if k.dim() not in (3, 4):
-                raise ValueError("k must be [tokens, heads, d] or [seqs, n, heads, d]")
-            hk = k.shape[-2]
-            if out_k is None:
-                out_k = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-            rk = _rows(k, "k", hk, d, q.dtype, tokens, per)
-            rko = _rows(out_k, "out_k", hk, d, q.dtype, tokens, per)
-        elif out_k is not None:
-            raise ValueError("out_k without k")
-        rc = load().rkv_rope_apply(rope._c, dt, d, tokens, max(per, 1), positions.data_ptr(),
-                                   1 if inverse else 0, hq, rq, ro, hk, rk, rko, s)
-    _check(rc, "rkv_rope_apply")
+    if _away(q, stream):
+        return _elsewhere(rkv_rope_apply, q, stream, rope, positions, q, k, out_q, out_k, inverse)
+    dev = q.get_device()
+    sh = q.shape
+    if len(sh) == 3:
+        tokens, hq, d = sh
+        per = tokens
+    elif len(sh) == 4:
+        seqs, per, hq, d = sh
+        tokens = seqs * per
+    else:
+        raise ValueError("q must be [tokens, heads, d] or [seqs, n, heads, d]")
+    dt, code = q.dtype, _dtype(q)
+    if out_q is None:
+        out_q = torch.empty(sh, dtype=dt, device=q.device)
+    rk = rko = None
+    hk = 0
+    if k is not None:
+        hk = k.shape[-2] if k.dim() > 1 else 0
+        if out_k is None:
+            out_k = torch.empty(k.shape, dtype=dt, device=q.device)
+        rk = _rows(k, "k", dev, hk, d, dt, tokens, per)
+        rko = _rows(out_k, "out_k", dev, hk, d, dt, tokens, per)
+    elif out_k is not None:
+        raise ValueError("out_k without k")
+    rc = load().rkv_rope_apply(rope._packed, code, d, tokens, per or 1,
+                               _token_ints(positions, "positions", dev, tokens),
+                               1 if inverse else 0, hq, _rows(q, "q", dev, hq, d, dt, tokens, per),
+                               _rows(out_q, "out_q", dev, hq, d, dt, tokens, per), hk, rk, rko,
+                               _raw_stream(dev))
+    if rc:
+        _check(rc, "rkv_rope_apply")
     return out_q if k is None else (out_q, out_k)
 
 
 # ------------------------------------------------------------------ append --
 
-def _append(call, where, cache_args, ref, desc_shape, k, v, block_table, lens, cu_tokens, rope,
-            positions, q, out_q, workspace, s):
-    nb, H, bs, d = desc_shape
-    _same_device(ref, k=k, v=v, block_table=block_table, lens=lens, cu_tokens=cu_tokens,
-                 positions=positions, q=q, out_q=out_q, workspace=workspace)
+def _append(call, where, cache_args, dev, shape, k, v, block_table, lens, cu_tokens, rope,
+            positions, q, out_q, workspace):
+    nb, H, bs, d = shape
     if block_table.dim() != 2:
         raise ValueError("block_table must be int32 [num_seqs, max_blocks_per_seq]")
     S, mb = block_table.shape
-    _int32(block_table, "block_table", (S, mb))
-    _int32(lens, "lens", (S,))
-    if k.dim() not in (3, 4):
-        raise ValueError("k must be [tokens, H, d] or [seqs, n, H, d]")
-    tokens = k.shape[0] if k.dim() == 3 else k.shape[0] * k.shape[1]
-    if cu_tokens is not None:
-        if k.dim() != 3:
-            raise ValueError("with cu_tokens, tokens are numbered through: k [tokens, H, d]")
-        _int32(cu_tokens, "cu_tokens", (S + 1,))
-        per, new = tokens, 0
+    dims = k.dim()
+    if dims == 3:
+        tokens = k.shape[0]
+    elif dims == 4:
+        tokens = k.shape[0] * k.shape[1]
     else:
-        if S == 0 or tokens % S != 0:
-            if tokens != 0:
-                raise ValueError("without cu_tokens every sequence brings the same number of tokens")
-        new = tokens // S if S else 0
-        per = new
-    if positions is not None and (positions.dtype != torch.int32 or positions.numel() != tokens
-                                  or not positions.is_contiguous()):
-        raise ValueError("positions must be contiguous int32, one per token")
-    if positions is not None and rope is None:
-        raise ValueError("positions without a rope")
-    dt = _dtype(k)
-    rk = _rows(k, "k", H, d, k.dtype, tokens, per)
-    rv = _rows(v, "v", H, d, k.dtype, tokens, per)
+        raise ValueError("k must be [tokens, H, d] or [seqs, n, H, d]")
+    cu = pos = None
+    new = 0
+    if cu_tokens is not None:
+        if dims != 3:
+            raise ValueError("with cu_tokens, tokens are numbered through: k [tokens, H, d]")
+        cu = _ints(cu_tokens, "cu_tokens", dev, S + 1)
+        per = tokens
+    else:
+        if tokens and (S == 0 or tokens % S):
+            raise ValueError("without cu_tokens every sequence brings the same number of tokens")
+        per = new = tokens // S if S else 0
+    if positions is not None:
+        if rope is None:
+            raise ValueError("positions without a rope")
+        pos = _token_ints(positions, "positions", dev, tokens)
+    dt, code = k.dtype, _dtype(k)
     rq = ro = None
     G = 1
     if q is not None:
-        hq = q.shape[-2]
-        if hq % H != 0 or hq == 0:
+        hq = q.shape[-2] if q.dim() > 1 else 0
+        G = hq // H if H else 0
+        if G == 0 or G * H != hq:
             raise ValueError("the heads of q must be a multiple of the KV heads")
-        G = hq // H
         if out_q is None:
             out_q = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        rq = _rows(q, "q", hq, d, k.dtype, tokens, per)
-        ro = _rows(out_q, "out_q", hq, d, k.dtype, tokens, per)
+        rq = _rows(q, "q", dev, hq, d, dt, tokens, per)
+        ro = rq if out_q is q else _rows(out_q, "out_q", dev, hq, d, dt, tokens, per)
     elif out_q is not None:
         raise ValueError("out_q without q")
-    wp, _ = _workspace(workspace)
-    desc = _PagedDesc(S, H, G, d, bs, nb, mb, dt)
-    rc = call(desc, None if rope is None else rope._c, *cache_args, block_table.data_ptr(),
-              lens.data_ptr(), tokens, new, None if cu_tokens is None else cu_tokens.data_ptr(),
-              None if positions is None else positions.data_ptr(), rk, rv, rq, ro, wp, s)
-    _check(rc, where)
+    rc = call(_pack_desc(S, H, G, d, bs, nb, mb, code), None if rope is None else rope._packed,
+              *cache_args, _ints(block_table, "block_table", dev, S, mb),
+              _ints(lens, "lens", dev, S), tokens, new, cu, pos,
+              _rows(k, "k", dev, H, d, dt, tokens, per), _rows(v, "v", dev, H, d, dt, tokens, per),
+              rq, ro, _workspace(workspace, dev)[0], _raw_stream(dev))
+    if rc:
+        _check(rc, where)
     return out_q
 
 
-def _pool_shape(K_pool, V_pool):
-    if K_pool.dim() != 4 or V_pool.shape != K_pool.shape or V_pool.dtype != K_pool.dtype:
-        raise ValueError("K_pool, V_pool must be [num_blocks, H, block_size, head_dim] of one dtype")
-    if not K_pool.is_contiguous() or not V_pool.is_contiguous():
-        raise ValueError("K_pool, V_pool must be contiguous")
-    _same_device(K_pool, V_pool=V_pool)
-    return K_pool.shape
+def _pools(K_pool, V_pool, dev: int):
+    """The pools' common shape."""
+    sh = K_pool.shape
+    if len(sh) != 4 or V_pool.shape != sh or V_pool.dtype != K_pool.dtype \
+            or not K_pool.is_contiguous() or not V_pool.is_contiguous() \
+            or V_pool.get_device() != dev:
+        raise ValueError("K_pool, V_pool must be contiguous [num_blocks, H, block_size, head_dim] "
+                         "of one dtype on one device")
+    return sh
 
 
 def rkv_paged_append(K_pool, V_pool, k, v, block_table, lens, cu_tokens=None,
@@ -254,13 +255,16 @@ def rkv_paged_append(K_pool, V_pool, k, v, block_table, lens, cu_tokens=None,
     without, every sequence the same number) or [S, n, H, d].  positions
     default to the rows written.  q is turned (without a rope: copied) into
     out_q, which is returned (None without q)."""
-    with _Call(K_pool, stream) as s:
-        shape = _pool_shape(K_pool, V_pool)
-        if k.dtype != K_pool.dtype:
-            raise ValueError("k, v and the pools must share a dtype")
-        return _append(load().rkv_paged_append, "rkv_paged_append",
-                       (K_pool.data_ptr(), V_pool.data_ptr()), K_pool, shape, k, v, block_table,
-                       lens, cu_tokens, rope, positions, q, out_q, workspace, s)
+    if _away(K_pool, stream):
+        return _elsewhere(rkv_paged_append, K_pool, stream, K_pool, V_pool, k, v, block_table,
+                          lens, cu_tokens, rope, positions, q, out_q, workspace)
+    dev = K_pool.get_device()
+    shape = _pools(K_pool, V_pool, dev)
+    if k.dtype != K_pool.dtype:
+        raise ValueError("k, v and the pools must share a dtype")
+    return _append(load().rkv_paged_append, "rkv_paged_append",
+                   (K_pool.data_ptr(), V_pool.data_ptr()), dev, shape, k, v, block_table, lens,
+                   cu_tokens, rope, positions, q, out_q, workspace)
 
 
 # ------------------------------------------------------------------ 4 bits --
@@ -272,21 +276,23 @@ class Q4Cache:
 
     def __init__(self, K_codes, K_scales, V_codes, V_scales):
         for t, n in ((K_codes, "K_codes"), (V_codes, "V_codes")):
-            if t.dtype != torch.uint8 or t.dim() != 4 or not t.is_contiguous() or not t.is_cuda:
+            if t.dtype != _U8 or t.dim() != 4 or not t.is_contiguous() or not t.is_cuda:
                 raise ValueError(f"{n} must be contiguous CUDA uint8 [num_blocks, H, block_size, d/2]")
         nb, H, bs, half = K_codes.shape
         for t, n in ((K_scales, "K_scales"), (V_scales, "V_scales")):
-            if t.dtype != torch.bfloat16 or tuple(t.shape) != (nb, H, bs, half // 16, 2) \
-                    or not t.is_contiguous() or half % 16:
+            if t.dtype != torch.bfloat16 or half % 16 or not t.is_contiguous() \
+                    or t.shape != (nb, H, bs, half // 16, 2):
                 raise ValueError(f"{n} must be contiguous bf16 [num_blocks, H, block_size, d/32, 2]")
         if V_codes.shape != K_codes.shape:
             raise ValueError("K_codes and V_codes must have one shape")
-        _same_device(K_codes, K_scales=K_scales, V_codes=V_codes, V_scales=V_scales)
+        if any(t.device != K_codes.device for t in (K_scales, V_codes, V_scales)):
+            raise ValueError("the arrays must be on one device")
         self.K_codes, self.K_scales, self.V_codes, self.V_scales = (K_codes, K_scales, V_codes,
                                                                     V_scales)
         self.shape = (nb, H, bs, 2 * half)
         self._c = _Q4Cache(K_codes.data_ptr(), K_scales.data_ptr(), V_codes.data_ptr(),
                            V_scales.data_ptr())
+        self._packed = bytes(self._c)
 
 
 def alloc_q4_cache(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int,
@@ -294,8 +300,8 @@ def alloc_q4_cache(num_blocks: int, num_kv_heads: int, block_size: int, head_dim
     """A zeroed 4-bit cache (5 bits a value with its scales)."""
     t = []
     for _ in range(2):
-        t.append(torch.zeros((num_blocks, num_kv_heads, block_size, head_dim // 2),
-                             dtype=torch.uint8, device=device))
+        t.append(torch.zeros((num_blocks, num_kv_heads, block_size, head_dim // 2), dtype=_U8,
+                             device=device))
         t.append(torch.zeros((num_blocks, num_kv_heads, block_size, head_dim // 32, 2),
                              dtype=torch.bfloat16, device=device))
     return Q4Cache(*t)
@@ -305,10 +311,13 @@ def rkv_q4_append(cache: Q4Cache, k, v, block_table, lens, cu_tokens=None,
                   rope: RopePlan | None = None, positions=None, q=None, out_q=None,
                   workspace=None, stream=None):
     """rkv_paged_append into a 4-bit cache (k, v, q bf16 or fp32)."""
-    with _Call(cache.K_codes, stream) as s:
-        return _append(load().rkv_q4_append, "rkv_q4_append", (cache._c,), cache.K_codes,
-                       cache.shape, k, v, block_table, lens, cu_tokens, rope, positions, q, out_q,
-                       workspace, s)
+    at = cache.K_codes
+    if _away(at, stream):
+        return _elsewhere(rkv_q4_append, at, stream, cache, k, v, block_table, lens, cu_tokens,
+                          rope, positions, q, out_q, workspace)
+    return _append(load().rkv_q4_append, "rkv_q4_append", (cache._packed,), at.get_device(),
+                   cache.shape, k, v, block_table, lens, cu_tokens, rope, positions, q, out_q,
+                   workspace)
 
 
 def rkv_q4_read(cache: Q4Cache, block_table, lens, n_rows: int, first=None, out_K=None,
@@ -317,50 +326,48 @@ def rkv_q4_read(cache: Q4Cache, block_table, lens, n_rows: int, first=None, out_
     None: from row 0) as values [S * H, n_rows, d], the layout of rkv_score and
     rkv_compress.  Rows at or past lens[s] are not written (zeros where the
     output is allocated here)."""
+    at = cache.K_codes
+    if _away(at, stream):
+        return _elsewhere(rkv_q4_read, at, stream, cache, block_table, lens, n_rows, first, out_K,
+                          out_V, dtype, workspace)
+    dev = at.get_device()
     nb, H, bs, d = cache.shape
-    with _Call(cache.K_codes, stream) as s:
-        _same_device(cache.K_codes, block_table=block_table, lens=lens, first=first, out_K=out_K,
-                     out_V=out_V, workspace=workspace)
-        if block_table.dim() != 2:
-            raise ValueError("block_table must be int32 [num_seqs, max_blocks_per_seq]")
-        S, mb = block_table.shape
-        _int32(block_table, "block_table", (S, mb))
-        _int32(lens, "lens", (S,))
-        if first is not None:
-            _int32(first, "first", (S,))
-        shape = (S * H, int(n_rows), d)
-        if out_K is None:
-            out_K = torch.zeros(shape, dtype=dtype if out_V is None else out_V.dtype,
-                                device=cache.K_codes.device)
-        if out_V is None:
-            out_V = torch.zeros(shape, dtype=out_K.dtype, device=cache.K_codes.device)
-        for t, n in ((out_K, "out_K"), (out_V, "out_V")):
-            if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype != out_K.dtype:
-                raise ValueError(f"{n} must be contiguous {list(shape)}, K and V of one dtype")
-        wp, _ = _workspace(workspace)
-        desc = _PagedDesc(S, H, 1, d, bs, nb, mb, _dtype(out_K))
-        rc = load().rkv_q4_read(desc, cache._c, block_table.data_ptr(), lens.data_ptr(),
-                                None if first is None else first.data_ptr(), int(n_rows),
-                                out_K.data_ptr(), out_V.data_ptr(), wp, s)
-    _check(rc, "rkv_q4_read")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [num_seqs, max_blocks_per_seq]")
+    S, mb = block_table.shape
+    n_rows = int(n_rows)
+    shape = (S * H, n_rows, d)
+    if out_K is None:
+        out_K = torch.zeros(shape, dtype=dtype if out_V is None else out_V.dtype, device=at.device)
+    dt, code = out_K.dtype, _dtype(out_K)
+    if out_V is None:
+        out_V = torch.zeros(shape, dtype=dt, device=at.device)
+    for t, n in ((out_K, "out_K"), (out_V, "out_V")):
+        if t.shape != shape or t.dtype != dt or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{n} must be contiguous {list(shape)}, K and V of one dtype, on the "
+                             "cache's device")
+    rc = load().rkv_q4_read(_pack_desc(S, H, 1, d, bs, nb, mb, code), cache._packed,
+                            _ints(block_table, "block_table", dev, S, mb),
+                            _ints(lens, "lens", dev, S),
+                            None if first is None else _ints(first, "first", dev, S), n_rows,
+                            out_K.data_ptr(), out_V.data_ptr(), _workspace(workspace, dev)[0],
+                            _raw_stream(dev))
+    if rc:
+        _check(rc, "rkv_q4_read")
     return out_K, out_V
 
 
 # --------------------------------------------------------------- attention --
 
-def _attention_shape(q, H: int):
-    if q.dim() != 4 or q.shape[2] == 0 or q.shape[2] % H != 0:
-        raise ValueError("q must be [num_seqs, n_new, H * gqa_group, d]")
-    return q.shape
-
-
 def rkv_attention_workspace_size(q, num_kv_heads: int, max_rows: int) -> int:
     """Workspace bytes of rkv_paged_attention and rkv_q4_attention for q [S,
     n_new, heads, d] over at most max_rows rows a sequence."""
-    S, T, hq, d = _attention_shape(q, num_kv_heads)
-    desc = _PagedDesc(S, num_kv_heads, hq // num_kv_heads, d, 1, 1, max(int(max_rows), 1),
-                      _dtype(q))
-    n = int(load().rkv_attention_workspace_size(_byref(desc), T, int(max_rows)))
+    H = int(num_kv_heads)
+    if q.dim() != 4 or H < 1 or q.shape[2] == 0 or q.shape[2] % H:
+        raise ValueError("q must be [num_seqs, n_new, H * gqa_group, d]")
+    S, T, hq, d = q.shape
+    desc = _pack_desc(S, H, hq // H, d, 1, 1, max(int(max_rows), 1), _dtype(q))
+    n = int(load().rkv_attention_workspace_size(desc, T, int(max_rows)))
     if n == 0:
         raise ValueError("invalid workspace request")
     return n
@@ -368,45 +375,50 @@ def rkv_attention_workspace_size(q, num_kv_heads: int, max_rows: int) -> int:
 
 def alloc_attention_workspace(q, num_kv_heads: int, max_rows: int) -> torch.Tensor:
     """A zero-filled uint8 tensor of rkv_attention_workspace_size() bytes."""
-    return torch.zeros(rkv_attention_workspace_size(q, num_kv_heads, max_rows), dtype=torch.uint8,
+    return torch.zeros(rkv_attention_workspace_size(q, num_kv_heads, max_rows), dtype=_U8,
                        device=q.device)
 
 
-def _attention(call, where, cache_args, ref, shape, q, block_table, lens, max_rows, scale, out, lse,
-               workspace, s):
+def _attention(call, where, cache_args, dev, shape, q, block_table, lens, max_rows, scale, out,
+               lse, workspace):
     nb, H, bs, d = shape
-    _same_device(ref, q=q, block_table=block_table, lens=lens, out=out,
-                 lse=lse if isinstance(lse, torch.Tensor) else None, workspace=workspace)
-    S, T, hq, dq = _attention_shape(q, H)
-    if block_table.dim() != 2 or block_table.shape[0] != S:
+    sh = q.shape
+    if len(sh) != 4:
+        raise ValueError("q must be [num_seqs, n_new, H * gqa_group, d]")
+    S, T, hq, _ = sh
+    G = hq // H if H else 0
+    if G == 0 or G * H != hq:
+        raise ValueError("the heads of q must be a multiple of the KV heads")
+    if block_table.dim() != 2:
         raise ValueError("block_table must be int32 [num_seqs, max_blocks_per_seq]")
     mb = block_table.shape[1]
-    _int32(block_table, "block_table", (S, mb))
-    _int32(lens, "lens", (S,))
-    dt = _dtype(q)
-    if max_rows is None:
-        max_rows = mb * bs
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+    dt = q.dtype
+    max_rows = mb * bs if max_rows is None else int(max_rows)
     if out is None:
-        out = torch.empty((S, T, hq, d), dtype=q.dtype, device=q.device)
+        out = torch.empty(sh, dtype=dt, device=q.device)
+    at = None
     if lse is True:
-        lse = torch.empty((S, T, hq), dtype=torch.float32, device=q.device)
+        lse = torch.empty((S, T, hq), dtype=_F32, device=q.device)
     elif lse is False:
         lse = None
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (S, T, hq)
-                            or not lse.is_contiguous()):
-        raise ValueError("lse must be contiguous fp32 [num_seqs, n_new, heads]")
-    rq = _rows(q, "q", hq, d, q.dtype, S * T, T)
-    ro = _rows(out, "out", hq, d, q.dtype, S * T, T)
-    desc = _PagedDesc(S, H, hq // H, d, bs, nb, mb, dt)
+    if lse is not None:
+        if lse.dtype != _F32 or lse.shape != (S, T, hq) or not lse.is_contiguous() \
+                or lse.get_device() != dev:
+            raise ValueError("lse must be contiguous fp32 [num_seqs, n_new, heads] on the device of "
+                             "the other tensors")
+        at = lse.data_ptr()
+    desc = _pack_desc(S, H, G, d, bs, nb, mb, _dtype(q))
     if workspace is None:
-        n = load().rkv_attention_workspace_size(desc, T, int(max_rows))
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
-    wp, wn = _workspace(workspace)
-    rc = call(desc, T, rq, *cache_args, block_table.data_ptr(), lens.data_ptr(), int(max_rows),
-              float(scale), ro, None if lse is None else lse.data_ptr(), wp, wn, s)
-    _check(rc, where)
+        n = load().rkv_attention_workspace_size(desc, T, max_rows)
+        workspace = torch.empty(max(n, 256), dtype=_U8, device=q.device)
+    wp, wn = _workspace(workspace, dev)
+    tokens = S * T
+    rc = call(desc, T, _rows(q, "q", dev, hq, d, dt, tokens, T), *cache_args,
+              _ints(block_table, "block_table", dev, S, mb), _ints(lens, "lens", dev, S), max_rows,
+              1.0 / math.sqrt(d) if scale is None else scale,
+              _rows(out, "out", dev, hq, d, dt, tokens, T), at, wp, wn, _raw_stream(dev))
+    if rc:
+        _check(rc, where)
     return out if lse is None else (out, lse)
 
 
@@ -420,19 +432,25 @@ def rkv_paged_attention(q, K_pool, V_pool, block_table, lens, max_rows: int | No
     or (out, lse) when lse is True or an fp32 tensor [S, n_new, H * G].
     Without a workspace (rkv_attention_workspace_size) scratch is allocated
     and device errors are not reported."""
-    with _Call(K_pool, stream) as s:
-        shape = _pool_shape(K_pool, V_pool)
-        if q.dtype != K_pool.dtype:
-            raise ValueError("q and the pools must share a dtype")
-        return _attention(load().rkv_paged_attention, "rkv_paged_attention",
-                          (K_pool.data_ptr(), V_pool.data_ptr()), K_pool, shape, q, block_table,
-                          lens, max_rows, scale, out, lse, workspace, s)
+    if _away(K_pool, stream):
+        return _elsewhere(rkv_paged_attention, K_pool, stream, q, K_pool, V_pool, block_table,
+                          lens, max_rows, scale, out, lse, workspace)
+    dev = K_pool.get_device()
+    shape = _pools(K_pool, V_pool, dev)
+    if q.dtype != K_pool.dtype:
+        raise ValueError("q and the pools must share a dtype")
+    return _attention(load().rkv_paged_attention, "rkv_paged_attention",
+                      (K_pool.data_ptr(), V_pool.data_ptr()), dev, shape, q, block_table, lens,
+                      max_rows, scale, out, lse, workspace)
 
 
 def rkv_q4_attention(q, cache: Q4Cache, block_table, lens, max_rows: int | None = None,
                      scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
     """rkv_paged_attention over a 4-bit cache (q bf16)."""
-    with _Call(cache.K_codes, stream) as s:
-        return _attention(load().rkv_q4_attention, "rkv_q4_attention", (cache._c,), cache.K_codes,
-                          cache.shape, q, block_table, lens, max_rows, scale, out, lse, workspace,
-                          s)
+    at = cache.K_codes
+    if _away(at, stream):
+        return _elsewhere(rkv_q4_attention, at, stream, q, cache, block_table, lens, max_rows,
+                          scale, out, lse, workspace)
+    return _attention(load().rkv_q4_attention, "rkv_q4_attention", (cache._packed,),
+                      at.get_device(), cache.shape, q, block_table, lens, max_rows, scale, out,
+                      lse, workspace)

@@ -237,31 +237,30 @@ def load(path: str | None = None):
         lib.rkv_compress_noalloc.argtypes = [dp, vp, vp, vp, i32, i32, i32, f32, i32, f32, vp,
                                              vp, vp, vp]
         lib.rkv_compress_noalloc.restype = i32
-        rows, rope, q4 = (ctypes.POINTER(_Rows), ctypes.POINTER(_RopePlan),
-                          ctypes.POINTER(_Q4Cache))
-        lib.rkv_rope_init.argtypes = [ctypes.POINTER(_RopeConfig), rope]
+        # descriptors, plans and row views go as addresses (byref() or packed
+        # bytes): these calls run once per layer and token, and building ctypes
+        # structures would cost more than the kernels
+        lib.rkv_rope_init.argtypes = [ctypes.POINTER(_RopeConfig), ctypes.POINTER(_RopePlan)]
         lib.rkv_rope_init.restype = i32
         lib.rkv_rope_init_freqs.argtypes = [i32, i32, ctypes.POINTER(ctypes.c_double),
-                                            ctypes.c_double, rope]
+                                            ctypes.c_double, ctypes.POINTER(_RopePlan)]
         lib.rkv_rope_init_freqs.restype = i32
-        lib.rkv_rope_apply.argtypes = [rope, i32, i32, i64, i64, vp, i32, i32, rows, rows, i32,
-                                       rows, rows, vp]
+        lib.rkv_rope_apply.argtypes = [vp, i32, i32, i64, i64, vp, i32, i32, vp, vp, i32, vp, vp,
+                                       vp]
         lib.rkv_rope_apply.restype = i32
-        lib.rkv_paged_append.argtypes = [pdp, rope, vp, vp, vp, vp, i64, i32, vp, vp, rows, rows,
-                                         rows, rows, vp, vp]
+        lib.rkv_paged_append.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, vp, vp, vp, vp, vp, vp,
+                                         vp, vp]
         lib.rkv_paged_append.restype = i32
-        lib.rkv_q4_append.argtypes = [pdp, rope, q4, vp, vp, i64, i32, vp, vp, rows, rows, rows,
-                                      rows, vp, vp]
+        lib.rkv_q4_append.argtypes = [vp, vp, vp, vp, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp]
         lib.rkv_q4_append.restype = i32
-        lib.rkv_q4_read.argtypes = [pdp, q4, vp, vp, vp, i32, vp, vp, vp, vp]
+        lib.rkv_q4_read.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, vp]
         lib.rkv_q4_read.restype = i32
-        lib.rkv_attention_workspace_size.argtypes = [pdp, i32, i32]
+        lib.rkv_attention_workspace_size.argtypes = [vp, i32, i32]
         lib.rkv_attention_workspace_size.restype = sz
-        lib.rkv_paged_attention.argtypes = [pdp, i32, rows, vp, vp, vp, vp, i32, f32, rows, vp,
-                                            vp, sz, vp]
+        lib.rkv_paged_attention.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, f32, vp, vp, vp, sz,
+                                            vp]
         lib.rkv_paged_attention.restype = i32
-        lib.rkv_q4_attention.argtypes = [pdp, i32, rows, q4, vp, vp, i32, f32, rows, vp, vp, sz,
-                                         vp]
+        lib.rkv_q4_attention.argtypes = [vp, i32, vp, vp, vp, vp, i32, f32, vp, vp, vp, sz, vp]
         lib.rkv_q4_attention.restype = i32
         lib.rkv_kernel_name.argtypes = [i32]
         lib.rkv_kernel_name.restype = ctypes.c_char_p

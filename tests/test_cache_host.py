@@ -70,20 +70,20 @@ GB = 1 << 30
 
 def _rows(off=0, seq=1 << 13, tok=4096, head=128, ptr=None):
     from decode_kv_cache_02_gb300 import rkv
-    return rkv._Rows((BASE + off) if ptr is None else ptr, seq, tok, head)
+    return bytes(rkv._Rows((BASE + off) if ptr is None else ptr, seq, tok, head))
 
 
 def _pdesc(**kw):
     from decode_kv_cache_02_gb300 import rkv
-    return rkv._PagedDesc(kw.get("S", 4), kw.get("H", 8), kw.get("G", 4), kw.get("d", 128),
-                          kw.get("bs", 16), kw.get("nb", 400), kw.get("mb", 80),
-                          kw.get("dtype", 0))
+    return bytes(rkv._PagedDesc(kw.get("S", 4), kw.get("H", 8), kw.get("G", 4), kw.get("d", 128),
+                                kw.get("bs", 16), kw.get("nb", 400), kw.get("mb", 80),
+                                kw.get("dtype", 0)))
 
 
 def test_rope_apply_refusals(lib):
     """Every refused call is answered on the host (made-up addresses)."""
     from decode_kv_cache_02_gb300 import cache
-    plan = cache.RopePlan(128)._c
+    plan = cache.RopePlan(128)._packed
     some = object()
 
     def call(plan=plan, dtype=0, d=128, n=10, per=10, pos=BASE, hq=32, q=some, oq=some, hk=8,
@@ -115,7 +115,7 @@ def test_rope_apply_refusals(lib):
 def test_append_refusals(lib):
     from decode_kv_cache_02_gb300 import cache, rkv
     some = object()
-    q4 = rkv._Q4Cache(BASE + 10 * GB, BASE + 11 * GB, BASE + 12 * GB, BASE + 13 * GB)
+    q4 = bytes(rkv._Q4Cache(BASE + 10 * GB, BASE + 11 * GB, BASE + 12 * GB, BASE + 13 * GB))
 
     def call(fn="paged", desc=None, rope=None, K=BASE + 10 * GB, V=BASE + 12 * GB, table=BASE,
              lens=BASE, n=4, new=1, cu=None, pos=None, k=some, v=some, q=some, oq=some, ws=None,
@@ -141,21 +141,21 @@ def test_append_refusals(lib):
         assert call(fn, k=None) == 1 and call(fn, v=None) == 1
         assert call(fn, oq=None) == 1 and call(fn, q=None) == 1     # q and out_q go together
         assert call(fn, ws=BASE + 16) == 3
-        assert call(fn, rope=cache.RopePlan(128)._c, desc=_pdesc(d=64)) == 1
+        assert call(fn, rope=cache.RopePlan(128)._packed, desc=_pdesc(d=64)) == 1
         assert call(fn, oq=_rows(2 * GB + 256)) == 4                # out_q runs into q
         assert call(fn, k=_rows(10 * GB)) == 4                      # input inside the pool
         assert call(fn, oq=_rows(12 * GB)) == 4                     # output inside the pool
     assert call(K=None) == 1 and call(K=BASE + 8) == 1
     assert call(V=BASE + 10 * GB) == 4                              # K and V pools the same
     assert call("q4", c=None) == 1
-    assert call("q4", c=rkv._Q4Cache(BASE, 0, BASE, BASE)) == 1
-    assert call("q4", c=rkv._Q4Cache(BASE + 10 * GB, BASE + 11 * GB, BASE + 10 * GB,
-                                     BASE + 13 * GB)) == 4
+    assert call("q4", c=bytes(rkv._Q4Cache(BASE, 0, BASE, BASE))) == 1
+    assert call("q4", c=bytes(rkv._Q4Cache(BASE + 10 * GB, BASE + 11 * GB, BASE + 10 * GB,
+                                           BASE + 13 * GB))) == 4
 
 
 def test_q4_read_refusals(lib):
     from decode_kv_cache_02_gb300 import rkv
-    q4 = rkv._Q4Cache(BASE + 10 * GB, BASE + 11 * GB, BASE + 12 * GB, BASE + 13 * GB)
+    q4 = bytes(rkv._Q4Cache(BASE + 10 * GB, BASE + 11 * GB, BASE + 12 * GB, BASE + 13 * GB))
 
     def call(desc=None, c=q4, table=BASE, lens=BASE, n=5, K=BASE + GB, V=BASE + 2 * GB, ws=None):
         return lib.rkv_q4_read(_pdesc() if desc is None else desc, c, table, lens, None, n, K, V,
@@ -169,13 +169,13 @@ def test_q4_read_refusals(lib):
 
 def test_attention_sizes_and_refusals(lib):
     from decode_kv_cache_02_gb300 import rkv
-    size = lambda T, rows, **kw: lib.rkv_attention_workspace_size(ctypes.byref(_pdesc(**kw)), T, rows)  # noqa: E731
+    size = lambda T, rows, **kw: lib.rkv_attention_workspace_size(_pdesc(**kw), T, rows)  # noqa: E731
     assert size(1, 100) >= 256
     assert size(0, 100) == 0 and size(1, 0) == 0 and size(1, 80 * 16 + 1) == 0
     assert size(65, 100) == 0 and size(1, 100, d=80) == 0
     # a longer cache never needs less than its own chunks, and an empty batch needs the error word
     assert size(1, 1280, S=0) == 256
-    q4 = rkv._Q4Cache(BASE + 10 * GB, BASE + 11 * GB, BASE + 12 * GB, BASE + 13 * GB)
+    q4 = bytes(rkv._Q4Cache(BASE + 10 * GB, BASE + 11 * GB, BASE + 12 * GB, BASE + 13 * GB))
     some = object()
 
     def call(fn="paged", desc=None, T=1, q=some, K=BASE + 10 * GB, V=BASE + 12 * GB, c=q4,
