@@ -221,7 +221,10 @@ int attend(const rkv_paged_desc* desc, int n_new, const rkv_rows* q, const void*
     if (rc) return rc;
     if (!isfinite(scale)) return RKV_ERR_INVALID_ARG;
     const AttnPlan pl = rkv::attn_plan(a);
-    if (pl.ctas >= ((int64_t)1 << 31)) return RKV_ERR_INVALID_ARG;
+    // the kernel counts units and pool rows in 32 bits
+    if (a.num_seqs * a.pg.H * (int64_t)((max_rows - 1) / pl.unit + 1) >= ((int64_t)1 << 31) ||
+        pool_rows(desc) >= ((int64_t)1 << 32) - 1)
+        return RKV_ERR_UNSUPPORTED;
     if (!workspace || !aligned_ws(workspace) || workspace_bytes < attention_bytes(pl))
         return RKV_ERR_WORKSPACE;
     if (desc->num_seqs == 0) return RKV_OK;
@@ -253,7 +256,7 @@ int attend(const rkv_paged_desc* desc, int n_new, const rkv_rows* q, const void*
     a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = rkv::timed_cache(q4 ? rkv::kCacheAttnQ4 : rkv::kCacheAttn, s, run_attention, &a);
-    if (e == cudaSuccess && pl.splits > 1)
+    if (e == cudaSuccess && pl.join)
         e = rkv::timed_cache(rkv::kCacheAttnCombine, s, run_combine, &a);
     return rc_of(e);
 }
@@ -440,10 +443,16 @@ int rkv_q4_read(const rkv_paged_desc* desc, const rkv_q4_cache* cache,
 }
 
 size_t rkv_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int max_rows) {
-    // the 4-bit cache's plan is the bf16 pool's: one size serves both
+    // one size serves the pool and the 4-bit cache
     AttnArgs a;
     if (check_attention(desc, nullptr, n_new, max_rows, false, &a)) return 0;
-    return attention_bytes(rkv::attn_plan(a));
+    size_t n = attention_bytes(rkv::attn_plan(a));
+    if (desc->dtype == RKV_DTYPE_BF16) {
+        a.q4 = true;
+        const size_t m = attention_bytes(rkv::attn_plan(a));
+        if (m > n) n = m;
+    }
+    return n;
 }
 
 int rkv_paged_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,

@@ -267,11 +267,12 @@ struct AttnArgs {
     float* partial = nullptr;  // attn_plan().partial_floats of scratch
     DeviceStatus* status = nullptr;
 };
-// How a call is cut: row groups of `rows` queries per KV head, each
-// sequence's rows in chunks of `chunk`, at most `splits` of them.
+// How a call is cut: groups of `rows` queries per KV head; the units (`unit`
+// rows of one sequence and KV head) of the whole batch in `runs` equal runs;
+// join: pieces of a sequence may have to be joined by a second launch.
 struct AttnPlan {
-    int rows = 8, groups = 1, chunk = 0, splits = 1;
-    int64_t ctas = 0;
+    int rows = 8, groups = 1, unit = 64, runs = 0;
+    bool join = false;
     size_t partial_floats = 0;
 };
 AttnPlan attn_plan(const AttnArgs& a);
