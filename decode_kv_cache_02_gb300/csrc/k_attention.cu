@@ -31,7 +31,6 @@
 //
 // The running maximum moves only when a logit passes it by more than 8 (log2):
 // p stays below 2^8 and the rescaling almost never runs.
-#include <stdlib.h>
 #include "rkv_common.cuh"
 #include "rkv_internal.h"
 
@@ -74,6 +73,7 @@ struct Params {
     float* lse;
     float* partial;     // [slot][rows][D]
     float* partial_ml;  // [slot][rows][2]
+    int4* joins;        // [run][group]: (sequence, head, parts) of the problem to join, if parts
     int H, G, T, R, groups, runs, max_rows;
     int max_blocks, log2bs, num_blocks;
     float scale, slack;  // of base-2 logits, positive; how far they may pass the maximum
@@ -484,14 +484,36 @@ RKV_DEV uint32_t run_of(const Place& pl, uint32_t u) {
     const uint32_t big = more * (per + 1);
     return u < big ? u / (per + 1) : more + (u - big) / per;
 }
+// Cuts the line and finds sequence pl.s with first unit *first*, given a
+// thread's stretch [a, b) of sequences, `sum` units of it and `upto` units up to
+// its end: true in the thread that owns the run's first unit.
+RKV_DEV bool own_stretch(const Params& p, int unit, uint32_t run, uint32_t all, int a, uint32_t sum,
+                         uint32_t upto, Place& pl, uint32_t& first) {
+    pl.n = all * p.H;
+    pl.runs = min((uint32_t)p.runs, pl.n);
+    pl.u0 = pl.u1 = 0;
+    if (run < pl.runs) {
+        pl.u0 = first_of(pl, run);
+        pl.u1 = first_of(pl, run + 1);
+    }
+    first = (upto - sum) * p.H;
+    if (first > pl.u0 || pl.u0 >= upto * p.H) return false;
+    for (pl.s = a;; ++pl.s) {
+        const uint32_t w = units_of(rows_of(p, pl.s), unit) * p.H;
+        if (pl.u0 < first + w) return true;
+        first += w;
+    }
+}
 template <int THREADS>
 RKV_DEV Place find_place(const Params& p, int unit, uint32_t run) {
     __shared__ uint32_t found[2], warp_sum[THREADS / 32];
-    Place pl;
-    // each thread owns a stretch of sequences
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.num_seqs + THREADS - 1) / THREADS;
-    const int a = min(tid * per, p.num_seqs), b = min(a + per, p.num_seqs);
+    // each lane of every warp owns a stretch of sequences (no barrier), with
+    // many sequences each thread of the block
+    const bool small = p.num_seqs <= 256;
+    const int n = small ? 32 : THREADS, me = small ? lane : tid;
+    const int per = (p.num_seqs + n - 1) / n;
+    const int a = min(me * per, p.num_seqs), b = min(a + per, p.num_seqs);
     uint32_t sum = 0;
     for (int s = a; s < b; ++s) sum += units_of(rows_of(p, s), unit);
     uint32_t upto = sum;
@@ -500,45 +522,41 @@ RKV_DEV Place find_place(const Params& p, int unit, uint32_t run) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += y;
     }
-    if (lane == 31) warp_sum[warp] = upto;
-    __syncthreads();
-    uint32_t all = 0;
+    Place pl;
+    uint32_t first = 0;
+    if (small) {
+        const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+        const bool mine = own_stretch(p, unit, run, all, a, sum, upto, pl, first);
+        const int owner = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+        pl.s = __shfl_sync(0xffffffffu, pl.s, owner);
+        first = __shfl_sync(0xffffffffu, first, owner);
+    } else {
+        if (lane == 31) warp_sum[warp] = upto;
+        __syncthreads();
+        uint32_t all = 0;
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) upto += warp_sum[w];
-        all += warp_sum[w];
-    }
-    pl.n = all * p.H;
-    pl.runs = min((uint32_t)p.runs, pl.n);
-    pl.u0 = pl.u1 = 0;
-    if (run < pl.runs) {
-        pl.u0 = first_of(pl, run);
-        pl.u1 = first_of(pl, run + 1);
-    }
-    uint32_t first = (upto - sum) * p.H;  // of this thread's stretch
-    if (first <= pl.u0 && pl.u0 < upto * p.H) {
-        int s = a;
-        for (;; ++s) {
-            const uint32_t w = units_of(rows_of(p, s), unit) * p.H;
-            if (pl.u0 < first + w) break;
-            first += w;
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) upto += warp_sum[w];
+            all += warp_sum[w];
         }
-        found[0] = s;
-        found[1] = first;
+        if (own_stretch(p, unit, run, all, a, sum, upto, pl, first)) {
+            found[0] = pl.s;
+            found[1] = first;
+        }
+        __syncthreads();
+        pl.s = found[0];
+        first = found[1];
     }
-    __syncthreads();
-    pl.s = found[0];
     const uint32_t n_s = units_of(rows_of(p, pl.s), unit);
-    const uint32_t h = (pl.u0 - found[1]) / n_s;
-    pl.h = h;
-    pl.start = found[1] + h * n_s;
+    pl.h = (pl.u0 - first) / n_s;
+    pl.start = first + pl.h * n_s;
     return pl;
 }
 
 // A piece of a problem that a block works on.
 struct Piece {
     int s, h, len, c0, c1;
-    uint32_t slot;
+    uint32_t slot, parts;  // parts: blocks that share the problem, where it begins here
     bool whole;
 };
 // The next piece of the run (false: none left), which then starts behind it.
@@ -555,6 +573,7 @@ RKV_DEV bool next_piece(const Params& p, int unit, uint32_t run, Place& pl, Piec
     c.whole = take == n_s;
     // a piece that an earlier block began, or one that a later block ends
     c.slot = 2 * run + (j > 0 ? 0 : 1);
+    c.parts = j > 0 || c.whole ? 0 : run_of(pl, pl.start + n_s - 1) - run + 1;
     if (threadIdx.x == 0 && j == 0 && pl.h == 0 && c.len != p.lens[pl.s])
         set_error(p.status, kDevErrIndex, (unsigned)pl.s);
     pl.u0 += take;
@@ -647,7 +666,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
     if constexpr (Q4) uk = unpack_constants();
 
     Place place = find_place<kWarps * 32>(p, UNIT, run);
-    Piece c;
+    Piece c{};
     while (next_piece(p, UNIT, run, place, c)) {
         const int s = c.s, h = c.h, len = c.len, c0 = c.c0, c1 = c.c1;
 
@@ -946,6 +965,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                                        (int64_t)c.slot * p.groups + group, c.whole);
         __syncthreads();  // the next piece's copies overwrite what was just read
     }
+    if (p.joins && tid == 0) p.joins[blockIdx.x] = make_int4(c.s, c.h, c.parts, 0);
 }
 
 // ------------------------------------------------------------ fp32 pools --
@@ -973,7 +993,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
     uint8_t* ring = smem + warp * (S::DEPTH * S::BYTES);
 
     Place place = find_place<kWarps * 32>(p, UNIT, run);
-    Piece c;
+    Piece c{};
     while (next_piece(p, UNIT, run, place, c)) {
         for (int e = tid; e < ROWS * UPR; e += kWarps * 32) {
             const int r = row_first + e / UPR, u = e % UPR;
@@ -1128,77 +1148,64 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
                                c.whole);
         __syncthreads();
     }
+    if (p.joins && tid == 0) p.joins[blockIdx.x] = make_int4(c.s, c.h, c.parts, 0);
 }
 
 // ------------------------------------------------------------------ join --
 
-// Joins the pieces of the problem that begins in a block's run and ends in a
-// later one.  Four warps share a query: each takes every fourth piece.
-constexpr int kJoinThreads = 512;
+// Joins the pieces of the problem that begins in a run and ends in a later one:
+// a block per (run, group) and query (every gridDim.y-th), eight warps that
+// take every eighth piece each.
+constexpr int kJoinWarps = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(
-    const __grid_constant__ Params p, int rows, int unit) {
-    constexpr int LANES = D / 4, QUERIES = kJoinThreads / 128;
-    __shared__ float4 sh_v[kJoinThreads / 32][32];
-    __shared__ float sh_sum[kJoinThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
+    const __grid_constant__ Params p, int rows) {
+    constexpr int LANES = D / 4;
+    __shared__ float4 sh_v[kJoinWarps][32];
+    __shared__ float sh_m[kJoinWarps], sh_l[kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = blockIdx.x % p.groups;
-    const uint32_t run = blockIdx.x / p.groups;
+    const int run = blockIdx.x / p.groups;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
-    Place place = find_place<kJoinThreads>(p, unit, run);
-    if (place.u0 == place.u1) return;
-    // the problem of the run's last unit
-    const uint32_t u1 = place.u1;
-    int s = place.s, h = place.h;
-    uint32_t start = place.start, n_s = units_of(rows_of(p, s), unit);
-    while (start + n_s < u1) {
-        // whole heads of the sequence that end within the run, then the next one
-        const uint32_t skip = min((u1 - 1 - start) / n_s, (uint32_t)(p.H - h));
-        start += skip * n_s;
-        h += skip;
-        if (h == p.H) {
-            h = 0;
-            ++s;
-            n_s = units_of(rows_of(p, s), unit);
-        }
-    }
-    if (start < place.u0 || start + n_s <= u1) return;  // begun earlier, or whole
-    const uint32_t parts = run_of(place, start + n_s - 1) - run + 1;
-    auto slot = [&](uint32_t i) {
-        return ((int64_t)(2 * (run + i) + (i == 0 ? 1 : 0)) * p.groups + group) * rows;
-    };
-    for (int r0 = 0; r0 < rows && group * rows + r0 < p.R; r0 += QUERIES) {
-        const int r = r0 + warp / 4, row = group * rows + r;
-        const bool on = r < rows && row < p.R;
-        float mx = -INFINITY, sum = 0.f;
+    const int4 job = p.joins[blockIdx.x];
+    const int s = job.x, h = job.y, parts = job.z;
+    if (parts == 0) return;
+    for (int r = blockIdx.y; r < rows && group * rows + r < p.R; r += gridDim.y) {
+        const int row = group * rows + r;
+        float m = -INFINITY, l = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on) {
-            for (uint32_t i = lane; i < parts; i += 32) mx = fmaxf(mx, p.partial_ml[(slot(i) + r) * 2]);
-            mx = warp_max(mx);
 #pragma unroll 4
-            for (uint32_t i = warp & 3; i < parts; i += 4) {
-                const int64_t at = slot(i) + r;
-                const float2 ml = *reinterpret_cast<const float2*>(p.partial_ml + at * 2);
-                const float f = weight(ml.x, ml.y, mx, p.scale);
-                sum += ml.y * f;
-                if (lane < LANES) {
-                    const float4 x = *reinterpret_cast<const float4*>(p.partial + at * D + lane * 4);
-                    if (f != 0.f) {
-                        v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
-                    }
-                }
-            }
+        for (int i = warp; i < parts; i += kJoinWarps) {
+            const int64_t at =
+                ((int64_t)(2 * (run + i) + (i == 0 ? 1 : 0)) * p.groups + group) * rows + r;
+            const float2 ml = *reinterpret_cast<const float2*>(p.partial_ml + at * 2);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (lane < LANES) x = *reinterpret_cast<const float4*>(p.partial + at * D + lane * 4);
+            const float mx = fmaxf(m, ml.x);
+            const float f = weight(m, l, mx, p.scale), g = weight(ml.x, ml.y, mx, p.scale);
+            m = mx;
+            l = l * f + ml.y * g;
+            v = make_float4(v.x * f + x.x * g, v.y * f + x.y * g, v.z * f + x.z * g,
+                            v.w * f + x.w * g);
         }
         __syncthreads();
         sh_v[warp][lane] = v;
-        if (lane == 0) sh_sum[warp] = sum;
+        if (lane == 0) {
+            sh_m[warp] = m;
+            sh_l[warp] = l;
+        }
         __syncthreads();
-        if (!on || (warp & 3) != 0) continue;
+        if (warp != 0) continue;
+        float mx = sh_m[0], sum = 0.f;
 #pragma unroll
-        for (int w = 1; w < 4; ++w) {
-            const float4 x = sh_v[warp + w][lane];
-            v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
-            sum += sh_sum[warp + w];
+        for (int w = 1; w < kJoinWarps; ++w) mx = fmaxf(mx, sh_m[w]);
+        v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float f = weight(sh_m[w], sh_l[w], mx, p.scale);
+            const float4 x = sh_v[w][lane];
+            v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
+            sum += sh_l[w] * f;
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int tk = row / p.G, hd = h * p.G + row - tk * p.G;
@@ -1226,7 +1233,9 @@ Params params(const AttnArgs& a, const AttnPlan& pl) {
     p.o_seq = a.out.seq; p.o_tok = a.out.tok; p.o_head = a.out.head;
     p.lse = a.lse;
     p.partial = a.partial;
-    p.partial_ml = a.partial + 2 * (int64_t)pl.runs * pl.groups * pl.rows * a.d;
+    const int64_t slots = 2 * (int64_t)pl.runs * pl.groups;
+    p.partial_ml = a.partial + slots * pl.rows * a.d;
+    p.joins = pl.join ? reinterpret_cast<int4*>(p.partial_ml + slots * pl.rows * 2) : nullptr;
     p.H = a.pg.H; p.G = a.G; p.T = a.n_new; p.R = a.n_new * a.G;
     p.groups = pl.groups; p.runs = pl.runs; p.max_rows = a.max_rows;
     p.max_blocks = a.pg.max_blocks; p.log2bs = a.pg.log2bs; p.num_blocks = a.pg.num_blocks;
@@ -1287,11 +1296,13 @@ AttnPlan attn_plan(const AttnArgs& a) {
     // fp32 rows of 128), with 4-bit rows registers for three
     const int blocks = 152 * (is_f32(a) && a.d == 128 ? 1 : (a.q4 && pl.rows == 8 ? 3 : 2));
     const int64_t units = a.num_seqs * a.pg.H * (((int64_t)a.max_rows + pl.unit - 1) / pl.unit);
-    int64_t runs = ((int64_t)blocks * (getenv("RKV_MULT") ? atoi(getenv("RKV_MULT")) : 1) + pl.groups - 1) / pl.groups;
+    int64_t runs = (blocks + pl.groups - 1) / pl.groups;
     if (runs > units) runs = units;
     pl.runs = (int)runs;
     pl.join = a.max_rows > pl.unit;
-    pl.partial_floats = pl.join ? (size_t)2 * pl.runs * pl.groups * pl.rows * (a.d + 2) : 0;
+    // two pieces of a run, and what it leaves to join (4 words)
+    pl.partial_floats =
+        pl.join ? (size_t)pl.runs * pl.groups * (2 * pl.rows * (a.d + 2) + 4) : 0;
     return pl;
 }
 
@@ -1310,12 +1321,15 @@ cudaError_t go_join(const Params& p, const AttnPlan& pl, cudaStream_t s) {
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(pl.runs * pl.groups));
-    cfg.blockDim = dim3(kJoinThreads);
+    // most blocks find nothing to join: a few for each run
+    const int blocks = pl.runs * pl.groups, used = p.R < pl.rows ? p.R : pl.rows;
+    const int y = 2048 / blocks < 1 ? 1 : 2048 / blocks;
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)(used < y ? used : y));
+    cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, D>, p, pl.rows, pl.unit);
+    return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, D>, p, pl.rows);
 }
 
 cudaError_t launch_attention_combine(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
