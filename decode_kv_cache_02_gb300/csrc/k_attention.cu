@@ -365,6 +365,22 @@ RKV_DEV void values_bf16(uint32_t st, int base, const uint32_t (&pb)[NT][2], uin
     }
 }
 
+// Whether row r of a stage holds an infinity or a NaN in V (4 bits: in its
+// scales).
+template <int D, bool Q4>
+RKV_DEV bool unfinite(uint32_t st, int r) {
+    using S = Stage<D, Q4>;
+    const uint32_t row = Q4 ? st + S::vs() + r * S::SROW : st + S::V + r * S::ROW;
+    bool bad = false;
+#pragma unroll 4
+    for (int i = 0; i < (Q4 ? S::SROW : S::ROW) / 8; ++i) {
+        const uint2 x = lds8(row + 8 * i);
+        bad |= (x.x & 0x7f80u) == 0x7f80u || (x.x & 0x7f800000u) == 0x7f800000u;
+        bad |= (x.y & 0x7f80u) == 0x7f80u || (x.y & 0x7f800000u) == 0x7f800000u;
+    }
+    return bad;
+}
+
 // The same for a 4-bit stage; p: probabilities of 16 keys as accumulators lie,
 // pb: as operand.  low: row w (W + w) of the accumulators collects sum of p *
 // low (scale) of group w.  MASKED: a hidden row's NaN stays out (some of the
@@ -855,10 +871,15 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                         x[kt][n][i + 2] = ex2(fmaf(x[kt][n][i + 2], p.scale, -ref[n][i]));
                         l[n][i] += x[kt][n][i] + x[kt][n][i + 2];
                     }
-            // rows that only some of the tokens see: what a hidden row holds (an infinity, a
-            // NaN) must not reach the others (rows nobody sees are zeros here: rows past len
-            // and rows without a block)
-            const bool apart = masked && p.T > 1;
+            // rows that only some of the tokens see: an infinity or a NaN there must not reach
+            // the others as 0 * inf, so such a stage is taken one token at a time (rows nobody
+            // sees are zeros here: rows past len and rows without a block)
+            bool apart = false;
+            if (masked && p.T > 1) {
+                const int r = row0 + lane;
+                const bool part = lane < S::KEYS && r < c1 && r > all_see;
+                apart = __any_sync(0xffffffffu, part && unfinite<D, Q4>(st, lane));
+            }
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
                 uint32_t pb[NT][2];
@@ -1153,9 +1174,9 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
 
 // ------------------------------------------------------------------ join --
 
-// Joins the pieces of the problem that begins in a run and ends in a later one:
-// a block per (run, group) and query (every gridDim.y-th), eight warps that
-// take every eighth piece each.
+// Joins the pieces of the problem that begins in a run and ends in a later one.
+// A warp takes a query; where the pieces are many (few long sequences), the
+// block's eight warps share a query's pieces.
 constexpr int kJoinWarps = 8;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
@@ -1170,12 +1191,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
     const int4 job = p.joins[blockIdx.x];
     const int s = job.x, h = job.y, parts = job.z;
     if (parts == 0) return;
-    for (int r = blockIdx.y; r < rows && group * rows + r < p.R; r += gridDim.y) {
-        const int row = group * rows + r;
-        float m = -INFINITY, l = 0.f;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int used = min(rows, p.R - group * rows);
+    // the sum over pieces first, first + step, ...
+    auto gather = [&](int r, int first, int step, float& m, float& l, float4& v) {
+        m = -INFINITY;
+        l = 0.f;
+        v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int i = warp; i < parts; i += kJoinWarps) {
+        for (int i = first; i < parts; i += step) {
             const int64_t at =
                 ((int64_t)(2 * (run + i) + (i == 0 ? 1 : 0)) * p.groups + group) * rows + r;
             const float2 ml = *reinterpret_cast<const float2*>(p.partial_ml + at * 2);
@@ -1188,6 +1211,29 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
             v = make_float4(v.x * f + x.x * g, v.y * f + x.y * g, v.z * f + x.z * g,
                             v.w * f + x.w * g);
         }
+    };
+    auto write = [&](int r, float m, float l, float4 v) {
+        const int row = group * rows + r;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int tk = row / p.G, hd = h * p.G + row - tk * p.G;
+        if (lane < LANES)
+            store4(reinterpret_cast<T*>(p.out) + s * p.o_seq + tk * p.o_tok + hd * p.o_head + lane * 4,
+                   make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+        if (lane == 0 && p.lse)
+            p.lse[((int64_t)s * p.T + tk) * p.H * p.G + hd] =
+                l == 0.f ? -INFINITY : (m * p.scale + log2f(l)) * kLn2;
+    };
+    float m, l;
+    float4 v;
+    if (parts <= 8) {
+        for (int r = blockIdx.y * kJoinWarps + warp; r < used; r += gridDim.y * kJoinWarps) {
+            gather(r, 0, 1, m, l, v);
+            write(r, m, l, v);
+        }
+        return;
+    }
+    for (int r = blockIdx.y; r < used; r += gridDim.y) {
+        gather(r, warp, kJoinWarps, m, l, v);
         __syncthreads();
         sh_v[warp][lane] = v;
         if (lane == 0) {
@@ -1196,25 +1242,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
         }
         __syncthreads();
         if (warp != 0) continue;
-        float mx = sh_m[0], sum = 0.f;
+        m = sh_m[0];
 #pragma unroll
-        for (int w = 1; w < kJoinWarps; ++w) mx = fmaxf(mx, sh_m[w]);
+        for (int w = 1; w < kJoinWarps; ++w) m = fmaxf(m, sh_m[w]);
+        l = 0.f;
         v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kJoinWarps; ++w) {
-            const float f = weight(sh_m[w], sh_l[w], mx, p.scale);
+            const float f = weight(sh_m[w], sh_l[w], m, p.scale);
             const float4 x = sh_v[w][lane];
             v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
-            sum += sh_l[w] * f;
+            l += sh_l[w] * f;
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int tk = row / p.G, hd = h * p.G + row - tk * p.G;
-        if (lane < LANES)
-            store4(reinterpret_cast<T*>(p.out) + s * p.o_seq + tk * p.o_tok + hd * p.o_head + lane * 4,
-                   make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-        if (lane == 0 && p.lse)
-            p.lse[((int64_t)s * p.T + tk) * p.H * p.G + hd] =
-                sum == 0.f ? -INFINITY : (mx * p.scale + log2f(sum)) * kLn2;
+        write(r, m, l, v);
     }
 }
 
@@ -1323,8 +1363,9 @@ cudaError_t go_join(const Params& p, const AttnPlan& pl, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
     // most blocks find nothing to join: a few for each run
     const int blocks = pl.runs * pl.groups, used = p.R < pl.rows ? p.R : pl.rows;
-    const int y = 2048 / blocks < 1 ? 1 : 2048 / blocks;
-    cfg.gridDim = dim3((unsigned)blocks, (unsigned)(used < y ? used : y));
+    const int most = 2048 / blocks, least = (used + kJoinWarps - 1) / kJoinWarps;
+    const int y = most < least ? least : (most < used ? most : used);
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)y);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
     cfg.attrs = &at;
