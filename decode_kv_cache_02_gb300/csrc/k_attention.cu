@@ -75,6 +75,7 @@ struct Params {
     float* partial_ml;  // [slot][rows][2]
     int4* joins;        // [run][group]: (sequence, head, parts) of the problem to join, if parts
     int H, G, T, R, groups, runs, max_rows;
+    uint32_t lead;
     int max_blocks, log2bs, num_blocks;
     float scale, slack;  // of base-2 logits, positive; how far they may pass the maximum
     uint32_t flip;       // scale < 0: sign bits for the queries
@@ -477,7 +478,9 @@ RKV_DEV int rows_of(const Params& p, int s) {
     return n < 0 ? 0 : (n > p.max_rows ? p.max_rows : n);
 }
 // Units of a sequence's problem; an empty one has a unit too (its zeros are
-// written by it).
+// written by it).  On the line a problem is p.lead places longer: what a block
+// spends on beginning and ending one, so that runs over many short sequences
+// are not the last to finish.
 RKV_DEV uint32_t units_of(int rows, int unit) {
     return rows <= unit ? 1u : (uint32_t)(rows - 1) / (uint32_t)unit + 1u;
 }
@@ -515,7 +518,7 @@ RKV_DEV bool own_stretch(const Params& p, int unit, uint32_t run, uint32_t all, 
     first = (upto - sum) * p.H;
     if (first > pl.u0 || pl.u0 >= upto * p.H) return false;
     for (pl.s = a;; ++pl.s) {
-        const uint32_t w = units_of(rows_of(p, pl.s), unit) * p.H;
+        const uint32_t w = (units_of(rows_of(p, pl.s), unit) + p.lead) * p.H;
         if (pl.u0 < first + w) return true;
         first += w;
     }
@@ -531,7 +534,7 @@ RKV_DEV Place find_place(const Params& p, int unit, uint32_t run) {
     const int per = (p.num_seqs + n - 1) / n;
     const int a = min(me * per, p.num_seqs), b = min(a + per, p.num_seqs);
     uint32_t sum = 0;
-    for (int s = a; s < b; ++s) sum += units_of(rows_of(p, s), unit);
+    for (int s = a; s < b; ++s) sum += units_of(rows_of(p, s), unit) + p.lead;
     uint32_t upto = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -563,7 +566,7 @@ RKV_DEV Place find_place(const Params& p, int unit, uint32_t run) {
         pl.s = found[0];
         first = found[1];
     }
-    const uint32_t n_s = units_of(rows_of(p, pl.s), unit);
+    const uint32_t n_s = units_of(rows_of(p, pl.s), unit) + p.lead;
     pl.h = (pl.u0 - first) / n_s;
     pl.start = first + pl.h * n_s;
     return pl;
@@ -578,29 +581,34 @@ struct Piece {
 // The next piece of the run (false: none left), which then starts behind it.
 // A sequence's bad length is recorded by the block of its first unit.
 RKV_DEV bool next_piece(const Params& p, int unit, uint32_t run, Place& pl, Piece& c) {
-    if (pl.u0 >= pl.u1) return false;
-    c.s = pl.s;
-    c.h = pl.h;
-    c.len = rows_of(p, pl.s);
-    const uint32_t n_s = units_of(c.len, unit), j = pl.u0 - pl.start;
-    const uint32_t take = min(n_s - j, pl.u1 - pl.u0);
-    c.c0 = j * unit;
-    c.c1 = j + take == n_s ? c.len : (j + take) * unit;
-    c.whole = take == n_s;
-    // a piece that an earlier block began, or one that a later block ends
-    c.slot = 2 * run + (j > 0 ? 0 : 1);
-    c.parts = j > 0 || c.whole ? 0 : run_of(pl, pl.start + n_s - 1) - run + 1;
-    if (threadIdx.x == 0 && j == 0 && pl.h == 0 && c.len != p.lens[pl.s])
-        set_error(p.status, kDevErrIndex, (unsigned)pl.s);
-    pl.u0 += take;
-    if (j + take == n_s) {
-        pl.start += n_s;
-        if (++pl.h == p.H) {
-            pl.h = 0;
-            ++pl.s;
+    while (pl.u0 < pl.u1) {
+        c.s = pl.s;
+        c.h = pl.h;
+        c.len = rows_of(p, pl.s);
+        const uint32_t n_s = units_of(c.len, unit), n_l = n_s + p.lead;
+        const uint32_t from = pl.u0 - pl.start, to = min(n_l, pl.u1 - pl.start);
+        const uint32_t j = from > p.lead ? from - p.lead : 0, e = to > p.lead ? to - p.lead : 0;
+        c.c0 = j * unit;
+        c.c1 = e == n_s ? c.len : e * unit;
+        c.whole = j == 0 && e == n_s;
+        // a piece that an earlier block began, or one that a later block ends
+        c.slot = 2 * run + (j > 0 ? 0 : 1);
+        c.parts = j > 0 || c.whole || e == 0 ? 0 : run_of(pl, pl.start + n_l - 1) - run + 1;
+        pl.u0 = pl.start + to;
+        if (to == n_l) {
+            pl.start += n_l;
+            if (++pl.h == p.H) {
+                pl.h = 0;
+                ++pl.s;
+            }
+        }
+        if (e > j) {
+            if (threadIdx.x == 0 && j == 0 && c.h == 0 && c.len != p.lens[c.s])
+                set_error(p.status, kDevErrIndex, (unsigned)c.s);
+            return true;
         }
     }
-    return true;
+    return false;
 }
 
 // What a part with maximum m and sum l counts beside a common maximum mx: an
@@ -1278,6 +1286,7 @@ Params params(const AttnArgs& a, const AttnPlan& pl) {
     p.joins = pl.join ? reinterpret_cast<int4*>(p.partial_ml + slots * pl.rows * 2) : nullptr;
     p.H = a.pg.H; p.G = a.G; p.T = a.n_new; p.R = a.n_new * a.G;
     p.groups = pl.groups; p.runs = pl.runs; p.max_rows = a.max_rows;
+    p.lead = pl.lead;
     p.max_blocks = a.pg.max_blocks; p.log2bs = a.pg.log2bs; p.num_blocks = a.pg.num_blocks;
     // a scale of (almost) nothing counts as one that still orders the logits
     const float x = a.scale * kLog2e, y = x < 0.f ? -x : x;
@@ -1336,6 +1345,11 @@ AttnPlan attn_plan(const AttnArgs& a) {
     // fp32 rows of 128), with 4-bit rows registers for three
     const int blocks = 152 * (is_f32(a) && a.d == 128 ? 1 : (a.q4 && pl.rows == 8 ? 3 : 2));
     const int64_t units = a.num_seqs * a.pg.H * (((int64_t)a.max_rows + pl.unit - 1) / pl.unit);
+    // a problem's beginning and end cost about as much as this many units (64
+    // ragged sequences of 131 .. 4224 rows, us at 0, 1, 2, 4, 8: bf16 103, 102,
+    // 95, 95, 96; 4 bits 64, 60, 56, 58, 62; 8 new tokens, head_dim 64: 72, 70,
+    // 66, 61, 61)
+    pl.lead = a.q4 ? 2 : 4;
     int64_t runs = (blocks + pl.groups - 1) / pl.groups;
     if (runs > units) runs = units;
     pl.runs = (int)runs;

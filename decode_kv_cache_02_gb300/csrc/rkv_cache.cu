@@ -222,7 +222,8 @@ int attend(const rkv_paged_desc* desc, int n_new, const rkv_rows* q, const void*
     if (!isfinite(scale)) return RKV_ERR_INVALID_ARG;
     const AttnPlan pl = rkv::attn_plan(a);
     // the kernel counts units and pool rows in 32 bits
-    if (a.num_seqs * a.pg.H * (int64_t)((max_rows - 1) / pl.unit + 1) >= ((int64_t)1 << 31) ||
+    if (a.num_seqs * a.pg.H * ((int64_t)(max_rows - 1) / pl.unit + 1 + pl.lead) >=
+            ((int64_t)1 << 31) ||
         pool_rows(desc) >= ((int64_t)1 << 32) - 1)
         return RKV_ERR_UNSUPPORTED;
     if (!workspace || !aligned_ws(workspace) || workspace_bytes < attention_bytes(pl))

@@ -271,7 +271,7 @@ struct AttnArgs {
 // rows of one sequence and KV head) of the whole batch in `runs` equal runs;
 // join: pieces of a sequence may have to be joined by a second launch.
 struct AttnPlan {
-    int rows = 8, groups = 1, unit = 64, runs = 0;
+    int rows = 8, groups = 1, unit = 64, runs = 0, lead = 0;
     bool join = false;
     size_t partial_floats = 0;
 };
