@@ -1,15 +1,18 @@
 // k_tokens.cu -- new tokens on their way to the cache: rotary positions, the
-// append to a paged pool, and the append to a 4-bit pool, in one kernel.
+// append to a paged pool, and the append to a 4-bit pool, in one kernel; and
+// reading 4-bit rows back.
 //
 // Rotation: pair i of a head is turned by pos * f_i.  The plan holds f_i /
 // (2 pi) as a 64-bit fixed-point part of a turn, so the low 64 bits of
 // pos * turns[i] are the angle modulo one turn, exactly; the upper 32 of them,
-// read as a signed number, go through sincospif.  A block computes the sines
-// of its tokens once into shared memory and all heads of the token use them.
+// read as a signed number, go through sincospif.
 //
-// Every value is read and written once, 16 bytes (eight bf16) a step: the
-// rotation and the append are bound by HBM for many tokens and by launch and
-// load latency for a decode step.
+// Every value is read and written once, 16 bytes (eight bf16) a step, so many
+// tokens are bound by HBM and a decode step by launch and load latency.  A
+// thread takes the same pairs of several heads of one token: it issues all of
+// its loads first, then finds the position (and, with an append, the row: a
+// warp searches the ragged sequences 32 ways) and computes eight sines once for
+// its heads; nothing waits on a table of sines.
 //
 // 4 bits: four neighbouring lanes own one row; lane t holds values 32 w + 8 t
 // .. + 7 of every group w, so a group's minimum and maximum take two shuffles
@@ -26,7 +29,6 @@ namespace rkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 32;  // tokens per block
 
 struct Div {  // n / d for 0 <= n < 2^31
     uint32_t d, mul, shift;
@@ -43,99 +45,73 @@ RKV_DEV uint32_t div_by(uint32_t n, const Div& v) {
 
 struct Params {
     TokenArgs a;
-    int half;             // rot / 2
-    int tpb;              // tokens per block
-    int items_q, items_k; // items per token: the heads of q; of k (and v)
-    int items;
-    Div div_items, div_iph, div_ipv, div_units;
-    int iph, ipv;         // items per rotated head, per copied head
-    int units;            // 4-bit lanes per token
+    int half;          // rot / 2
+    int iph, ipv;      // items of a rotated head, of a copied head
+    int uq, uk, units; // a token's units: those of q, of k, all
+    int tokens;        // tokens a block may meet
+    int64_t total;     // units of all tokens
+    Div div_units, div_iph, div_ipv, div_seq;
 };
 
 // What a block knows of each of its tokens.
 struct Token {
-    int64_t seq, within;  // sequence and place in it (0 and the token itself where numbered through)
-    int64_t row;          // pool row of head 0 (head stride 1 << log2bs rows), or -1
+    int64_t row;  // pool row of head 0 (heads are 1 << log2bs rows apart), or -1
     int pos;
-    int live;
+    int live;     // 0: padding behind the last sequence
 };
 
-RKV_DEV void store8(float* p, const float* v) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-RKV_DEV uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&b);
-}
-RKV_DEV void store8(__nv_bfloat16* p, const float* v) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-}
-RKV_DEV void copy8(const float* x, float* y) {
-    const float4 a = reinterpret_cast<const float4*>(x)[0], b = reinterpret_cast<const float4*>(x)[1];
-    reinterpret_cast<float4*>(y)[0] = a;
-    reinterpret_cast<float4*>(y)[1] = b;
-}
-RKV_DEV void copy8(const __nv_bfloat16* x, __nv_bfloat16* y) {
-    *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(x);
-}
-RKV_DEV float from_f(float, float v) { return v; }
-RKV_DEV __nv_bfloat16 from_f(__nv_bfloat16, float v) { return __float2bfloat16_rn(v); }
-
-// One item of a rotated head: eight pairs (VEC: two runs of eight elements,
-// or eight elements of neighbouring pairs), or one pair, or what passes
-// through.  An item owns what it writes, so x may be y.
-template <typename T, bool VEC, bool INTER>
-RKV_DEV void rotate_item(const T* x, T* y, int item, const Params& p, const float* cs,
-                         const float* sn) {
-    const int rot = p.a.rot, half = p.half;
-    if constexpr (VEC) {
-        const int turning = INTER ? rot / 8 : half / 8;
-        if (item >= turning) {
-            const int e = rot + (item - turning) * 8;
-            if (x != y) copy8(x + e, y + e);
-            return;
-        }
-        if constexpr (INTER) {
-            float v[8], o[8];
-            load8(x + item * 8, v);
+// Eight elements as loaded.
+template <typename T> struct Eight;
+template <> struct Eight<__nv_bfloat16> {
+    uint4 u;
+    RKV_DEV void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+    RKV_DEV void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
+    RKV_DEV void get(float* o) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float c = cs[item * 4 + i], s = sn[item * 4 + i];
-                o[2 * i] = v[2 * i] * c - v[2 * i + 1] * s;
-                o[2 * i + 1] = v[2 * i + 1] * c + v[2 * i] * s;
-            }
-            store8(y + item * 8, o);
-        } else {
-            float u[8], v[8], o[8], r[8];
-            load8(x + item * 8, u);
-            load8(x + half + item * 8, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float c = cs[item * 8 + i], s = sn[item * 8 + i];
-                o[i] = u[i] * c - v[i] * s;
-                r[i] = v[i] * c + u[i] * s;
-            }
-            store8(y + item * 8, o);
-            store8(y + half + item * 8, r);
+        for (int t = 0; t < 4; ++t) {
+            o[2 * t] = __uint_as_float(w[t] << 16);
+            o[2 * t + 1] = __uint_as_float(w[t] & 0xffff0000u);
         }
-    } else {
-        if (item >= half) {
-            const int e = rot + (item - half);
-            if (x != y) y[e] = x[e];
-            return;
-        }
-        const int e = INTER ? 2 * item : item, f = INTER ? e + 1 : e + half;
-        const float u = Elem<T>::to_f(x[e]), v = Elem<T>::to_f(x[f]);
-        const float c = cs[item], s = sn[item];
-        y[e] = from_f(T(), u * c - v * s);
-        y[f] = from_f(T(), v * c + u * s);
     }
-}
+    static RKV_DEV uint32_t pack(float lo, float hi) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&b);
+    }
+    RKV_DEV void set(const float* v) {
+        u = make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
+    }
+};
+template <> struct Eight<float> {
+    float4 a, b;
+    RKV_DEV void load(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    RKV_DEV void store(float* p) const {
+        reinterpret_cast<float4*>(p)[0] = a;
+        reinterpret_cast<float4*>(p)[1] = b;
+    }
+    RKV_DEV void get(float* o) const {
+        o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+        o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+    }
+    RKV_DEV void set(const float* v) {
+        a = make_float4(v[0], v[1], v[2], v[3]);
+        b = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
+// One element (the rotated part does not split into steps of eight).
+template <typename T> RKV_DEV T one_of(float v);
+template <> RKV_DEV float one_of<float>(float v) { return v; }
+template <> RKV_DEV __nv_bfloat16 one_of<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-RKV_DEV int64_t view_at(const RowsView& v, const Token& t, int head) {
-    return t.seq * v.seq + t.within * v.tok + (int64_t)head * v.head;
+// (cos, sin) times the factor of pair i at a position.
+RKV_DEV void turn_of(const TokenArgs& a, int pos, int i, float& c, float& s) {
+    const uint64_t turn = (uint64_t)(int64_t)pos * a.turns[i];
+    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+    c *= a.factor;
+    s *= a.inverse ? -a.factor : a.factor;
 }
 
 // The last s with cu[s] <= j, searched 32 ways by a warp (cu[0] <= j).
@@ -152,9 +128,45 @@ RKV_DEV int64_t find_seq(const int32_t* cu, int64_t n, int64_t j) {
     return lo;
 }
 
-// One 4-bit row's share of a lane: values of W groups.
+// The place of token j in an append (by a whole warp).
+RKV_DEV Token place_token(const TokenArgs& a, int64_t j) {
+    Token t;
+    t.live = 1;
+    t.row = -1;
+    t.pos = 0;
+    int64_t s, first, count;
+    if (a.cu == nullptr) {
+        s = (uint32_t)j / (uint32_t)a.per_seq;
+        first = s * a.per_seq;
+        count = a.per_seq;
+    } else {
+        t.live = j < a.cu[a.num_seqs] && j >= a.cu[0];
+        s = t.live ? find_seq(a.cu, a.num_seqs, j) : 0;
+        first = a.cu[s];
+        count = a.cu[s + 1] - first;
+    }
+    if (!t.live) return t;
+    const int64_t r = (int64_t)a.lens[s] - count + (j - first);
+    t.pos = a.positions ? a.positions[j] : (int)r;
+    bool ok = r >= 0 && r < ((int64_t)a.pg.max_blocks << a.pg.log2bs);
+    if (ok) {
+        const int blk = a.pg.table[s * a.pg.max_blocks + (r >> a.pg.log2bs)];
+        ok = (unsigned)blk < (unsigned)a.pg.num_blocks;
+        t.row = (((int64_t)blk * a.pg.H) << a.pg.log2bs) + (r & ((1 << a.pg.log2bs) - 1));
+    }
+    if (!ok) {
+        t.row = -1;
+        if ((threadIdx.x & 31) == 0) set_error(a.status, kDevErrIndex, (unsigned)s);
+    }
+    return t;
+}
+
+// One 4-bit row's share of a lane: values of W groups.  The four lanes of the
+// row take part.
 template <int W>
-RKV_DEV void quantise_store(float (&v)[W][8], int t, uint8_t* codes, uint32_t* scales) {
+RKV_DEV void quantise_store(const float (&v)[W][8], int t, bool write, uint8_t* codes,
+                            uint32_t* scales) {
+    const uint32_t quad = 0xfu << (threadIdx.x & 28);
     uint32_t h[W][2], pair = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
@@ -167,9 +179,9 @@ RKV_DEV void quantise_store(float (&v)[W][8], int t, uint8_t* codes, uint32_t* s
         }
 #pragma unroll
         for (int o = 1; o <= 2; o <<= 1) {
-            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            bad += __shfl_xor_sync(0xffffffffu, bad, o);
+            mn = fminf(mn, __shfl_xor_sync(quad, mn, o));
+            mx = fmaxf(mx, __shfl_xor_sync(quad, mx, o));
+            bad += __shfl_xor_sync(quad, bad, o);
         }
         __nv_bfloat16 lo = __float2bfloat16_rd(mn);
         float lof = __bfloat162float(lo);
@@ -192,7 +204,7 @@ RKV_DEV void quantise_store(float (&v)[W][8], int t, uint8_t* codes, uint32_t* s
         if (t == w)
             pair = (uint32_t)__bfloat16_as_ushort(sc) | ((uint32_t)__bfloat16_as_ushort(lo) << 16);
     }
-    if (codes == nullptr) return;
+    if (!write) return;
     if constexpr (W == 4) {
         reinterpret_cast<uint4*>(codes)[t] =
             make_uint4(h[0][0] | (h[1][0] << 16), h[2][0] | (h[3][0] << 16),
@@ -204,195 +216,244 @@ RKV_DEV void quantise_store(float (&v)[W][8], int t, uint8_t* codes, uint32_t* s
     if (t < W) scales[t] = pair;
 }
 
-// Eight elements of x at e, turned where they lie below rot (out of place:
-// the partners are read again, from L1).
-template <typename T, bool VEC, bool INTER>
-RKV_DEV void load_turned(const T* x, int e, const Params& p, const float* cs, const float* sn,
-                         float* o) {
+// The lane's part of a K row turned in place: values 32 w + 8 t .. of group w;
+// cs, sn: the token's cosines and sines, x: the row (partners that lie in
+// another lane are read again).
+template <typename T, bool VEC, bool INTER, int W>
+RKV_DEV void turn_row(float (&v)[W][8], const T* x, int t, const Params& p, const float* cs,
+                      const float* sn) {
     const int rot = p.a.rot, half = p.half;
-    load8(x + e, o);
-    if (e >= rot) return;
-    if constexpr (VEC && INTER) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float c = cs[e / 2 + i], s = sn[e / 2 + i], u = o[2 * i], v = o[2 * i + 1];
-            o[2 * i] = u * c - v * s;
-            o[2 * i + 1] = v * c + u * s;
-        }
-    } else if constexpr (VEC) {
-        const bool first = e < half;
-        const int i0 = first ? e : e - half;
-        float v[8];
-        load8(x + (first ? e + half : e - half), v);
+    for (int w = 0; w < W; ++w) {
+        const int e = 32 * w + 8 * t;
+        if (e >= rot) continue;
+        if constexpr (VEC && INTER) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float c = cs[i0 + i], s = first ? -sn[i0 + i] : sn[i0 + i];
-            o[i] = o[i] * c + v[i] * s;
-        }
-    } else {
+            for (int i = 0; i < 4; ++i) {
+                const float c = cs[e / 2 + i], s = sn[e / 2 + i], a = v[w][2 * i], b = v[w][2 * i + 1];
+                v[w][2 * i] = a * c - b * s;
+                v[w][2 * i + 1] = b * c + a * s;
+            }
+        } else if constexpr (VEC) {
+            const bool first = e < half;
+            const int i0 = first ? e : e - half;
+            Eight<T> other;
+            other.load(x + (first ? e + half : e - half));
+            float o[8];
+            other.get(o);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int at = e + i;
-            if (at < rot) {
-                const bool first = INTER ? (at & 1) == 0 : at < half;
-                const int k = INTER ? at >> 1 : (first ? at : at - half);
-                const int other = INTER ? at ^ 1 : (first ? at + half : at - half);
-                const float v = Elem<T>::to_f(x[other]);
-                o[i] = o[i] * cs[k] + (first ? -v : v) * sn[k];
+            for (int i = 0; i < 8; ++i) {
+                const float c = cs[i0 + i], s = first ? -sn[i0 + i] : sn[i0 + i];
+                v[w][i] = v[w][i] * c + o[i] * s;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int at = e + i;
+                if (at < rot) {
+                    const bool first = INTER ? (at & 1) == 0 : at < half;
+                    const int k = INTER ? at >> 1 : (first ? at : at - half);
+                    const int other = INTER ? at ^ 1 : (first ? at + half : at - half);
+                    const float o = Elem<T>::to_f(x[other]);
+                    v[w][i] = v[w][i] * cs[k] + (first ? -o : o) * sn[k];
+                }
             }
         }
     }
 }
 
-// VEC: the rotated part splits into whole steps of eight.
+// Heads that a thread takes together.
+template <typename T> constexpr int kHeads = sizeof(T) == 2 ? 4 : 2;
+
+// VEC: the rotated part splits into whole steps of eight.  A unit is one item
+// (the eight pairs, or eight elements, that a thread holds; without VEC one
+// pair or element) of kHeads heads, or a lane of a 4-bit row.
 template <typename T, bool VEC, bool INTER, bool Q4, int W>
 __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant__ Params p) {
-    extern __shared__ float sines[];  // [tpb][2][half]
-    __shared__ Token tok[kMaxTokens];
+    extern __shared__ __align__(16) uint8_t smem[];
+    Token* tok = reinterpret_cast<Token*>(smem);                          // [tokens]
+    float* sines = reinterpret_cast<float*>(smem + sizeof(Token) * p.tokens);  // 4 bits: [tokens][2][half]
+    constexpr int HG = kHeads<T>;
     const TokenArgs& a = p.a;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t j0 = (int64_t)blockIdx.x * p.tpb;
-    const int n_tok = (int)(a.num_tokens - j0 < p.tpb ? a.num_tokens - j0 : p.tpb);
+    const int tid = threadIdx.x;
     const bool append = a.pg.table != nullptr;
+    const int64_t id0 = (int64_t)blockIdx.x * kThreads;
+    const int64_t j0 = id0 / p.units;
+    const uint32_t e = (uint32_t)(id0 - j0 * p.units) + tid;  // unit counted from token j0
+    const bool on = id0 + tid < p.total;
+    const uint32_t tl = div_by(e, p.div_units);
+    const int64_t j = j0 + tl;
+    uint32_t unit = e - tl * p.units;
 
-    for (int i = tid >> 5; i < n_tok; i += kThreads / 32) {
-        const int64_t j = j0 + i;
-        Token t;
-        t.live = 1;
-        t.row = -1;
-        t.pos = 0;
-        if (!append) {
-            t.seq = j / a.per_seq;
-            t.within = j - t.seq * a.per_seq;
+    // sources: tokens by sequence, or numbered through
+    const int64_t seq = a.cu ? 0 : div_by((uint32_t)j, p.div_seq), within = j - seq * a.per_seq;
+    const bool is_q = unit < (uint32_t)p.uq;
+    const bool is_k = !Q4 && !is_q && unit < (uint32_t)(p.uq + p.uk);
+    const RowsView& src = is_q ? a.q : (is_k ? a.k : a.v);
+    uint32_t item = 0, head = 0;
+    bool turning = false;  // the item is turned (else copied)
+    int at = 0;            // its first element
+    Eight<T> x[HG], y[HG];
+    [[maybe_unused]] Eight<T> row4[W];
+    T one_x[HG], one_y[HG];
+    [[maybe_unused]] bool is_v4 = false;
+    const T* from = nullptr;
+    if (!Q4 || is_q) {
+        uint32_t u = unit - (is_q ? 0 : (is_k ? p.uq : p.uq + p.uk));
+        const bool rotated = is_q || is_k;
+        const uint32_t g = div_by(u, rotated ? p.div_iph : p.div_ipv);
+        item = u - g * (rotated ? p.iph : p.ipv);
+        head = g * HG;
+        if (!rotated) {
+            at = item * 8;
+        } else if constexpr (VEC) {
+            const uint32_t n = INTER ? a.rot / 8 : p.half / 8;
+            turning = item < n;
+            at = turning ? item * 8 : a.rot + (item - n) * 8;
         } else {
-            int64_t s, first, count;
-            if (a.cu == nullptr) {
-                s = j / a.per_seq;
-                first = s * a.per_seq;
-                count = a.per_seq;
-                t.seq = s;
-                t.within = j - first;
+            turning = item < (uint32_t)p.half;
+            at = turning ? (INTER ? 2 * item : item) : a.rot + (item - p.half);
+        }
+        from = static_cast<const T*>(src.data) + seq * src.seq + within * src.tok + head * src.head + at;
+#pragma unroll
+        for (int k = 0; k < HG; ++k) {
+            if (!on || head + k >= (uint32_t)src.heads) continue;
+            const T* f = from + k * src.head;
+            if (VEC || !rotated) {
+                x[k].load(f);
+                if (!INTER && turning) y[k].load(f + p.half);
             } else {
-                t.live = j < a.cu[a.num_seqs] && j >= a.cu[0];
-                s = t.live ? find_seq(a.cu, a.num_seqs, j) : 0;
-                first = a.cu[s];
-                count = a.cu[s + 1] - first;
-                t.seq = 0;
-                t.within = j;
-            }
-            const int64_t r = (int64_t)a.lens[s] - count + (j - first);
-            if (t.live) {
-                t.pos = (int)r;
-                bool ok = r >= 0 && r < ((int64_t)a.pg.max_blocks << a.pg.log2bs);
-                if (ok) {
-                    const int blk = a.pg.table[s * a.pg.max_blocks + (r >> a.pg.log2bs)];
-                    ok = (unsigned)blk < (unsigned)a.pg.num_blocks;
-                    t.row = (((int64_t)blk * a.pg.H) << a.pg.log2bs) +
-                            (r & ((1 << a.pg.log2bs) - 1));
-                }
-                if (!ok) {
-                    t.row = -1;
-                    if (lane == 0) set_error(a.status, kDevErrIndex, (unsigned)s);
-                }
+                one_x[k] = *f;
+                if (turning) one_y[k] = f[INTER ? 1 : p.half];
             }
         }
-        if (t.live && a.positions) t.pos = a.positions[j];
-        if (lane == 0) tok[i] = t;
+    } else if constexpr (Q4) {
+        // K of all heads, then V: a warp rarely holds both
+        const uint32_t u = unit - p.uq, r = u >> 2;
+        is_v4 = r >= (uint32_t)a.k.heads;
+        head = r - (is_v4 ? a.k.heads : 0);
+        const RowsView& v = is_v4 ? a.v : a.k;
+        from = static_cast<const T*>(v.data) + seq * v.seq + within * v.tok + head * v.head;
+        if (on)
+#pragma unroll
+            for (int w = 0; w < W; ++w) row4[w].load(from + 32 * w + 8 * (u & 3));
     }
-    __syncthreads();
-    for (int e = tid; e < n_tok * p.half; e += kThreads) {
-        const int i = e / p.half, k = e - i * p.half;
-        const uint64_t turn = (uint64_t)(int64_t)tok[i].pos * a.turns[k];
-        float s, c;
-        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-        float* cs = sines + i * 2 * p.half;
-        cs[k] = c * a.factor;
-        cs[p.half + k] = (a.inverse ? -s : s) * a.factor;
-    }
-    __syncthreads();
 
-    const T* q = static_cast<const T*>(a.q.data);
-    const T* kk = static_cast<const T*>(a.k.data);
-    const T* vv = static_cast<const T*>(a.v.data);
-    const int64_t hs = (int64_t)1 << a.pg.log2bs;  // rows between heads of a block
-    const int step = kThreads * gridDim.y;
-    for (uint32_t e = blockIdx.y * kThreads + tid; e < (uint32_t)(n_tok * p.items); e += step) {
-        const uint32_t i = div_by(e, p.div_items);
-        uint32_t it = e - i * p.items;
-        const Token& t = tok[i];
-        if (!t.live) continue;
-        [[maybe_unused]] const float* cs = sines + i * 2 * p.half;
-        if (it < (uint32_t)p.items_q) {
-            const uint32_t h = div_by(it, p.div_iph);
-            rotate_item<T, VEC, INTER>(q + view_at(a.q, t, h),
-                                       static_cast<T*>(a.out_q.data) + view_at(a.out_q, t, h),
-                                       it - h * p.iph, p, cs, cs + p.half);
-            continue;
+    // positions and rows
+    Token t;
+    t.live = 1;
+    t.row = -1;
+    t.pos = 0;
+    if (append) {
+        const int warp = tid >> 5;
+        const int64_t last = min(id0 + kThreads, p.total) - 1;
+        const int n = (int)(last / p.units - j0) + 1;
+        for (int i = warp; i < n; i += kThreads / 32) {
+            const Token x = place_token(a, j0 + i);
+            if ((tid & 31) == 0) tok[i] = x;
         }
-        it -= p.items_q;
-        if constexpr (!Q4) {
-            if (it < (uint32_t)p.items_k) {
-                const uint32_t h = div_by(it, p.div_iph);
-                T* dst;
-                if (append) {
-                    if (t.row < 0) continue;
-                    dst = static_cast<T*>(a.k_pool) + (t.row + h * hs) * a.d;
-                } else {
-                    dst = static_cast<T*>(a.out_k.data) + view_at(a.out_k, t, h);
-                }
-                rotate_item<T, VEC, INTER>(kk + view_at(a.k, t, h), dst, it - h * p.iph, p, cs,
-                                           cs + p.half);
-            } else {
-                it -= p.items_k;
-                const uint32_t h = div_by(it, p.div_ipv);
-                const int at = (it - h * p.ipv) * 8;
-                if (t.row < 0) continue;
-                copy8(vv + view_at(a.v, t, h) + at,
-                      static_cast<T*>(a.v_pool) + (t.row + h * hs) * a.d + at);
+        __syncthreads();
+        if constexpr (Q4) {
+            for (int q = tid; q < n * p.half; q += kThreads) {
+                const int i = q / p.half, k = q - i * p.half;
+                float c, s;
+                turn_of(a, tok[i].pos, k, c, s);
+                sines[i * 2 * p.half + k] = c;
+                sines[i * 2 * p.half + p.half + k] = s;
             }
+            __syncthreads();
         }
+        if (on) t = tok[tl];
+    } else if (on) {
+        t.pos = a.positions[j];
     }
-    if constexpr (Q4) {
-        // whole warps take part in every step: the shuffles need all lanes
-        const uint32_t total = (uint32_t)(n_tok * p.units);
-        for (uint32_t e0 = blockIdx.y * kThreads + (tid & ~31); e0 < total; e0 += step) {
-            const uint32_t e = e0 + lane, u = e < total ? e : total - 1;
-            const uint32_t i = div_by(u, p.div_units), it = u - i * p.units;
-            const Token& t = tok[i];
-            const int tl = lane & 3;
-            // K of all heads, then V: a warp rarely holds both
-            const bool is_v = (it >> 2) >= (uint32_t)a.k.heads;
-            const uint32_t h = (it >> 2) - (is_v ? a.k.heads : 0);
-            const bool ok = e < total && t.live && t.row >= 0;
-            float x[W][8];
-            if (t.live) {
-                const float* cs = sines + i * 2 * p.half;
-                const T* src = is_v ? vv + view_at(a.v, t, h) : kk + view_at(a.k, t, h);
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    if (is_v)
-                        load8(src + 32 * w + 8 * tl, x[w]);
-                    else
-                        load_turned<T, VEC, INTER>(src, 32 * w + 8 * tl, p, cs, cs + p.half, x[w]);
-                }
-            } else {
-#pragma unroll
-                for (int w = 0; w < W; ++w)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) x[w][k] = 0.f;
-            }
-            const int64_t row = ok ? t.row + h * hs : 0;
-            quantise_store<W>(x, tl,
-                              ok ? (is_v ? a.q4p.v_codes : a.q4p.k_codes) + row * (a.d / 2) : nullptr,
-                              (is_v ? a.q4p.v_scales : a.q4p.k_scales) + row * W);
+    if (!on || !t.live) {
+        return;  // (a 4-bit row's four lanes leave together)
+    }
+
+    const int64_t hs = (int64_t)1 << a.pg.log2bs;  // rows between heads of a block
+    if (!Q4 || is_q) {
+        if (!is_q && append && t.row < 0) return;
+        T* to;
+        int64_t step;
+        if (is_q || !append) {
+            const RowsView& dst = is_q ? a.out_q : a.out_k;
+            to = static_cast<T*>(dst.data) + seq * dst.seq + within * dst.tok + head * dst.head + at;
+            step = dst.head;
+        } else {
+            to = static_cast<T*>(is_k ? a.k_pool : a.v_pool) + (t.row + head * hs) * a.d + at;
+            step = hs * a.d;
         }
+        const bool rotated = is_q || is_k;
+        if (VEC || !rotated) {
+            constexpr int PAIRS = INTER ? 4 : 8;
+            float cs[PAIRS], sn[PAIRS];
+            if (turning) {
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) turn_of(a, t.pos, item * PAIRS + i, cs[i], sn[i]);
+            }
+#pragma unroll
+            for (int k = 0; k < HG; ++k) {
+                if (head + k >= (uint32_t)src.heads) break;
+                T* q = to + k * step;
+                if (turning) {
+                    float u[8], v[8], o[8];
+                    x[k].get(u);
+                    if constexpr (INTER) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            o[2 * i] = u[2 * i] * cs[i] - u[2 * i + 1] * sn[i];
+                            o[2 * i + 1] = u[2 * i + 1] * cs[i] + u[2 * i] * sn[i];
+                        }
+                        x[k].set(o);
+                    } else {
+                        y[k].get(v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = u[i] * cs[i] - v[i] * sn[i];
+                        x[k].set(o);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = v[i] * cs[i] + u[i] * sn[i];
+                        y[k].set(o);
+                        y[k].store(q + p.half);
+                    }
+                }
+                x[k].store(q);
+            }
+        } else {
+            float c = 1.f, s = 0.f;
+            if (turning) turn_of(a, t.pos, item, c, s);
+#pragma unroll
+            for (int k = 0; k < HG; ++k) {
+                if (head + k >= (uint32_t)src.heads) break;
+                T* q = to + k * step;
+                if (!turning) {
+                    *q = one_x[k];
+                    continue;
+                }
+                const float u = Elem<T>::to_f(one_x[k]), v = Elem<T>::to_f(one_y[k]);
+                *q = one_of<T>(u * c - v * s);
+                q[INTER ? 1 : p.half] = one_of<T>(v * c + u * s);
+            }
+        }
+    } else if constexpr (Q4) {
+        const int l = (unit - p.uq) & 3;
+        float v[W][8];
+#pragma unroll
+        for (int w = 0; w < W; ++w) row4[w].get(v[w]);
+        if (!is_v4 && p.half > 0) {
+            const float* cs = sines + tl * 2 * p.half;
+            turn_row<T, VEC, INTER, W>(v, from, l, p, cs, cs + p.half);
+        }
+        const int64_t row = t.row + head * hs;
+        quantise_store<W>(v, l, t.row >= 0, (is_v4 ? a.q4p.v_codes : a.q4p.k_codes) + row * (a.d / 2),
+                          (is_v4 ? a.q4p.v_scales : a.q4p.k_scales) + row * W);
     }
 }
 
 template <typename T, bool VEC, bool INTER>
-cudaError_t go(const Params& p, dim3 grid, size_t smem, cudaStream_t s) {
+cudaError_t go(const Params& p, unsigned grid, size_t smem, cudaStream_t s) {
     if (!p.a.q4)
-        tokens_kernel<T, VEC, INTER, false, 4><<<grid, kThreads, smem, s>>>(p);
+        tokens_kernel<T, VEC, INTER, false, 2><<<grid, kThreads, smem, s>>>(p);
     else if (p.a.d == 128)
         tokens_kernel<T, VEC, INTER, true, 4><<<grid, kThreads, smem, s>>>(p);
     else
@@ -400,10 +461,39 @@ cudaError_t go(const Params& p, dim3 grid, size_t smem, cudaStream_t s) {
     return cudaGetLastError();
 }
 template <typename T>
-cudaError_t go(const Params& p, bool vec, dim3 grid, size_t smem, cudaStream_t s) {
-    if (p.a.interleaved)
-        return vec ? go<T, true, true>(p, grid, smem, s) : go<T, false, true>(p, grid, smem, s);
-    return vec ? go<T, true, false>(p, grid, smem, s) : go<T, false, false>(p, grid, smem, s);
+cudaError_t go(Params& p, cudaStream_t s) {
+    const TokenArgs& a = p.a;
+    const bool vec = a.rot == 0 || (a.interleaved ? a.rot % 8 == 0 : a.rot % 16 == 0);
+    // without a rotation every item is a copy of eight
+    p.iph = !vec ? p.half + (a.d - a.rot)
+                 : (a.interleaved ? a.rot / 8 : p.half / 8) + (a.d - a.rot) / 8;
+    p.ipv = a.d / 8;
+    constexpr int HG = kHeads<T>;
+    const auto groups = [&](int heads) { return (heads + HG - 1) / HG; };
+    p.uq = a.q.data ? groups(a.q.heads) * p.iph : 0;
+    p.uk = a.k.data && !a.q4 ? groups(a.k.heads) * p.iph : 0;
+    if (a.q4) {
+        // rows of four lanes start at multiples of four
+        p.uq = (p.uq + 3) / 4 * 4;
+        p.units = p.uq + a.k.heads * 2 * 4;
+    } else {
+        p.units = p.uq + p.uk + (a.v.data ? groups(a.v.heads) * p.ipv : 0);
+    }
+    p.total = a.num_tokens * p.units;
+    p.tokens = (kThreads - 1) / p.units + 2;
+    p.div_units = make_div(p.units);
+    p.div_iph = make_div(p.iph);
+    p.div_ipv = make_div(p.ipv);
+    p.div_seq = make_div((uint32_t)a.per_seq);
+    const int64_t blocks = (p.total + kThreads - 1) / kThreads;
+    if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
+    const size_t smem = a.pg.table ? sizeof(Token) * p.tokens +
+                                         (a.q4 ? sizeof(float) * 2 * p.half * p.tokens : 0)
+                                   : 0;
+    const unsigned g = (unsigned)blocks;
+    if (a.interleaved)
+        return vec ? go<T, true, true>(p, g, smem, s) : go<T, false, true>(p, g, smem, s);
+    return vec ? go<T, true, false>(p, g, smem, s) : go<T, false, false>(p, g, smem, s);
 }
 
 // ------------------------------------------------------------- q4 read --
@@ -454,7 +544,9 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const __grid_constant
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             v[k] = fmaf(sc, (float)((half[k >> 2][w] >> (4 * (k & 3))) & 15u), lo);
-        store8(dst + 32 * w + 8 * t, v);
+        Eight<T> o;
+        o.set(v);
+        o.store(dst + 32 * w + 8 * t);
     }
 }
 
@@ -465,33 +557,7 @@ cudaError_t launch_tokens(const TokenArgs& a, cudaStream_t s) {
     Params p;
     p.a = a;
     p.half = a.rot / 2;
-    const bool vec = a.rot == 0 || (a.interleaved ? a.rot % 8 == 0 : a.rot % 16 == 0);
-    // without a rotation every item is a copy of eight
-    p.iph = !vec ? p.half + (a.d - a.rot)
-                 : (a.interleaved ? a.rot / 8 : p.half / 8) + (a.d - a.rot) / 8;
-    p.ipv = a.d / 8;
-    p.items_q = a.q.data ? a.q.heads * p.iph : 0;
-    p.items_k = (a.k.data && !a.q4) ? a.k.heads * p.iph : 0;
-    p.items = p.items_q + p.items_k + (a.v.data && !a.q4 ? a.v.heads * p.ipv : 0);
-    p.units = a.q4 ? a.k.heads * 2 * 4 : 0;
-    p.div_items = make_div(p.items ? p.items : 1);
-    p.div_iph = make_div(p.iph);
-    p.div_ipv = make_div(p.ipv);
-    p.div_units = make_div(p.units ? p.units : 1);
-    // a block takes enough tokens for about two steps of its threads, and a
-    // token with many heads is shared by several blocks while tokens are few
-    const int per_token = p.items + p.units;
-    int tpb = 2 * kThreads / per_token;
-    tpb = tpb < 1 ? 1 : (tpb > kMaxTokens ? kMaxTokens : tpb);
-    while (tpb > 1 && (a.num_tokens + tpb - 1) / tpb < 304) tpb /= 2;
-    p.tpb = tpb;
-    const int64_t blocks = (a.num_tokens + tpb - 1) / tpb;
-    int64_t split = 1;
-    while (blocks * split < 152 && split * kThreads < per_token) split *= 2;
-    const dim3 grid((unsigned)blocks, (unsigned)split);
-    const size_t smem = sizeof(float) * (size_t)tpb * 2 * (p.half ? p.half : 1);
-    return a.dtype == RKV_DTYPE_BF16 ? go<__nv_bfloat16>(p, vec, grid, smem, s)
-                                     : go<float>(p, vec, grid, smem, s);
+    return a.dtype == RKV_DTYPE_BF16 ? go<__nv_bfloat16>(p, s) : go<float>(p, s);
 }
 
 cudaError_t launch_q4_read(const Q4ReadArgs& a, cudaStream_t s) {

@@ -384,8 +384,8 @@ int rkv_rope_apply(const rkv_rope_plan* plan, int dtype, int head_dim, int64_t n
  * k, v, q).  With cu_tokens NULL every sequence brings new_per_seq tokens
  * (num_tokens = num_seqs * new_per_seq); otherwise sequence s brings tokens
  * cu_tokens[s] .. cu_tokens[s + 1] - 1 ([num_seqs + 1] int32 on the device,
- * ascending from 0), num_tokens bounds cu_tokens[num_seqs], and tokens past it
- * (padding) are neither read nor written.  k and v have num_kv_heads heads.
+ * ascending from 0), num_tokens bounds cu_tokens[num_seqs], and for tokens past
+ * it (padding) nothing is written.  k and v have num_kv_heads heads.
  * With a rope, k is turned by positions (NULL: by the rows it is written to);
  * q (num_kv_heads * gqa_group heads; may be NULL) is turned the same way, or
  * copied without a rope, into out_q (which may be q).  Rows outside the table
