@@ -47,10 +47,11 @@ struct Params {
     TokenArgs a;
     int half;          // rot / 2
     int iph, ipv;      // items of a rotated head, of a copied head
-    int uq, uk, units; // a token's units: those of q, of k, all
+    int uq, uk, ukv;   // a token's units: those of q, of k, of k and v
     int tokens;        // tokens a block may meet
-    int64_t total;     // units of all tokens
-    Div div_units, div_iph, div_ipv, div_seq;
+    int q_blocks;      // the first blocks take the q of all tokens, the others k and v
+    int64_t total_q, total_kv;
+    Div div_q, div_kv, div_iph, div_ipv, div_seq;
 };
 
 // What a block knows of each of its tokens.
@@ -106,10 +107,32 @@ template <typename T> RKV_DEV T one_of(float v);
 template <> RKV_DEV float one_of<float>(float v) { return v; }
 template <> RKV_DEV __nv_bfloat16 one_of<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// (cos, sin) of an angle in units of 2^-32 turn.  The angle is taken to the
+// nearest quarter turn in whole numbers, and what is left, at most pi / 4, goes
+// through the Taylor series of both functions (to x^9 and x^10: the next terms
+// are below 2^-28 of the result); the quarter turns swap and change signs.
+RKV_DEV void sine_of(uint32_t turn, float& c, float& s) {
+    const uint32_t near = turn + 0x20000000u;
+    const float x = (float)(int32_t)(turn - (near & 0xc0000000u)) * 1.4629180792671596e-9f;  // 2 pi 2^-32
+    const float t = x * x;
+    float u = fmaf(t, 2.7557319e-6f, -1.9841270e-4f);  // 1 / 9!, -1 / 7!
+    u = fmaf(t, u, 8.3333333e-3f);
+    u = fmaf(t, u, -1.6666667e-1f);
+    u = fmaf(x * t, u, x);
+    float v = fmaf(t, -2.7557319e-7f, 2.4801587e-5f);  // -1 / 10!, 1 / 8!
+    v = fmaf(t, v, -1.3888889e-3f);
+    v = fmaf(t, v, 4.1666667e-2f);
+    v = fmaf(t, v, -0.5f);
+    v = fmaf(t, v, 1.f);
+    const bool swap = (near & 0x40000000u) != 0;
+    const uint32_t cs = (near + 0x40000000u) & 0x80000000u, sn = near & 0x80000000u;
+    c = __uint_as_float(__float_as_uint(swap ? u : v) ^ cs);
+    s = __uint_as_float(__float_as_uint(swap ? v : u) ^ sn);
+}
 // (cos, sin) times the factor of pair i at a position.
 RKV_DEV void turn_of(const TokenArgs& a, int pos, int i, float& c, float& s) {
     const uint64_t turn = (uint64_t)(int64_t)pos * a.turns[i];
-    sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
+    sine_of((uint32_t)(turn >> 32), c, s);
     c *= a.factor;
     s *= a.inverse ? -a.factor : a.factor;
 }
@@ -130,24 +153,37 @@ RKV_DEV int64_t find_seq(const int32_t* cu, int64_t n, int64_t j) {
 
 // The place of token j in an append (by a whole warp).
 RKV_DEV Token place_token(const TokenArgs& a, int64_t j) {
+    const int lane = threadIdx.x & 31;
     Token t;
     t.live = 1;
     t.row = -1;
-    t.pos = 0;
-    int64_t s, first, count;
+    t.pos = a.positions ? a.positions[j] : 0;
+    int64_t s, first, count, len;
     if (a.cu == nullptr) {
         s = (uint32_t)j / (uint32_t)a.per_seq;
         first = s * a.per_seq;
         count = a.per_seq;
+        len = a.lens[s];
+    } else if (a.num_seqs <= 32) {
+        // one look at all sequences: those that end at or before j come before its own
+        const bool in = lane < a.num_seqs;
+        const int c0 = in ? a.cu[lane] : 0, c1 = in ? a.cu[lane + 1] : 0, n = in ? a.lens[lane] : 0;
+        const int before = __popc(__ballot_sync(0xffffffffu, in && c1 <= j));
+        t.live = before < a.num_seqs && j >= __shfl_sync(0xffffffffu, c0, 0);
+        s = before < a.num_seqs ? before : 0;
+        first = __shfl_sync(0xffffffffu, c0, (int)s);
+        count = __shfl_sync(0xffffffffu, c1, (int)s) - first;
+        len = __shfl_sync(0xffffffffu, n, (int)s);
     } else {
         t.live = j < a.cu[a.num_seqs] && j >= a.cu[0];
         s = t.live ? find_seq(a.cu, a.num_seqs, j) : 0;
         first = a.cu[s];
         count = a.cu[s + 1] - first;
+        len = a.lens[s];
     }
     if (!t.live) return t;
-    const int64_t r = (int64_t)a.lens[s] - count + (j - first);
-    t.pos = a.positions ? a.positions[j] : (int)r;
+    const int64_t r = len - count + (j - first);
+    if (!a.positions) t.pos = (int)r;
     bool ok = r >= 0 && r < ((int64_t)a.pg.max_blocks << a.pg.log2bs);
     if (ok) {
         const int blk = a.pg.table[s * a.pg.max_blocks + (r >> a.pg.log2bs)];
@@ -156,7 +192,7 @@ RKV_DEV Token place_token(const TokenArgs& a, int64_t j) {
     }
     if (!ok) {
         t.row = -1;
-        if ((threadIdx.x & 31) == 0) set_error(a.status, kDevErrIndex, (unsigned)s);
+        if (lane == 0) set_error(a.status, kDevErrIndex, (unsigned)s);
     }
     return t;
 }
@@ -277,18 +313,20 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
     const TokenArgs& a = p.a;
     const int tid = threadIdx.x;
     const bool append = a.pg.table != nullptr;
-    const int64_t id0 = (int64_t)blockIdx.x * kThreads;
-    const int64_t j0 = id0 / p.units;
-    const uint32_t e = (uint32_t)(id0 - j0 * p.units) + tid;  // unit counted from token j0
-    const bool on = id0 + tid < p.total;
-    const uint32_t tl = div_by(e, p.div_units);
+    const bool is_q = blockIdx.x < (unsigned)p.q_blocks;
+    const int64_t id0 = (int64_t)(blockIdx.x - (is_q ? 0 : p.q_blocks)) * kThreads;
+    const int units = is_q ? p.uq : p.ukv;
+    const int64_t total = is_q ? p.total_q : p.total_kv;
+    const int64_t j0 = id0 / units;
+    const uint32_t e = (uint32_t)(id0 - j0 * units) + tid;  // unit counted from token j0
+    const bool on = id0 + tid < total;
+    const uint32_t tl = div_by(e, is_q ? p.div_q : p.div_kv);
     const int64_t j = j0 + tl;
-    uint32_t unit = e - tl * p.units;
+    const uint32_t unit = e - tl * units;
 
     // sources: tokens by sequence, or numbered through
     const int64_t seq = a.cu ? 0 : div_by((uint32_t)j, p.div_seq), within = j - seq * a.per_seq;
-    const bool is_q = unit < (uint32_t)p.uq;
-    const bool is_k = !Q4 && !is_q && unit < (uint32_t)(p.uq + p.uk);
+    const bool is_k = !Q4 && !is_q && unit < (uint32_t)p.uk;
     const RowsView& src = is_q ? a.q : (is_k ? a.k : a.v);
     uint32_t item = 0, head = 0;
     bool turning = false;  // the item is turned (else copied)
@@ -299,7 +337,7 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
     [[maybe_unused]] bool is_v4 = false;
     const T* from = nullptr;
     if (!Q4 || is_q) {
-        uint32_t u = unit - (is_q ? 0 : (is_k ? p.uq : p.uq + p.uk));
+        const uint32_t u = is_q || is_k ? unit : unit - p.uk;
         const bool rotated = is_q || is_k;
         const uint32_t g = div_by(u, rotated ? p.div_iph : p.div_ipv);
         item = u - g * (rotated ? p.iph : p.ipv);
@@ -329,47 +367,48 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
         }
     } else if constexpr (Q4) {
         // K of all heads, then V: a warp rarely holds both
-        const uint32_t u = unit - p.uq, r = u >> 2;
+        const uint32_t r = unit >> 2;
         is_v4 = r >= (uint32_t)a.k.heads;
         head = r - (is_v4 ? a.k.heads : 0);
         const RowsView& v = is_v4 ? a.v : a.k;
         from = static_cast<const T*>(v.data) + seq * v.seq + within * v.tok + head * v.head;
         if (on)
 #pragma unroll
-            for (int w = 0; w < W; ++w) row4[w].load(from + 32 * w + 8 * (u & 3));
+            for (int w = 0; w < W; ++w) row4[w].load(from + 32 * w + 8 * (unit & 3));
     }
 
-    // positions and rows
+    // positions and rows (q wants the rows only where they are its positions)
     Token t;
     t.live = 1;
     t.row = -1;
     t.pos = 0;
-    if (append) {
+    if (append && (!is_q || (a.rot > 0 && !a.positions))) {
         const int warp = tid >> 5;
-        const int64_t last = min(id0 + kThreads, p.total) - 1;
-        const int n = (int)(last / p.units - j0) + 1;
+        const int64_t last = min(id0 + kThreads, total) - 1;
+        const int n = (int)(last / units - j0) + 1;
         for (int i = warp; i < n; i += kThreads / 32) {
             const Token x = place_token(a, j0 + i);
             if ((tid & 31) == 0) tok[i] = x;
         }
         __syncthreads();
         if constexpr (Q4) {
-            for (int q = tid; q < n * p.half; q += kThreads) {
-                const int i = q / p.half, k = q - i * p.half;
-                float c, s;
-                turn_of(a, tok[i].pos, k, c, s);
-                sines[i * 2 * p.half + k] = c;
-                sines[i * 2 * p.half + p.half + k] = s;
+            if (!is_q) {
+                for (int q = tid; q < n * p.half; q += kThreads) {
+                    const int i = q / p.half, k = q - i * p.half;
+                    float c, s;
+                    turn_of(a, tok[i].pos, k, c, s);
+                    sines[i * 2 * p.half + k] = c;
+                    sines[i * 2 * p.half + p.half + k] = s;
+                }
+                __syncthreads();
             }
-            __syncthreads();
         }
         if (on) t = tok[tl];
     } else if (on) {
-        t.pos = a.positions[j];
+        if (a.positions) t.pos = a.positions[j];
+        if (a.cu) t.live = j < a.cu[a.num_seqs] && j >= a.cu[0];
     }
-    if (!on || !t.live) {
-        return;  // (a 4-bit row's four lanes leave together)
-    }
+    if (!on || !t.live) return;  // (a 4-bit row's four lanes leave together)
 
     const int64_t hs = (int64_t)1 << a.pg.log2bs;  // rows between heads of a block
     if (!Q4 || is_q) {
@@ -436,7 +475,7 @@ __global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant_
             }
         }
     } else if constexpr (Q4) {
-        const int l = (unit - p.uq) & 3;
+        const int l = unit & 3;
         float v[W][8];
 #pragma unroll
         for (int w = 0; w < W; ++w) row4[w].get(v[w]);
@@ -472,21 +511,20 @@ cudaError_t go(Params& p, cudaStream_t s) {
     const auto groups = [&](int heads) { return (heads + HG - 1) / HG; };
     p.uq = a.q.data ? groups(a.q.heads) * p.iph : 0;
     p.uk = a.k.data && !a.q4 ? groups(a.k.heads) * p.iph : 0;
-    if (a.q4) {
-        // rows of four lanes start at multiples of four
-        p.uq = (p.uq + 3) / 4 * 4;
-        p.units = p.uq + a.k.heads * 2 * 4;
-    } else {
-        p.units = p.uq + p.uk + (a.v.data ? groups(a.v.heads) * p.ipv : 0);
-    }
-    p.total = a.num_tokens * p.units;
-    p.tokens = (kThreads - 1) / p.units + 2;
-    p.div_units = make_div(p.units);
+    p.ukv = a.q4 ? a.k.heads * 2 * 4 : p.uk + (a.v.data ? groups(a.v.heads) * p.ipv : 0);
+    p.total_q = a.num_tokens * p.uq;
+    p.total_kv = a.num_tokens * p.ukv;
+    const int least = p.uq > 0 && (p.ukv == 0 || p.uq < p.ukv) ? p.uq : p.ukv;
+    p.tokens = (kThreads - 1) / least + 2;
+    p.div_q = make_div(p.uq > 0 ? p.uq : 1);
+    p.div_kv = make_div(p.ukv > 0 ? p.ukv : 1);
     p.div_iph = make_div(p.iph);
     p.div_ipv = make_div(p.ipv);
     p.div_seq = make_div((uint32_t)a.per_seq);
-    const int64_t blocks = (p.total + kThreads - 1) / kThreads;
+    const int64_t qb = (p.total_q + kThreads - 1) / kThreads;
+    const int64_t blocks = qb + (p.total_kv + kThreads - 1) / kThreads;
     if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
+    p.q_blocks = (int)qb;
     const size_t smem = a.pg.table ? sizeof(Token) * p.tokens +
                                          (a.q4 ? sizeof(float) * 2 * p.half * p.tokens : 0)
                                    : 0;

@@ -51,10 +51,10 @@ def rotate(x, pos, f, interleaved=False, m=1.0, inverse=False):
 def rotate_bound(x, y, rot, interleaved, dtype, m=1.0):
     """|error| allowed for y = rotate(x) computed in fp32 and rounded to dtype.
 
-    The phase is cut to 2^-32 of a turn and turned into a float (2^-25 relative
-    of at most pi: 1.6 * 2^-24), sincospif is within 2 ulp (2^-23 at most), the
-    factor, the two products and the sum round once each: below 6 * 2^-24 times
-    (|x| + |x'|); 8 leaves room for the plan's own rounding at far positions."""
+    The phase is cut to 2^-32 of a turn (below 2^-29), sine and cosine are
+    within 2 ulp (2^-23 at most), the factor, the two products and the sum round
+    once each: below 6 * 2^-24 times (|x| + |x'|); 8 leaves room for the plan's
+    own rounding at far positions."""
     x = x.double().cpu().abs()
     s = x.clone()
     if rot:
