@@ -23,7 +23,6 @@
 
 #include "rkv_common.cuh"
 #include "rkv_internal.h"
-#include "rkv_paged.cuh"
 
 namespace rkv {
 namespace {
@@ -304,8 +303,14 @@ template <typename T> constexpr int kHeads = sizeof(T) == 2 ? 4 : 2;
 // VEC: the rotated part splits into whole steps of eight.  A unit is one item
 // (the eight pairs, or eight elements, that a thread holds; without VEC one
 // pair or element) of kHeads heads, or a lane of a 4-bit row.
+// Four blocks an SM where the registers would allow three (28.9 thousand tokens
+// appended: 127 -> 122 us; 16.8 thousand at 4 bits and read back: 105 -> 96 us;
+// five: 103 us); the others are left to the compiler (67.5 us at 16384 x 48 heads, 69.6
+// with a bound of three).
+template <typename T, bool INTER, bool Q4>
+constexpr int kBlocks = Q4 || (sizeof(T) == 2 && !INTER) ? 4 : 0;
 template <typename T, bool VEC, bool INTER, bool Q4, int W>
-__global__ void __launch_bounds__(kThreads) tokens_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) uint8_t smem[];
     Token* tok = reinterpret_cast<Token*>(smem);                          // [tokens]
     float* sines = reinterpret_cast<float*>(smem + sizeof(Token) * p.tokens);  // 4 bits: [tokens][2][half]
@@ -539,24 +544,27 @@ cudaError_t go(Params& p, cudaStream_t s) {
 // A lane's 32 (W = 4) or 16 values of a row; four lanes a row as in the append.
 template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) q4_read_kernel(const __grid_constant__ Q4ReadArgs a,
-                                                           int64_t total, int both) {
+                                                           int64_t total, int both, Div by_rows,
+                                                           Div by_heads) {
     const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (e >= total) return;
     const int t = (int)(e & 3);
-    int64_t r = e >> 2;
-    const int i = (int)(r % a.n_rows);
-    r /= a.n_rows;  // problem (and tensor)
+    uint32_t r = div_by((uint32_t)(e >> 2), by_rows);  // problem (and tensor)
+    const int i = (int)((uint32_t)(e >> 2) - r * (uint32_t)a.n_rows);
     bool is_v = a.out_k == nullptr;
     if (both) {
         is_v = r & 1;
         r >>= 1;
     }
-    const int64_t s = r / a.pg.H;
+    const uint32_t s = div_by(r, by_heads), h = r - s * (uint32_t)a.pg.H;
     const int64_t row = (a.first ? a.first[s] : 0) + (int64_t)i;
     if (row >= a.lens[s]) return;
-    bool ok = row >= 0 && row < ((int64_t)a.pg.max_blocks << a.pg.log2bs);
     int64_t phys = -1;
-    if (ok) phys = paged_phys_row(a.pg, r, (int)row);
+    if (row >= 0 && row < ((int64_t)a.pg.max_blocks << a.pg.log2bs)) {
+        const int blk = a.pg.table[(int64_t)s * a.pg.max_blocks + (row >> a.pg.log2bs)];
+        if ((unsigned)blk < (unsigned)a.pg.num_blocks)
+            phys = (((int64_t)blk * a.pg.H + h) << a.pg.log2bs) | (row & ((1 << a.pg.log2bs) - 1));
+    }
     if (phys < 0) {
         set_error(a.status, kDevErrIndex, (unsigned)s);
         return;
@@ -573,7 +581,7 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const __grid_constant
         half[0][0] = c.x & 0xffffu; half[0][1] = c.x >> 16;
         half[1][0] = c.y & 0xffffu; half[1][1] = c.y >> 16;
     }
-    T* dst = static_cast<T*>(is_v ? a.out_v : a.out_k) + (r * a.n_rows + i) * (W * 32);
+    T* dst = static_cast<T*>(is_v ? a.out_v : a.out_k) + ((int64_t)r * a.n_rows + i) * (W * 32);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         const uint32_t pr = scales[w];
@@ -604,12 +612,13 @@ cudaError_t launch_q4_read(const Q4ReadArgs& a, cudaStream_t s) {
     if (total == 0) return cudaSuccess;
     const int64_t blocks = (total + kThreads - 1) / kThreads;
     const unsigned g = (unsigned)blocks;
+    const Div rows = make_div((uint32_t)a.n_rows), heads = make_div((uint32_t)a.pg.H);
     if (a.dtype == RKV_DTYPE_BF16) {
-        if (a.d == 128) q4_read_kernel<__nv_bfloat16, 4><<<g, kThreads, 0, s>>>(a, total, both);
-        else q4_read_kernel<__nv_bfloat16, 2><<<g, kThreads, 0, s>>>(a, total, both);
+        if (a.d == 128) q4_read_kernel<__nv_bfloat16, 4><<<g, kThreads, 0, s>>>(a, total, both, rows, heads);
+        else q4_read_kernel<__nv_bfloat16, 2><<<g, kThreads, 0, s>>>(a, total, both, rows, heads);
     } else {
-        if (a.d == 128) q4_read_kernel<float, 4><<<g, kThreads, 0, s>>>(a, total, both);
-        else q4_read_kernel<float, 2><<<g, kThreads, 0, s>>>(a, total, both);
+        if (a.d == 128) q4_read_kernel<float, 4><<<g, kThreads, 0, s>>>(a, total, both, rows, heads);
+        else q4_read_kernel<float, 2><<<g, kThreads, 0, s>>>(a, total, both, rows, heads);
     }
     return cudaGetLastError();
 }

@@ -421,7 +421,7 @@ int rkv_q4_read(const rkv_paged_desc* desc, const rkv_q4_cache* cache,
     a.dtype = desc->dtype;
     a.d = desc->head_dim;
     const int64_t rows = desc->num_seqs * (int64_t)desc->num_kv_heads * n_rows;
-    if (rows >= ((int64_t)1 << 35)) return RKV_ERR_INVALID_ARG;
+    if (rows >= ((int64_t)1 << 30)) return RKV_ERR_UNSUPPORTED;
     const int64_t bytes = rows * a.d * elem(a.dtype);
     const Span ks = span_of(out_K, out_K ? bytes : 0), vs = span_of(out_V, out_V ? bytes : 0);
     if (overlap(ks, vs)) return RKV_ERR_ALIAS;
