@@ -6,7 +6,9 @@
 // sequences and KV heads form one line of units (64 or 128 rows), cut into
 // equal runs, one per block, as many blocks as the SMs hold at once: ragged
 // batches are balanced whatever their lengths, and at most two pieces a block
-// are parts of a sequence that attn_combine_kernel joins.  Within a piece every
+// are parts of a sequence that attn_combine_kernel joins.  A few short sequences
+// take a cluster of blocks per problem instead, which join through their shared
+// memory: one launch.  Within a piece every
 // warp is on its own: it takes every fourth stage, copies it into its own ring
 // of shared memory (cp.async through the block table, rows past the sequence
 // filled with zeros), and keeps the maxima, sums and the output of up to 32
@@ -76,6 +78,7 @@ struct Params {
     int4* joins;        // [run][group]: (sequence, head, parts) of the problem to join, if parts
     int H, G, T, R, groups, runs, max_rows;
     uint32_t lead;
+    int cluster;  // blocks of a cluster that share a problem (0: runs of the line)
     int max_blocks, log2bs, num_blocks;
     float scale, slack;  // of base-2 logits, positive; how far they may pass the maximum
     uint32_t flip;       // scale < 0: sign bits for the queries
@@ -611,6 +614,22 @@ RKV_DEV bool next_piece(const Params& p, int unit, uint32_t run, Place& pl, Piec
     return false;
 }
 
+// A cluster's share of its problem: block `rank` of `p.cluster` takes the units
+// from rank * n_s / cluster on (maybe none).
+RKV_DEV void cluster_piece(const Params& p, int unit, int prob, int rank, Piece& c) {
+    c.s = prob / p.H;
+    c.h = prob - c.s * p.H;
+    c.len = rows_of(p, c.s);
+    const int n_s = units_of(c.len, unit);
+    const int j = rank * n_s / p.cluster, e = (rank + 1) * n_s / p.cluster;
+    c.c0 = j * unit;
+    c.c1 = e == j ? c.c0 : (e == n_s ? c.len : e * unit);
+    c.slot = c.parts = 0;
+    c.whole = true;
+    if (threadIdx.x == 0 && rank == 0 && c.h == 0 && c.len != p.lens[c.s])
+        set_error(p.status, kDevErrIndex, (unsigned)c.s);
+}
+
 // What a part with maximum m and sum l counts beside a common maximum mx: an
 // empty part nothing, one whose logits are all NaN its NaN.
 RKV_DEV float weight(float m, float l, float mx, float scale) {
@@ -669,6 +688,98 @@ RKV_DEV void finish(const Params& p, const float* acc, const float (&sh_m)[kWarp
     }
 }
 
+RKV_DEV uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+RKV_DEV void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address of another block's copy of this shared location.
+RKV_DEV uint32_t shared_of(uint32_t at, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
+    return r;
+}
+RKV_DEV float4 remote4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at));
+    return v;
+}
+RKV_DEV float2 remote2(uint32_t at) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+    return v;
+}
+
+// finish() for a cluster's blocks, through their shared memory: each joins its
+// warps, then takes its part of the problem's output over all blocks.  No second
+// launch and no scratch.
+constexpr int kCluster = 8;
+template <typename T, int D, int ROWS>
+RKV_DEV void finish_cluster(const Params& p, float* acc, const float (&sh_m)[kWarps][ROWS],
+                            const float (&sh_l)[kWarps][ROWS], float2 (&sh_ml)[ROWS], int s, int h,
+                            int row_first, uint32_t rank) {
+    const int tid = threadIdx.x;
+    for (int e = tid; e < ROWS * D / 4; e += kWarps * 32) {
+        const int r = e / (D / 4);
+        float4 v = *reinterpret_cast<const float4*>(acc + (size_t)e * 4);
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            const float4 y = *reinterpret_cast<const float4*>(acc + ((size_t)w * ROWS * D + e * 4));
+            v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+        }
+        *reinterpret_cast<float4*>(acc + (size_t)e * 4) = v;
+        if (e - r * (D / 4) == 0) {
+            const float mx = row_max(sh_m, r);
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                sum += sh_l[w][r] * weight(sh_m[w][r], sh_l[w][r], mx, p.scale);
+            sh_ml[r] = make_float2(mx, sum);
+        }
+    }
+    cluster_sync();
+    T* out = reinterpret_cast<T*>(p.out);
+    for (int e = rank * (kWarps * 32) + tid; e < ROWS * D / 4; e += p.cluster * (kWarps * 32)) {
+        const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+        const int row = row_first + r;
+        if (row >= p.R) break;
+        float2 ml[kCluster];
+        float4 x[kCluster];
+#pragma unroll
+        for (int i = 0; i < kCluster; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+            x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < p.cluster) {
+                ml[i] = remote2(shared_of(smem_at(&sh_ml[r]), i));
+                x[i] = remote4(shared_of(smem_at(acc + (size_t)e * 4), i));
+            }
+        }
+        float mx = ml[0].x, sum = 0.f;
+#pragma unroll
+        for (int i = 1; i < kCluster; ++i) mx = fmaxf(mx, ml[i].x);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kCluster; ++i) {
+            const float f = weight(ml[i].x, ml[i].y, mx, p.scale);
+            sum += ml[i].y * f;
+            v.x += x[i].x * f; v.y += x[i].y * f; v.z += x[i].z * f; v.w += x[i].w * f;
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int tk = row / p.G, hd = h * p.G + row - tk * p.G;
+        store4(out + s * p.o_seq + tk * p.o_tok + hd * p.o_head + d,
+               make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+        if (d == 0 && p.lse)
+            p.lse[((int64_t)s * p.T + tk) * p.H * p.G + hd] =
+                sum == 0.f ? -INFINITY : (mx * p.scale + log2f(sum)) * kLn2;
+    }
+    cluster_sync();  // nobody leaves while its shared memory is read
+}
+
 // NT * 8 queries of a KV head's group against a run of rows.
 template <int D, int NT, bool Q4>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kernel(const __grid_constant__ Params p) {
@@ -676,11 +787,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
     constexpr int ROWS = 8 * NT, W = D / 32, KT = S::KEYS / 16, UNIT = kWarps * S::KEYS;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sh_m[kWarps][ROWS], sh_l[kWarps][ROWS];
+    __shared__ __align__(8) float2 sh_ml[ROWS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     // groups of queries over the same rows are neighbours: the rows come from
     // HBM once and from L2 for the others
-    const int group = blockIdx.x % p.groups;
-    const uint32_t run = blockIdx.x / p.groups;
+    const uint32_t rank = cluster_rank();  // 0 where a block is alone
+    const uint32_t job = p.cluster ? blockIdx.x / p.cluster : blockIdx.x;
+    const int group = job % p.groups;
+    const uint32_t run = job / p.groups;  // (a cluster's problem)
     const int row_first = group * ROWS;  // first query row (token * G + head of the group)
     const int mask = (1 << p.log2bs) - 1;
     const uint32_t ring = smem_at(smem) + warp * (S::DEPTH * S::BYTES);
@@ -689,14 +803,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
     [[maybe_unused]] Unpack uk;
     if constexpr (Q4) uk = unpack_constants();
 
-    Place place = find_place<kWarps * 32>(p, UNIT, run);
+    Place place{};
     Piece c{};
-    while (next_piece(p, UNIT, run, place, c)) {
+    if (p.cluster)
+        cluster_piece(p, UNIT, run, rank, c);
+    else
+        place = find_place<kWarps * 32>(p, UNIT, run);
+    while (p.cluster || next_piece(p, UNIT, run, place, c)) {
         const int s = c.s, h = c.h, len = c.len, c0 = c.c0, c1 = c.c1;
 
         const int32_t* table = p.table + (int64_t)s * p.max_blocks;
-        const int stages = (c1 - c0 + S::KEYS - 1) / S::KEYS;
-        const int mine = warp < stages ? (stages - warp + kWarps - 1) / kWarps : 0;
         // the block id of this lane's row of the next stage (-1: no such row); looked at one
         // stage later, when the load has come back
         int look = c0 + warp * S::KEYS + lane;
@@ -990,6 +1106,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                 }
             }
         __syncthreads();
+        if (p.cluster) {
+            finish_cluster<__nv_bfloat16, D, ROWS>(p, acc, sh_m, sh_l, sh_ml, s, h, row_first, rank);
+            return;
+        }
         finish<__nv_bfloat16, D, ROWS>(p, acc, sh_m, sh_l, s, h, row_first,
                                        (int64_t)c.slot * p.groups + group, c.whole);
         __syncthreads();  // the next piece's copies overwrite what was just read
@@ -1287,6 +1407,7 @@ Params params(const AttnArgs& a, const AttnPlan& pl) {
     p.H = a.pg.H; p.G = a.G; p.T = a.n_new; p.R = a.n_new * a.G;
     p.groups = pl.groups; p.runs = pl.runs; p.max_rows = a.max_rows;
     p.lead = pl.lead;
+    p.cluster = pl.cluster;
     p.max_blocks = a.pg.max_blocks; p.log2bs = a.pg.log2bs; p.num_blocks = a.pg.num_blocks;
     // a scale of (almost) nothing counts as one that still orders the logits
     const float x = a.scale * kLog2e, y = x < 0.f ? -x : x;
@@ -1305,8 +1426,18 @@ cudaError_t go(const Params& p, unsigned ctas, cudaStream_t s) {
     auto kern = attn_kernel<D, NT, Q4>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kern<<<ctas, kWarps * 32, bytes, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = p.cluster ? p.cluster : 1;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = p.cluster ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 template <bool Q4>
 cudaError_t go(const Params& p, int d, int rows, unsigned ctas, cudaStream_t s) {
@@ -1329,6 +1460,12 @@ bool is_f32(const AttnArgs& a) { return !a.q4 && a.dtype == RKV_DTYPE_FP32; }
 
 }  // namespace
 
+// Up to how many units a cluster of eight takes a problem.  On the device, us,
+// line and join against cluster (KV heads 8): one sequence of 256 rows 7.3 / 5.1,
+// 1152 8.4 / 7.4, 4096 11.9 / 10.4, 8192 13.9 / 15.0; four of 1152 11.4 / 9.9, of
+// 4096 18.1 / 16.6; at 4 bits one of 1152 9.2 / 7.4, of 4096 10.5 / 9.7.
+constexpr int kClusterUnits = 64;
+
 AttnPlan attn_plan(const AttnArgs& a) {
     AttnPlan pl;
     const int R = a.n_new * a.G;
@@ -1344,7 +1481,14 @@ AttnPlan attn_plan(const AttnArgs& a) {
     // as many blocks as 152 SMs hold at once: shared memory for two (one with
     // fp32 rows of 128), with 4-bit rows registers for three
     const int blocks = 152 * (is_f32(a) && a.d == 128 ? 1 : (a.q4 && pl.rows == 8 ? 3 : 2));
-    const int64_t units = a.num_seqs * a.pg.H * (((int64_t)a.max_rows + pl.unit - 1) / pl.unit);
+    const int64_t per = ((int64_t)a.max_rows + pl.unit - 1) / pl.unit, problems = a.num_seqs * a.pg.H;
+    // a few short sequences: a cluster for each problem, one launch
+    if (!is_f32(a) && per > 1 && per <= kClusterUnits && problems * pl.groups * kCluster <= 304) {
+        pl.cluster = per >= 5 ? 8 : (per >= 3 ? 4 : 2);
+        pl.runs = (int)problems;
+        return pl;
+    }
+    const int64_t units = problems * per;
     // a problem's beginning and end cost about as much as this many units (64
     // ragged sequences of 131 .. 4224 rows, us at 0, 1, 2, 4, 8: bf16 103, 102,
     // 95, 95, 96; 4 bits 64, 60, 56, 58, 62; 8 new tokens, head_dim 64: 72, 70,
@@ -1361,7 +1505,7 @@ AttnPlan attn_plan(const AttnArgs& a) {
 }
 
 cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
-    const unsigned ctas = (unsigned)(pl.runs * pl.groups);
+    const unsigned ctas = (unsigned)(pl.runs * pl.groups * (pl.cluster ? pl.cluster : 1));
     if (ctas == 0) return cudaSuccess;
     const Params p = params(a, pl);
     if (is_f32(a)) return a.d == 128 ? go32<128>(p, ctas, s) : go32<64>(p, ctas, s);

@@ -272,6 +272,7 @@ struct AttnArgs {
 // join: pieces of a sequence may have to be joined by a second launch.
 struct AttnPlan {
     int rows = 8, groups = 1, unit = 64, runs = 0, lead = 0;
+    int cluster = 0;  // blocks that share a problem as a cluster (runs: problems)
     bool join = false;
     size_t partial_floats = 0;
 };

@@ -429,11 +429,17 @@ ATTN_CASES = [
     ([100, 70], 64, 1, 2, 64, 16),
     ([5000], 1, 1, 3, 128, 1024),
     ([4224, 17, 2048], 3, 1, 16, 64, 4),
+    # long enough, or enough sequences, that pieces of them are joined by a second launch
+    ([9001], 4, 1, 4, 64, 16),
+    ([8200, 3], 1, 2, 5, 128, 128),
+    ([(i * 37) % 300 for i in range(45)], 1, 1, 2, 64, 16),
+    ([700, 1, 0, 650] * 10, 2, 1, 16, 128, 32),
+    ([i % 7 * 40 for i in range(300)], 1, 1, 1, 64, 8),
 ]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "q4", "fp32"])
-@pytest.mark.parametrize("case", ATTN_CASES, ids=lambda c: f"{c[0]}-T{c[1]}H{c[2]}G{c[3]}d{c[4]}bs{c[5]}")
+@pytest.mark.parametrize("case", ATTN_CASES, ids=lambda c: f"S{len(c[0])}n{max(c[0])}-T{c[1]}H{c[2]}G{c[3]}d{c[4]}bs{c[5]}")
 def test_attention(case, kind):
     lens, T, H, G, d, bs = case
     S = len(lens)
