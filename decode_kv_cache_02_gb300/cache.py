@@ -18,7 +18,8 @@ import struct
 
 import torch
 
-from .rkv import (RKV_DTYPE_BF16, RKV_DTYPE_FP32, _Q4Cache, _RopeConfig, _RopePlan, _check, load)
+from . import rkv as _rkv
+from .rkv import RKV_DTYPE_BF16, RKV_DTYPE_FP32, _Q4Cache, _RopeConfig, _RopePlan, _check
 
 RKV_MAX_NEW_TOKENS = 64
 _DTYPE = {torch.bfloat16: RKV_DTYPE_BF16, torch.float32: RKV_DTYPE_FP32}
@@ -29,6 +30,10 @@ _pack_desc = struct.Struct("@q7i4x").pack     # rkv_paged_desc
 _pack_q4 = struct.Struct("@4P").pack          # rkv_q4_cache
 _current_device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def load():
+    return _rkv._lib or _rkv.load()  # without the lock once it is there
 
 
 def _elsewhere(fn, t: torch.Tensor, stream, *args, **kw):
@@ -76,19 +81,17 @@ def _dtype(t: torch.Tensor) -> int:
 def _rows(t, name: str, dev: int, heads, d: int, dtype, tokens: int, per_seq: int) -> bytes:
     """The rows of [tokens, heads, d] or [seqs, per_seq, heads, d], strides as
     they are, as an rkv_rows."""
-    sh, st = t.shape, t.stride()
-    if len(sh) == 4:
-        seqs, n, h, e = sh
-        ok = n == per_seq and seqs * n == tokens
-        seq, tok, head, one = st
-    elif len(sh) == 3:
-        n, h, e = sh
-        ok = n == tokens
+    st = t.stride()
+    if len(st) == 3:
         tok, head, one = st
         seq = per_seq * tok
+        ok = t.shape == (tokens, heads, d)
+    elif len(st) == 4:
+        seq, tok, head, one = st
+        ok = t.shape == (tokens // per_seq if per_seq else t.shape[0], per_seq, heads, d)
     else:
-        ok, h, e, one = False, 0, 0, 1
-    if not ok or h != heads or e != d or t.dtype != dtype or one != 1:
+        ok, one = False, 1
+    if not ok or one != 1 or t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype} [{tokens}, {heads}, {d}] or [{tokens // max(per_seq, 1)}, "
                          f"{per_seq}, {heads}, {d}] with a contiguous last dimension")
     if t.get_device() != dev:

@@ -33,6 +33,8 @@
 //
 // The running maximum moves only when a logit passes it by more than 8 (log2):
 // p stays below 2^8 and the rescaling almost never runs.
+#include <atomic>
+
 #include "rkv_common.cuh"
 #include "rkv_internal.h"
 
@@ -1418,13 +1420,28 @@ Params params(const AttnArgs& a, const AttnPlan& pl) {
     return p;
 }
 
+// Dynamic shared memory past 48 KB has to be asked for once per kernel and
+// device (half a microsecond, so not at every call).
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 template <int D, int NT, bool Q4>
 cudaError_t go(const Params& p, unsigned ctas, cudaStream_t s) {
     using S = Stage<D, Q4>;
     constexpr int ring = kWarps * S::DEPTH * S::BYTES, join = kWarps * 8 * NT * D * 4;
     constexpr int bytes = ring > join ? ring : join;
     auto kern = attn_kernel<D, NT, Q4>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kern, bytes, done);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
@@ -1450,7 +1467,8 @@ cudaError_t go32(const Params& p, unsigned ctas, cudaStream_t s) {
     constexpr int bytes = kWarps * Stage32<D>::DEPTH * Stage32<D>::BYTES;
     static_assert(bytes >= kWarps * 8 * D * 4, "the rings hold the join");
     auto kern = attn_f32_kernel<D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kern, bytes, done);
     if (e != cudaSuccess) return e;
     kern<<<ctas, kWarps * 32, bytes, s>>>(p);
     return cudaGetLastError();
