@@ -1537,10 +1537,12 @@ cudaError_t go_join(const Params& p, const AttnPlan& pl, cudaStream_t s) {
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    // most blocks find nothing to join: a few for each run
+    // most blocks find nothing to join.  With about as many problems as runs, or
+    // more, the pieces of one are few and a block's warps take a query each;
+    // otherwise a block takes a query.
     const int blocks = pl.runs * pl.groups, used = p.R < pl.rows ? p.R : pl.rows;
-    const int most = 2048 / blocks, least = (used + kJoinWarps - 1) / kJoinWarps;
-    const int y = most < least ? least : (most < used ? most : used);
+    const bool few = (int64_t)p.num_seqs * p.H * 8 >= pl.runs;
+    const int y = few ? (used + kJoinWarps - 1) / kJoinWarps : used;
     cfg.gridDim = dim3((unsigned)blocks, (unsigned)y);
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = s;
