@@ -79,6 +79,21 @@ int check_rows(const rkv_rows* r, int dtype, int d, int64_t heads, int64_t seqs,
     return RKV_OK;
 }
 
+// Whether rows a (written in place) stay clear of rows b of the same tokens:
+// memory apart, or two slices of the rows of one projection.
+bool apart(const RowsView& a, const Span& as, const RowsView& b, const Span& bs, int dtype, int d,
+           int64_t seqs, int64_t per_seq) {
+    if (!overlap(as, bs)) return true;
+    if (a.tok != b.tok || a.seq != b.seq) return false;
+    const int64_t es = elem(dtype);
+    const int64_t wa = (int64_t)(a.heads - 1) * a.head + d, wb = (int64_t)(b.heads - 1) * b.head + d;
+    const bool first = as.lo <= bs.lo;
+    const int64_t off = (int64_t)(first ? bs.lo - as.lo : as.lo - bs.lo) / es;
+    const int64_t step = per_seq > 1 ? a.tok : (seqs > 1 ? a.seq : 0);
+    // side by side within a token's row, the next token behind both
+    return off >= (first ? wa : wb) && (step == 0 || off + (first ? wb : wa) <= step);
+}
+
 bool same_rows(const RowsView& a, const RowsView& b) {
     return a.data == b.data && a.seq == b.seq && a.tok == b.tok && a.head == b.head;
 }
@@ -146,11 +161,16 @@ int check_append(const rkv_paged_desc* desc, const rkv_rope_plan* rope, const in
             return rc;
         if ((rc = check_rows(out_q, a->dtype, a->d, Hq, seqs, a->per_seq, true, &a->out_q, out_span)))
             return rc;
-        // rows of fused projections interleave in memory: spans of q, k and v
-        // may meet, an output may only be q itself or lie apart from the inputs
-        if (!same_rows(a->q, a->out_q) &&
-            (overlap(*out_span, in[0]) || overlap(*out_span, in[1]) || overlap(*out_span, in[2])))
+        // out_q is q itself, beside the k and v of a fused projection, or memory
+        // of its own
+        if (same_rows(a->q, a->out_q)) {
+            if (!apart(a->q, in[2], a->k, in[0], a->dtype, a->d, seqs, a->per_seq) ||
+                !apart(a->q, in[2], a->v, in[1], a->dtype, a->d, seqs, a->per_seq))
+                return RKV_ERR_ALIAS;
+        } else if (overlap(*out_span, in[0]) || overlap(*out_span, in[1]) ||
+                   overlap(*out_span, in[2])) {
             return RKV_ERR_ALIAS;
+        }
     } else if (out_q) {
         return RKV_ERR_INVALID_ARG;
     }
@@ -186,7 +206,7 @@ int check_attention(const rkv_paged_desc* desc, const int32_t* table, int n_new,
     if (n_new < 1 || max_rows < 1 ||
         (int64_t)max_rows > (int64_t)desc->max_blocks_per_seq * desc->block_size)
         return RKV_ERR_INVALID_ARG;
-    if (n_new > RKV_MAX_NEW_TOKENS || (int64_t)desc->num_kv_heads * desc->gqa_group > kMaxHeads ||
+    if (n_new > RKV_MAX_NEW_TOKENS || max_rows > (1 << 30) || (int64_t)desc->num_kv_heads * desc->gqa_group > kMaxHeads ||
         (q4 && desc->dtype != RKV_DTYPE_BF16))
         return RKV_ERR_UNSUPPORTED;
     a->dtype = desc->dtype;
@@ -356,12 +376,13 @@ int rkv_rope_apply(const rkv_rope_plan* plan, int dtype, int head_dim, int64_t n
                              &out[1])))
             return rc;
         const bool k_in = same_rows(a.k, a.out_k);
-        // q and k in place are two slices of a projection; an output of its
-        // own lies apart from everything else
+        // rows in place may be slices of one projection; an output of its own
+        // lies apart from everything else
         if (!k_in && (overlap(in[1], out[1]) || overlap(in[0], out[1]) || overlap(out[0], out[1])))
             return RKV_ERR_ALIAS;
         if (!q_in && (overlap(in[1], out[0]) || overlap(out[0], out[1]))) return RKV_ERR_ALIAS;
-        if (q_in && k_in && a.q.data == a.k.data) return RKV_ERR_ALIAS;
+        if ((q_in || k_in) && !apart(a.q, in[0], a.k, in[1], dtype, head_dim, seqs, tokens_per_seq))
+            return RKV_ERR_ALIAS;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return rc_of(rkv::timed_cache(rkv::kCacheRope, s, run_tokens, &a));

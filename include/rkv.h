@@ -374,7 +374,8 @@ int rkv_rope_init_freqs(int rot_dim, int interleaved, const double* freqs, doubl
  * by the opposite angles, which is the gradient's map (the transpose).
  * num_tokens tokens, tokens_per_seq of them (a divisor of num_tokens) per
  * sequence for seq_stride.  An output may be its input (same pointer and
- * strides); other overlaps are RKV_ERR_ALIAS.  fp32 arithmetic, one rounding. */
+ * strides), where q and k may be slices of one projection's rows; other
+ * overlaps are RKV_ERR_ALIAS.  fp32 arithmetic, one rounding. */
 int rkv_rope_apply(const rkv_rope_plan* plan, int dtype, int head_dim, int64_t num_tokens,
                    int64_t tokens_per_seq, const int32_t* positions, int inverse, int q_heads,
                    const rkv_rows* q, const rkv_rows* out_q, int k_heads, const rkv_rows* k,
@@ -388,7 +389,8 @@ int rkv_rope_apply(const rkv_rope_plan* plan, int dtype, int head_dim, int64_t n
  * it (padding) nothing is written.  k and v have num_kv_heads heads.
  * With a rope, k is turned by positions (NULL: by the rows it is written to);
  * q (num_kv_heads * gqa_group heads; may be NULL) is turned the same way, or
- * copied without a rope, into out_q (which may be q).  Rows outside the table
+ * copied without a rope, into out_q (which may be q, beside k and v of one
+ * projection).  Rows outside the table
  * and ids that name no block are recorded as a device error in `workspace`
  * (NULL: not recorded; else 256-byte aligned, only its error word is used)
  * and not written.  Two tokens of a call must not share a row of the pool.
@@ -441,8 +443,9 @@ int rkv_q4_read(const rkv_paged_desc* desc, const rkv_q4_cache* cache,
  * with query heads h * gqa_group .. of KV head h.  A token that sees no row
  * (lens[s] < n_new, or 0) gets zeros.  lse, unless NULL, receives
  * log(sum_j exp(scale * q . K_j)) [num_seqs, n_new, heads] fp32 (-inf where
- * nothing is seen).  Rows at or past lens[s] may hold anything.  max_rows (1
- * .. the table's rows) bounds lens; a larger lens[s] is recorded as a device
+ * nothing is seen).  Rows at or past lens[s] may hold anything, and what a row
+ * holds that only the later of the new tokens see stays out of the earlier
+ * ones.  max_rows (1 .. the table's rows, at most 2^30) bounds lens; a larger lens[s] is recorded as a device
  * error and cut to it, a negative one likewise to 0, and rows whose id names
  * no block are recorded and skipped.  Sums, the softmax's statistics and the
  * output before its one rounding are fp32; bf16 and 4-bit caches round the

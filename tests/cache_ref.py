@@ -147,6 +147,7 @@ def attention_bounds(out, lse, A, L, scale, d, rows, kind, extra=0.0, extra_v=0.
     A (`extra_v`: what the offsets add there); accumulation in fp32 over a
     warp's share of the rows and the join (rows / 4 + 64) 2^-24 A; the output's
     rounding 2^-8 |out| (bf16)."""
+    scale = abs(scale)
     delta = (L * (d + 4) * U32 + extra) * scale + (lse.abs().nan_to_num(0, 0, 0) + 8) * 4 * U32
     b = (2 * delta[..., None] + (rows / 4 + 64) * U32) * A + extra_v + 1e-30
     if kind != "fp32":

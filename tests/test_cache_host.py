@@ -110,6 +110,11 @@ def test_rope_apply_refusals(lib):
     assert call(oq=_rows(128)) == 4                          # output runs into the input
     assert call(ok=_rows(GB + 4096)) == 4                    # the two outputs meet
     assert call(k=_rows(), ok=_rows(), oq=_rows(), q=_rows()) == 4  # one tensor as both, in place
+    # in place, rows of a projection: k beginning inside q's heads, or running into the next token
+    into = lambda off, tok=6144: dict(q=_rows(tok=tok), oq=_rows(tok=tok), k=_rows(off, tok=tok), ok=_rows(off, tok=tok))  # noqa: E731
+    assert call(**into(2 * 31 * 128)) == 4
+    assert call(**into(2 * 32 * 128, tok=4096 + 512)) == 4
+    assert call(n=0, **into(2 * 32 * 128)) == 0
 
 
 def test_append_refusals(lib):
@@ -143,6 +148,7 @@ def test_append_refusals(lib):
         assert call(fn, ws=BASE + 16) == 3
         assert call(fn, rope=cache.RopePlan(128)._packed, desc=_pdesc(d=64)) == 1
         assert call(fn, oq=_rows(2 * GB + 256)) == 4                # out_q runs into q
+        assert call(fn, q=_rows(), oq=_rows(), k=_rows(2 * 128)) == 4  # q in place over k
         assert call(fn, k=_rows(10 * GB)) == 4                      # input inside the pool
         assert call(fn, oq=_rows(12 * GB)) == 4                     # output inside the pool
     assert call(K=None) == 1 and call(K=BASE + 8) == 1

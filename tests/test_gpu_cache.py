@@ -463,6 +463,17 @@ def test_attention(case, kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "q4", "fp32"])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-6, 3.0])
+def test_attention_scales(kind, scale):
+    """Negative scales turn the order of the logits, zero makes a mean."""
+    lens, T, H, G, d, bs = [300, 77], 2, 2, 3, 64, 16
+    cache, table, rows = make_cache(2, H, d, bs, lens, kind, 15)
+    q = rnd((2, T, H * G, d), FP if kind == "fp32" else BF, 3, scale=2.0)
+    out, lse = attend(kind, q, cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), scale=scale, lse=True)
+    check_attention(kind, q, out, lse, rows, lens, scale, cache)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q4", "fp32"])
 def test_attention_keeps_hidden_rows_out(kind):
     """A NaN or an infinity in a row that only the later of the new tokens see
     does not reach the earlier ones."""
@@ -658,10 +669,11 @@ def test_compress_into_four_bits():
     assert torch.isfinite(I).all() and torch.isinf(Z[:, -8:]).all()
 
 
-def test_streams_graphs_and_two_calls_at_once():
+@pytest.mark.parametrize("S", [3, 45])  # in one launch, and with pieces that a second one joins
+def test_streams_graphs_and_two_calls_at_once(S):
     """Calls on a stream of their own, captured and replayed on new values,
     and two calls at once with a workspace each."""
-    S, H, G, d, bs, n = 3, 2, 4, 128, 16, 400
+    H, G, d, bs, n = 2, 4, 128, 16, 400
     cache, table, rows = make_cache(S, H, d, bs, [n] * S, "bf16", 3, junk=False)
     K, V = cache
     plan = pkg.RopePlan(d)
