@@ -24,15 +24,19 @@
 // keys a step and the probabilities through tensor memory, between warps; at 8
 // to 32 queries a row the tensor pipe is under a tenth busy as it is.)
 //
-// 4 bits: codes become bf16 128 + c by placing the four bits in the mantissa
-// (one shift, one logic op for two), exactly.  A group's scale is applied to
-// its own accumulator (K) or to the probabilities (V), in fp32.  The constant
-// 128 and the group's low value enter through one more product each: (scale,
-// low) as stored against (-128, 1) times the queries' sums over the group,
-// those in three bf16 parts (K); low and scale against the probabilities (V).
+// 4 bits: codes become numbers by placing their bits in a mantissa, exactly: K
+// bf16 128 + c (a shift and a logic op for two), V fp16 c - 8 (half a shift, a
+// logic op and an FMA).  A group's scale is applied to its own accumulator (K)
+// or to the probabilities (V), in fp32.  K's constant 128 and the groups' low
+// values enter through one more product each: (scale, low) as stored against
+// (-128, 1) times the queries' sums over the group, those in three bf16 parts
+// (K); low and scale against the probabilities (V).  So the products are exact
+// up to the rounding of p * scale to fp16 and, for the lows, of p to bf16.
 //
 // The running maximum moves only when a logit passes it by more than 8 (log2):
 // p stays below 2^8 and the rescaling almost never runs.
+#include <cuda_fp16.h>
+
 #include <atomic>
 
 #include "rkv_common.cuh"
@@ -138,6 +142,17 @@ RKV_DEV void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+RKV_DEV void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                     uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+RKV_DEV uint32_t pack_f16(float lo, float hi) {
+    const __half2 b = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
 RKV_DEV uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -155,30 +170,45 @@ RKV_DEV float ex2(float x) {
 // The constants of the unpacking, held in registers: an instruction takes one
 // immediate, and each of these steps wants two.
 struct Unpack {
-    uint32_t mask, magic, centre;
+    uint32_t mask, magic;                    // K: bf16
+    uint32_t even, odd, half, less, sixteenth, less16;  // V: fp16
 };
 RKV_DEV Unpack unpack_constants() {
     Unpack k;
     asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(k.mask));
-    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(k.magic));   // 128, 128
-    asm volatile("mov.b32 %0, 0xc308c308;" : "=r"(k.centre));  // -136, -136
+    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(k.magic));      // bf16 128, 128
+    asm volatile("mov.b32 %0, 0x00f000f0;" : "=r"(k.odd));
+    asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k.half));       // fp16 1024, 1024
+    asm volatile("mov.b32 %0, 0xe408e408;" : "=r"(k.less));       // -1032, -1032
+    asm volatile("mov.b32 %0, 0x2c002c00;" : "=r"(k.sixteenth));  // 1/16, 1/16
+    asm volatile("mov.b32 %0, 0xd480d480;" : "=r"(k.less16));     // -72, -72
+    k.even = k.mask;
     return k;
+}
+RKV_DEV uint32_t and_or(uint32_t x, uint32_t mask, uint32_t magic) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(mask), "r"(magic));
+    return y;
 }
 // Codes i and i + 4 (i: the word's nibbles shifted down) as bf16 128 + c.
 RKV_DEV uint32_t codes_at(const Unpack& k, uint32_t w, int i) {
-    uint32_t x;
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w >> (4 * i)), "r"(k.mask), "r"(k.magic));
-    return x;
+    return and_or(w >> (4 * i), k.mask, k.magic);
 }
-// The same less 136: -8 .. 7, exactly.  The values' product wants codes around
-// zero: the rounding of p * scale is then that of the value itself, and long
-// sums do not carry a constant that the tensor core's accumulator would cut
-// digits for.
-RKV_DEV uint32_t centred_at(const Unpack& k, uint32_t w, int i) {
-    const uint32_t x = codes_at(k, w, i);
-    const __nv_bfloat162 y = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&x),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&k.centre));
-    return *reinterpret_cast<const uint32_t*>(&y);
+RKV_DEV __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+// Codes i and i + 4 less 8 as fp16, exactly: 1024 + c, or, four bits higher,
+// 1024 + 16 c, so that a word takes one shift.  The values' product wants codes
+// around zero (long sums carry no constant that the tensor core's accumulator
+// would cut digits for) and fp16 for the probabilities' eleven bits.
+RKV_DEV void centred(const Unpack& k, uint32_t w, uint32_t (&c)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t x = i ? w >> 8 : w;
+        const __half2 lo = __hadd2(as_half2(and_or(x, k.even, k.half)), as_half2(k.less));
+        const __half2 hi = __hfma2(as_half2(and_or(x, k.odd, k.half)), as_half2(k.sixteenth),
+                                   as_half2(k.less16));
+        c[2 * i] = *reinterpret_cast<const uint32_t*>(&lo);
+        c[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+    }
 }
 
 // Physical row (within 16) of row r of a key fragment.  Quarter-warp reads of
@@ -371,6 +401,20 @@ RKV_DEV void values_bf16(uint32_t st, int base, const uint32_t (&pb)[NT][2], uin
     }
 }
 
+// The largest scale of row r of a 4-bit stage's V: its bf16 bits without sign.
+template <int D>
+RKV_DEV uint32_t top_scale(uint32_t st, int r) {
+    using S = Stage<D, true>;
+    const uint32_t row = st + S::vs() + r * S::SROW;
+    if constexpr (S::W == 4) {
+        const uint4 x = lds16(row);
+        return max(max(x.x & 0x7fffu, x.y & 0x7fffu), max(x.z & 0x7fffu, x.w & 0x7fffu));
+    } else {
+        const uint2 x = lds8(row);
+        return max(x.x & 0x7fffu, x.y & 0x7fffu);
+    }
+}
+
 // Whether row r of a stage holds an infinity or a NaN in V (4 bits: in its
 // scales).
 template <int D, bool Q4>
@@ -430,11 +474,8 @@ RKV_DEV void values_q4(const Unpack& uk, uint32_t st, int base, const float (&p)
         const uint32_t u = __byte_perm(x[0][w >> 1], x[1][w >> 1], sel);
         const uint32_t v = __byte_perm(x[2][w >> 1], x[3][w >> 1], sel);
         uint32_t a[4], b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = centred_at(uk, u, i);
-            b[i] = centred_at(uk, v, i);
-        }
+        centred(uk, u, a);
+        centred(uk, v, b);
         const float s[2] = {__uint_as_float(sc[0][w] << 16), __uint_as_float(sc[1][w] << 16)};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -444,9 +485,10 @@ RKV_DEV void values_q4(const Unpack& uk, uint32_t st, int base, const float (&p)
                 y[i] = p[n][i] * s[i >> 1];
                 if (MASKED && p[n][i] == 0.f) y[i] = 0.f;
             }
-            const uint32_t b0 = transpose8x8(pack(y[0], y[1])), b1 = transpose8x8(pack(y[2], y[3]));
-            mma(o[2 * w][n], a[0], a[1], b[0], b[1], b0, b1);
-            mma(o[2 * w + 1][n], a[2], a[3], b[2], b[3], b0, b1);
+            const uint32_t b0 = transpose8x8(pack_f16(y[0], y[1]));
+            const uint32_t b1 = transpose8x8(pack_f16(y[2], y[3]));
+            mma_f16(o[2 * w][n], a[0], a[1], b[0], b[1], b0, b1);
+            mma_f16(o[2 * w + 1][n], a[2], a[3], b[2], b[3], b0, b1);
         }
     }
 }
@@ -632,11 +674,11 @@ RKV_DEV void cluster_piece(const Params& p, int unit, int prob, int rank, Piece&
         set_error(p.status, kDevErrIndex, (unsigned)c.s);
 }
 
-// What a part with maximum m and sum l counts beside a common maximum mx: an
+// What a part with sums relative to 2^m counts beside a common reference mx: an
 // empty part nothing, one whose logits are all NaN its NaN.
-RKV_DEV float weight(float m, float l, float mx, float scale) {
+RKV_DEV float weight(float m, float l, float mx) {
     if (m == -INFINITY) return l != l ? 1.f : 0.f;
-    return ex2((m - mx) * scale);
+    return ex2(m - mx);
 }
 template <int ROWS>
 RKV_DEV float row_max(const float (&sh_m)[kWarps][ROWS], int r) {
@@ -667,7 +709,7 @@ RKV_DEV void finish(const Params& p, const float* acc, const float (&sh_m)[kWarp
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            sum += sh_l[w][r] * weight(sh_m[w][r], sh_l[w][r], mx, p.scale);
+            sum += sh_l[w][r] * weight(sh_m[w][r], sh_l[w][r], mx);
             const float4 y = *reinterpret_cast<const float4*>(acc + ((size_t)w * ROWS + r) * D + d);
             v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
         }
@@ -678,7 +720,7 @@ RKV_DEV void finish(const Params& p, const float* acc, const float (&sh_m)[kWarp
                    make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
             if (d == 0 && p.lse)
                 p.lse[(s * p.T + tk) * (int64_t)p.H * p.G + hd] =
-                    sum == 0.f ? -INFINITY : (mx * p.scale + log2f(sum)) * kLn2;
+                    sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
         } else {
             *reinterpret_cast<float4*>(p.partial + (slot * ROWS + r) * D + d) = v;
             if (d == 0) {
@@ -740,7 +782,7 @@ RKV_DEV void finish_cluster(const Params& p, float* acc, const float (&sh_m)[kWa
             float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
-                sum += sh_l[w][r] * weight(sh_m[w][r], sh_l[w][r], mx, p.scale);
+                sum += sh_l[w][r] * weight(sh_m[w][r], sh_l[w][r], mx);
             sh_ml[r] = make_float2(mx, sum);
         }
     }
@@ -767,7 +809,7 @@ RKV_DEV void finish_cluster(const Params& p, float* acc, const float (&sh_m)[kWa
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kCluster; ++i) {
-            const float f = weight(ml[i].x, ml[i].y, mx, p.scale);
+            const float f = weight(ml[i].x, ml[i].y, mx);
             sum += ml[i].y * f;
             v.x += x[i].x * f; v.y += x[i].y * f; v.z += x[i].z * f; v.w += x[i].w * f;
         }
@@ -777,7 +819,7 @@ RKV_DEV void finish_cluster(const Params& p, float* acc, const float (&sh_m)[kWa
                make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
         if (d == 0 && p.lse)
             p.lse[((int64_t)s * p.T + tk) * p.H * p.G + hd] =
-                sum == 0.f ? -INFINITY : (mx * p.scale + log2f(sum)) * kLn2;
+                sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
     }
     cluster_sync();  // nobody leaves while its shared memory is read
 }
@@ -906,9 +948,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
             }
         const int all_see = len - p.T + row_first / p.G;  // rows up to this one are seen by all
 
-        // m: running maximum of q . k; ref: m * scale (0 while there is none)
+        // m: running maximum of q . k; sums are relative to 2^ref: m * scale (0 while there is
+        // none).  4 bits: and to 2^(bound - 7), V's scales so far being below 2^bound, so that p *
+        // scale stays below 2^15 in fp16 and keeps eleven bits down to 2^-29 of that.
         float m[NT][2], ref[NT][2], l[NT][2], o[D / 16][NT][4];
         [[maybe_unused]] float low[NT][4];
+        [[maybe_unused]] int bound = -60;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -966,7 +1011,19 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                         top[n][i] = fmaxf(top[n][i], fmaxf(x[kt][n][i], x[kt][n][i + 2]));
                     grow |= top[n][i] > m[n][i] + p.slack;
                 }
+            [[maybe_unused]] uint32_t most = 0;
+            if constexpr (Q4) {
+                most = top_scale<D>(st, lane);
+                grow |= (int)most >= ((bound + 127) << 7);
+            }
             if (__any_sync(0xffffffffu, grow)) {
+                if constexpr (Q4) {
+                    // (a scale that is not finite makes its own group's output NaN, no more)
+                    int e = most >= 0x7f80u ? 0 : (int)(most >> 7);
+#pragma unroll
+                    for (int sh = 1; sh <= 16; sh <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, sh));
+                    bound = max(bound, min(e - 126, 100));
+                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -975,9 +1032,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float f = m[n][i] == -INFINITY ? 0.f : ex2((m[n][i] - mx) * p.scale);
+                        const float base =
+                            mx == -INFINITY ? 0.f : mx * p.scale + (Q4 ? (float)(bound - 7) : 0.f);
+                        const float f = m[n][i] == -INFINITY ? 0.f : ex2(ref[n][i] - base);
                         m[n][i] = mx;
-                        ref[n][i] = mx == -INFINITY ? 0.f : mx * p.scale;
+                        ref[n][i] = base;
                         l[n][i] *= f;
 #pragma unroll
                         for (int e = 0; e < D / 16; ++e) {
@@ -1074,6 +1133,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
 #pragma unroll
                 for (int sh = 4; sh <= 16; sh <<= 1)
                     l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], sh);
+                m[n][i] = m[n][i] == -INFINITY ? m[n][i] : ref[n][i];  // from here on: base-2 logits
                 if (g == 0) {
                     sh_m[warp][8 * n + 2 * t + i] = m[n][i];
                     sh_l[warp][8 * n + 2 * t + i] = l[n][i];
@@ -1086,7 +1146,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = 8 * n + 2 * t + i;
-                const float f = weight(m[n][i], l[n][i], row_max(sh_m, r), p.scale);
+                const float f = weight(m[n][i], l[n][i], row_max(sh_m, r));
                 float* dst = acc + ((size_t)warp * ROWS + r) * D;
                 [[maybe_unused]] float add[W];
                 if constexpr (Q4)
@@ -1277,6 +1337,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             l[r] = warp_sum(l[r]);
+            m[r] = m[r] == -INFINITY ? m[r] : ref[r];  // from here on: base-2 logits
             if (lane == 0) {
                 sh_m[warp][r] = m[r];
                 sh_l[warp][r] = l[r];
@@ -1289,7 +1350,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
         float* acc = reinterpret_cast<float*>(smem);
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            const float f = weight(m[r], l[r], row_max(sh_m, r), p.scale);
+            const float f = weight(m[r], l[r], row_max(sh_m, r));
             if (lane < UPR)
                 *reinterpret_cast<float4*>(acc + ((size_t)warp * ROWS + r) * D + 4 * lane) =
                     make_float4(o[r][0] * f, o[r][1] * f, o[r][2] * f, o[r][3] * f);
@@ -1335,7 +1396,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (lane < LANES) x = *reinterpret_cast<const float4*>(p.partial + at * D + lane * 4);
             const float mx = fmaxf(m, ml.x);
-            const float f = weight(m, l, mx, p.scale), g = weight(ml.x, ml.y, mx, p.scale);
+            const float f = weight(m, l, mx), g = weight(ml.x, ml.y, mx);
             m = mx;
             l = l * f + ml.y * g;
             v = make_float4(v.x * f + x.x * g, v.y * f + x.y * g, v.z * f + x.z * g,
@@ -1351,7 +1412,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
                    make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
         if (lane == 0 && p.lse)
             p.lse[((int64_t)s * p.T + tk) * p.H * p.G + hd] =
-                l == 0.f ? -INFINITY : (m * p.scale + log2f(l)) * kLn2;
+                l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     };
     float m, l;
     float4 v;
@@ -1379,7 +1440,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
         v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kJoinWarps; ++w) {
-            const float f = weight(sh_m[w], sh_l[w], m, p.scale);
+            const float f = weight(sh_m[w], sh_l[w], m);
             const float4 x = sh_v[w][lane];
             v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
             l += sh_l[w] * f;

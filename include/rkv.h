@@ -448,8 +448,9 @@ int rkv_q4_read(const rkv_paged_desc* desc, const rkv_q4_cache* cache,
  * ones.  max_rows (1 .. the table's rows, at most 2^30) bounds lens; a larger lens[s] is recorded as a device
  * error and cut to it, a negative one likewise to 0, and rows whose id names
  * no block are recorded and skipped.  Sums, the softmax's statistics and the
- * output before its one rounding are fp32; bf16 and 4-bit caches round the
- * probabilities to bf16 for the second product.
+ * output before its one rounding are fp32; for the second product a bf16 cache
+ * rounds the probabilities to bf16, a 4-bit one probability times scale to
+ * fp16 (scales from 2^-80 to 2^100 at full accuracy).
  * q, out: rkv_rows by sequence and token (bf16 for 4-bit caches). */
 #define RKV_MAX_NEW_TOKENS 64
 size_t rkv_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int max_rows);

@@ -527,6 +527,36 @@ def test_attention_extreme_logits(kind):
         assert ((out.double().cpu() - e).abs() <= tol).all()
 
 
+def test_q4_attention_of_any_magnitude():
+    """V's scales far from 1 (a power of two on all of V turns up in the output)
+    and growing along the row (rows 2^60 smaller than others count as they
+    should)."""
+    lens, H, G, d, bs = [500, 37], 1, 3, 128, 16
+    cache, table, rows = make_cache(2, H, d, bs, lens, "q4", 25, junk=False)
+    q = rnd((2, 1, H * G, d), BF, 3)
+    lens_d = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    keep = cache.V_scales.clone()
+    for k in (-60, -20, 33, 90):
+        # (not bit for bit: the reference of the sums moves with the scales, and so do the
+        # roundings of its exponentials)
+        cache.V_scales.copy_(keep * 2.0 ** k)
+        out, lse = attend("q4", q, cache, table, lens_d, lse=True)
+        check_attention("q4", q, out, lse, [rows[0], [x * 2.0 ** k for x in rows[1]]], lens, 1 / math.sqrt(d), cache)
+    # the first rows tiny, the last large: the running bound moves, and the tiny ones still
+    # give their part of the sum of probabilities
+    grow = torch.ones(keep.shape[0], bs, dtype=torch.float64)
+    for s in range(2):
+        for r in range(lens[s]):
+            grow[int(table[s, r // bs]), r % bs] = 2.0 ** (r % 7 * 10 - 60 + (60 if r > lens[s] // 2 else 0))
+    cache.V_scales.copy_((keep.double().cpu() * grow[:, None, :, None, None]).to(BF).to(DEV))
+    vv = ref.values(cache.V_codes, cache.V_scales)
+    nb = -(-max(lens) // bs)
+    rows[1] = [vv[table[s, :nb].long().cpu().clamp(0, vv.shape[0] - 1)].transpose(0, 1).reshape(H, nb * bs, d)[:, :lens[s]]
+               for s in range(2)]
+    out, lse = attend("q4", q, cache, table, lens_d, lse=True)
+    check_attention("q4", q, out, lse, rows, lens, 1 / math.sqrt(d), cache)
+
+
 def test_attention_bad_blocks_and_lens():
     """Ids that name no block: recorded, their rows skipped.  lens past
     max_rows is recorded and cut, a negative one counts as none."""
