@@ -35,6 +35,13 @@
 //
 // The running maximum moves only when a logit passes it by more than 8 (log2):
 // p stays below 2^8 and the rescaling almost never runs.
+//
+// Measured (one GB300, KV heads 8): 64 ragged sequences to 4224 rows, G = 5,
+// head_dim 128: 94 us, 6.1 TB/s (copies alone 90); 256 of 1152, G = 4: 185 us,
+// 6.5 TB/s; 16 ragged to 16389 with 8 new tokens, head_dim 64: 61 us, 5.0 TB/s
+// (copies alone 55); one of 1152: 6.9 us.  4 bits: one of 131071, G = 5: 49 us,
+// 3.4 TB/s, about 400 instructions a warp for 16 rows at 0.55 a cycle of an SM
+// quarter (copies alone 39, no copies 45).
 #include <cuda_fp16.h>
 
 #include <atomic>
