@@ -53,9 +53,16 @@ struct Params {
     int iph, ipv;      // items of a rotated head, of a copied head
     int uq, uk, ukv;   // a token's units: those of q, of k, of k and v
     int tokens;        // tokens a block may meet
-    int q_blocks;      // the first blocks take the q of all tokens, the others k and v
+    // Blocks take the q of some tokens, or k and v.  In an append, of `period`
+    // blocks in a row the last is one of the `minor` rarer kind (q where minor_q),
+    // while there are any, so that both kinds are on an SM at a time: q streams
+    // while the blocks of k and v wait for their rows' places (28.9 thousand
+    // tokens 118 -> 110 us, 16.8 thousand at 4 bits 95 -> 86 us).  Where nothing
+    // waits, q_blocks of q come first (rotation alone: 64.4 us against 65.5).
+    uint32_t minor, q_blocks;
+    int minor_q;
     int64_t total_q, total_kv;
-    Div div_q, div_kv, div_iph, div_ipv, div_seq;
+    Div div_q, div_kv, div_iph, div_ipv, div_seq, period;
 };
 
 // What a block knows of each of its tokens.
@@ -133,9 +140,18 @@ RKV_DEV void sine_of(uint32_t turn, float& c, float& s) {
     c = __uint_as_float(__float_as_uint(swap ? u : v) ^ cs);
     s = __uint_as_float(__float_as_uint(swap ? v : u) ^ sn);
 }
+// The plan's turns in shared memory (lanes ask for different pairs, which
+// constant memory would serve one after another), so that neighbouring lanes'
+// first, second, .. pairs lie side by side: PAIRS pairs a lane.
+constexpr int kTurns = RKV_MAX_ROT_DIM / 2;
+template <int PAIRS>
+RKV_DEV int turn_slot(int i) {
+    return (i % PAIRS) * (kTurns / PAIRS) + i / PAIRS;
+}
 // (cos, sin) times the factor of pair i at a position.
-RKV_DEV void turn_of(const TokenArgs& a, int pos, int i, float& c, float& s) {
-    const uint64_t turn = (uint64_t)(int64_t)pos * a.turns[i];
+template <int PAIRS>
+RKV_DEV void turn_of(const TokenArgs& a, const uint64_t* turns, int pos, int i, float& c, float& s) {
+    const uint64_t turn = (uint64_t)(int64_t)pos * turns[turn_slot<PAIRS>(i)];
     sine_of((uint32_t)(turn >> 32), c, s);
     c *= a.factor;
     s *= a.inverse ? -a.factor : a.factor;
@@ -319,12 +335,23 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
     extern __shared__ __align__(16) uint8_t smem[];
     Token* tok = reinterpret_cast<Token*>(smem);                          // [tokens]
     float* sines = reinterpret_cast<float*>(smem + sizeof(Token) * p.tokens);  // 4 bits: [tokens][2][half]
-    constexpr int HG = kHeads<T>;
+    __shared__ uint64_t turns[kTurns];
+    constexpr int HG = kHeads<T>, PAIRS = VEC ? (INTER ? 4 : 8) : 1;
     const TokenArgs& a = p.a;
     const int tid = threadIdx.x;
     const bool append = a.pg.table != nullptr;
-    const bool is_q = blockIdx.x < (unsigned)p.q_blocks;
-    const int64_t id0 = (int64_t)(blockIdx.x - (is_q ? 0 : p.q_blocks)) * kThreads;
+    bool is_q;
+    uint32_t block;  // of its kind
+    if (append) {
+        const uint32_t turn = div_by(blockIdx.x, p.period);
+        const bool rare = turn < p.minor && blockIdx.x - turn * p.period.d == p.period.d - 1;
+        is_q = rare == (p.minor_q != 0);
+        block = rare ? turn : blockIdx.x - min(turn, p.minor);
+    } else {
+        is_q = blockIdx.x < p.q_blocks;
+        block = blockIdx.x - (is_q ? 0 : p.q_blocks);
+    }
+    const int64_t id0 = (int64_t)block * kThreads;
     const int units = is_q ? p.uq : p.ukv;
     const int64_t total = is_q ? p.total_q : p.total_kv;
     const int64_t j0 = id0 / units;
@@ -387,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
             for (int w = 0; w < W; ++w) row4[w].load(from + 32 * w + 8 * (unit & 3));
     }
 
+    if (tid < p.half) turns[turn_slot<PAIRS>(tid)] = a.turns[tid];
     // positions and rows (q wants the rows only where they are its positions)
     Token t;
     t.live = 1;
@@ -406,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
                 for (int q = tid; q < n * p.half; q += kThreads) {
                     const int i = q / p.half, k = q - i * p.half;
                     float c, s;
-                    turn_of(a, tok[i].pos, k, c, s);
+                    turn_of<PAIRS>(a, turns, tok[i].pos, k, c, s);
                     sines[i * 2 * p.half + k] = c;
                     sines[i * 2 * p.half + p.half + k] = s;
                 }
@@ -414,9 +442,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
             }
         }
         if (on) t = tok[tl];
-    } else if (on) {
-        if (a.positions) t.pos = a.positions[j];
-        if (a.cu) t.live = j < a.cu[a.num_seqs] && j >= a.cu[0];
+    } else {
+        if (on && a.positions) t.pos = a.positions[j];
+        if (on && a.cu) t.live = j < a.cu[a.num_seqs] && j >= a.cu[0];
+        if (p.half > 0) __syncthreads();  // the turns
     }
     if (!on || !t.live) return;  // (a 4-bit row's four lanes leave together)
 
@@ -435,11 +464,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
         }
         const bool rotated = is_q || is_k;
         if (VEC || !rotated) {
-            constexpr int PAIRS = INTER ? 4 : 8;
-            float cs[PAIRS], sn[PAIRS];
-            if (turning) {
+            constexpr int N = INTER ? 4 : 8;
+            float cs[N], sn[N];
+            if (VEC && turning) {
 #pragma unroll
-                for (int i = 0; i < PAIRS; ++i) turn_of(a, t.pos, item * PAIRS + i, cs[i], sn[i]);
+                for (int i = 0; i < N; ++i)
+                    turn_of<PAIRS>(a, turns, t.pos, item * N + i, cs[i], sn[i]);
             }
 #pragma unroll
             for (int k = 0; k < HG; ++k) {
@@ -470,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
             }
         } else {
             float c = 1.f, s = 0.f;
-            if (turning) turn_of(a, t.pos, item, c, s);
+            if (turning) turn_of<PAIRS>(a, turns, t.pos, item, c, s);
 #pragma unroll
             for (int k = 0; k < HG; ++k) {
                 if (head + k >= (uint32_t)src.heads) break;
@@ -532,9 +562,12 @@ cudaError_t go(Params& p, cudaStream_t s) {
     p.div_ipv = make_div(p.ipv);
     p.div_seq = make_div((uint32_t)a.per_seq);
     const int64_t qb = (p.total_q + kThreads - 1) / kThreads;
-    const int64_t blocks = qb + (p.total_kv + kThreads - 1) / kThreads;
+    const int64_t kb = (p.total_kv + kThreads - 1) / kThreads, blocks = qb + kb;
     if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
-    p.q_blocks = (int)qb;
+    p.q_blocks = (uint32_t)qb;
+    p.minor_q = qb < kb;
+    p.minor = (uint32_t)(p.minor_q ? qb : kb);
+    p.period = make_div(p.minor ? (uint32_t)((p.minor_q ? kb : qb) / p.minor) + 1 : 1);
     const size_t smem = a.pg.table ? sizeof(Token) * p.tokens +
                                          (a.q4 ? sizeof(float) * 2 * p.half * p.tokens : 0)
                                    : 0;
