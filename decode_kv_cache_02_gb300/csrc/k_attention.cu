@@ -61,7 +61,10 @@ template <int D, bool Q4>
 struct Stage {
     static constexpr int W = D / 32;
     static constexpr int KEYS = Q4 ? 32 : (D == 128 ? 16 : 32);
-    static constexpr int DEPTH = 3;
+    // one stage in flight is enough where a stage is 5 KB of long arithmetic (4
+    // bits, head_dim 128: 48.5 us against 49.7 with two, one of 131071; 84.8
+    // against 86.5, 64 of 4224), not for bf16 (256 of 1152: 184 us with two, 189)
+    static constexpr int DEPTH = Q4 ? 2 : 3;
     static constexpr int ROW = Q4 ? D / 2 : D * 2;
     static constexpr int SROW = Q4 ? W * 4 : 0;
     static constexpr int V = KEYS * ROW;
