@@ -39,9 +39,10 @@
 // Measured (one GB300, KV heads 8): 64 ragged sequences to 4224 rows, G = 5,
 // head_dim 128: 94 us, 6.1 TB/s (copies alone 90); 256 of 1152, G = 4: 185 us,
 // 6.5 TB/s; 16 ragged to 16389 with 8 new tokens, head_dim 64: 61 us, 5.0 TB/s
-// (copies alone 55); one of 1152: 6.9 us.  4 bits: one of 131071, G = 5: 49 us,
-// 3.4 TB/s, about 400 instructions a warp for 16 rows at 0.55 a cycle of an SM
-// quarter (copies alone 39, no copies 45).
+// (copies alone 55); one of 1152: 6.7 us.  4 bits: one of 131071, G = 5: 48.5
+// us, 3.5 TB/s, 387 instructions a warp for 16 rows at 0.58 a cycle of an SM
+// quarter, 168 of them logic, shifts and permutes at half rate (with a ring of
+// three: copies alone 39, no copies 45).
 #include <cuda_fp16.h>
 
 #include <atomic>
