@@ -89,9 +89,21 @@ bool apart(const RowsView& a, const Span& as, const RowsView& b, const Span& bs,
     const int64_t wa = (int64_t)(a.heads - 1) * a.head + d, wb = (int64_t)(b.heads - 1) * b.head + d;
     const bool first = as.lo <= bs.lo;
     const int64_t off = (int64_t)(first ? bs.lo - as.lo : as.lo - bs.lo) / es;
-    const int64_t step = per_seq > 1 ? a.tok : (seqs > 1 ? a.seq : 0);
-    // side by side within a token's row, the next token behind both
-    return off >= (first ? wa : wb) && (step == 0 || off + (first ? wb : wa) <= step);
+    // side by side within a token's row, the next token (whichever of tokens and
+    // sequences are neighbours) behind both, and the next row of those behind all
+    if (off < (first ? wa : wb)) return false;
+    int64_t width = off + (first ? wb : wa);
+    int64_t st[2] = {a.tok, a.seq}, n[2] = {per_seq, seqs};
+    if (n[0] > 1 && n[1] > 1 && st[0] > st[1]) {
+        st[0] = a.seq; st[1] = a.tok;
+        n[0] = seqs; n[1] = per_seq;
+    }
+    for (int i = 0; i < 2; ++i) {
+        if (n[i] <= 1) continue;
+        if (st[i] < width) return false;
+        width += st[i] * (n[i] - 1);
+    }
+    return true;
 }
 
 bool same_rows(const RowsView& a, const RowsView& b) {

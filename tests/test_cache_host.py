@@ -117,6 +117,19 @@ def test_rope_apply_refusals(lib):
     assert call(n=0, **into(2 * 32 * 128)) == 0
 
 
+def test_rows_in_place_of_several_sequences(lib):
+    """q and k turned in place, two sequences of five tokens: k between one
+    sequence's q and the next, so that one's k is the other's q."""
+    from decode_kv_cache_02_gb300 import cache
+    plan = cache.RopePlan(128)._packed
+
+    def call(seq, tok):
+        q, k = _rows(seq=seq, tok=tok), _rows(2 * 32 * 128, seq=seq, tok=tok)
+        return lib.rkv_rope_apply(plan, 0, 128, 10, 5, BASE, 0, 32, q, q, 8, k, k, None)
+    assert call(seq=4096, tok=10 * 5120) == 4            # sequences side by side within a token
+    assert call(seq=4 * 5120 + 4096, tok=5120) == 4      # the last token's k on the next sequence
+
+
 def test_append_refusals(lib):
     from decode_kv_cache_02_gb300 import cache, rkv
     some = object()

@@ -73,6 +73,24 @@ def test_rope(case, inverse):
     assert torch.equal(qkv[:, (hq + hk) * d:], before[:, (hq + hk) * d:])
 
 
+@pytest.mark.parametrize("order", ["sequence", "token"])
+def test_rope_in_place_of_several_sequences(order):
+    """Slices of a projection whose rows lie sequence by sequence or token by
+    token, turned in place: the bits of a call with outputs of its own."""
+    S, n, hq, hk, d = 3, 5, 4, 2, 64
+    plan = pkg.RopePlan(d)
+    qkv = rnd((S, n, (hq + 2 * hk) * d) if order == "sequence" else (n, S, (hq + 2 * hk) * d), BF, 77)
+    rows = qkv if order == "sequence" else qkv.transpose(0, 1)
+    q = rows[..., :hq * d].unflatten(-1, (hq, d))
+    k = rows[..., hq * d:(hq + hk) * d].unflatten(-1, (hk, d))
+    pos = torch.arange(S * n, dtype=torch.int32, device=DEV)
+    oq, ok = pkg.rkv_rope_apply(plan, pos, q.contiguous(), k.contiguous())
+    v = rows[..., (hq + hk) * d:].clone()
+    pkg.rkv_rope_apply(plan, pos, q, k, out_q=q, out_k=k)
+    assert torch.equal(q, oq) and torch.equal(k, ok)
+    assert torch.equal(rows[..., (hq + hk) * d:], v)
+
+
 def test_rope_is_the_gradients_map():
     """<R x, y> = <x, R^T y>, and R^T is the derivative: differences of the
     forward pass (linear, so any step is exact) along every input."""
