@@ -24,14 +24,15 @@
 // keys a step and the probabilities through tensor memory, between warps; at 8
 // to 32 queries a row the tensor pipe is under a tenth busy as it is.)
 //
-// 4 bits: codes become numbers by placing their bits in a mantissa, exactly: K
-// bf16 128 + c (a shift and a logic op for two), V fp16 c - 8 (half a shift, a
-// logic op and an FMA).  A group's scale is applied to its own accumulator (K)
-// or to the probabilities (V), in fp32.  K's constant 128 and the groups' low
-// values enter through one more product each: (scale, low) as stored against
-// (-128, 1) times the queries' sums over the group, those in three bf16 parts
-// (K); low and scale against the probabilities (V).  So the products are exact
-// up to the rounding of p * scale to fp16 and, for the lows, of p to bf16.
+// 4 bits: codes become fp16 numbers exactly: K as they lie, c * 2^-24 or c *
+// 2^-20 (half a shift and a logic op for two), against queries brought to fp16 by
+// a power of two a row; V c - 8 (an FMA more).  A group's scale applies to its
+// own accumulator (K) or to the probabilities (V), in fp32.  The groups' low
+// values enter through one more product each: (scale, low) as stored against (0,
+// 1) times the queries' sums over the group, those in three bf16 parts (K); low
+// and scale against the probabilities (V).  So the products are exact up to the
+// rounding of p * scale to fp16 and, for the lows, of p to bf16; a query's
+// elements below 2^-27 of its row's largest are off by up to 2^-35 of that.
 //
 // The running maximum moves only when a logit passes it by more than 8 (log2):
 // p stays below 2^8 and the rescaling almost never runs.
@@ -179,21 +180,22 @@ RKV_DEV float ex2(float x) {
     return y;
 }
 // The constants of the unpacking, held in registers: an instruction takes one
-// immediate, and each of these steps wants two.
+// immediate, and each of these steps wants two.  (up: a bf16 becomes fp32 by a
+// product with 2^16, which leaves the shifting pipe, the busiest, to others: 64
+// sequences of 4224 82.3 -> 81.3 us.)
 struct Unpack {
-    uint32_t mask, magic;                    // K: bf16
-    uint32_t even, odd, half, less, sixteenth, less16;  // V: fp16
+    uint32_t even, odd, half, less, sixteenth, less16;  // V's codes
+    uint32_t up;                                        // scales
 };
 RKV_DEV Unpack unpack_constants() {
     Unpack k;
-    asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(k.mask));
-    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(k.magic));      // bf16 128, 128
+    asm volatile("mov.b32 %0, 0x000f000f;" : "=r"(k.even));
+    asm volatile("mov.b32 %0, 0x00010000;" : "=r"(k.up));
     asm volatile("mov.b32 %0, 0x00f000f0;" : "=r"(k.odd));
     asm volatile("mov.b32 %0, 0x64006400;" : "=r"(k.half));       // fp16 1024, 1024
     asm volatile("mov.b32 %0, 0xe408e408;" : "=r"(k.less));       // -1032, -1032
     asm volatile("mov.b32 %0, 0x2c002c00;" : "=r"(k.sixteenth));  // 1/16, 1/16
     asm volatile("mov.b32 %0, 0xd480d480;" : "=r"(k.less16));     // -72, -72
-    k.even = k.mask;
     return k;
 }
 RKV_DEV uint32_t and_or(uint32_t x, uint32_t mask, uint32_t magic) {
@@ -201,10 +203,18 @@ RKV_DEV uint32_t and_or(uint32_t x, uint32_t mask, uint32_t magic) {
     asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(y) : "r"(x), "r"(mask), "r"(magic));
     return y;
 }
-// Codes i and i + 4 (i: the word's nibbles shifted down) as bf16 128 + c.
-RKV_DEV uint32_t codes_at(const Unpack& k, uint32_t w, int i) {
-    return and_or(w >> (4 * i), k.mask, k.magic);
+// A word's eight codes as fp16 numbers, exactly, as they lie: bits 0..3 of a half
+// are c * 2^-24 (subnormal), bits 4..7 c * 2^-20.  The kernel is bound by such
+// logic (against bf16 128 + c, three shifts a word and a constant to subtract:
+// one sequence of 131071 49.2 -> 47.5 us, 256 of 1152 102.8 -> 99.3).
+RKV_DEV void codes_of(uint32_t w, uint32_t (&c)[4]) {
+    const uint32_t x = w >> 8;
+    c[0] = w & 0x000f000fu;
+    c[1] = w & 0x00f000f0u;
+    c[2] = x & 0x000f000fu;
+    c[3] = x & 0x00f000f0u;
 }
+RKV_DEV float pow2(int e) { return __int_as_float((e + 127) << 23); }  // -126 .. 127
 RKV_DEV __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 // Codes i and i + 4 less 8 as fp16, exactly: 1024 + c, or, four bits higher,
 // 1024 + 16 c, so that a word takes one shift.  The values' product wants codes
@@ -309,8 +319,8 @@ RKV_DEV void logits_bf16(uint32_t st, int base, const uint32_t (&qf)[NT][D / 8],
     }
 }
 
-// The same for a 4-bit stage: sum over groups of scale * (q . (128 + c)), and
-// (scale, low) against qb (the parts of (-128, 1) * sum of q over the group).
+// The same for a 4-bit stage: sum over groups of scale * (q . c), and (scale,
+// low) against qb (the parts of (0, 1) * sum of q over the group).
 template <int D, int NT>
 RKV_DEV void logits_q4(const Unpack& uk, uint32_t st, int base, const uint32_t (&qf)[NT][D / 8],
                        const uint32_t (&qb)[NT][3], float (&c)[NT][4]) {
@@ -351,17 +361,14 @@ RKV_DEV void logits_q4(const Unpack& uk, uint32_t st, int base, const uint32_t (
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         uint32_t a[4], b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = codes_at(uk, word[0][w], i);
-            b[i] = codes_at(uk, word[1][w], i);
-        }
-        const float s[2] = {__uint_as_float(sc[0][w] << 16), __uint_as_float(sc[1][w] << 16)};
+        codes_of(word[0][w], a);
+        codes_of(word[1][w], b);
+        const float s[2] = {__uint_as_float(sc[0][w] * uk.up), __uint_as_float(sc[1][w] * uk.up)};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float x[4] = {0.f, 0.f, 0.f, 0.f};
-            mma(x, a[0], b[0], a[1], b[1], qf[n][4 * w], qf[n][4 * w + 1]);
-            mma(x, a[2], b[2], a[3], b[3], qf[n][4 * w + 2], qf[n][4 * w + 3]);
+            mma_f16(x, a[0], b[0], a[1], b[1], qf[n][4 * w], qf[n][4 * w + 1]);
+            mma_f16(x, a[2], b[2], a[3], b[3], qf[n][4 * w + 2], qf[n][4 * w + 3]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[n][i] = fmaf(s[i >> 1], x[i], c[n][i]);
         }
@@ -487,7 +494,7 @@ RKV_DEV void values_q4(const Unpack& uk, uint32_t st, int base, const float (&p)
         uint32_t a[4], b[4];
         centred(uk, u, a);
         centred(uk, v, b);
-        const float s[2] = {__uint_as_float(sc[0][w] << 16), __uint_as_float(sc[1][w] << 16)};
+        const float s[2] = {__uint_as_float(sc[0][w] * uk.up), __uint_as_float(sc[1][w] * uk.up)};
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float y[4];
@@ -908,8 +915,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
         // queries as the second operand: lane (g, t) holds row g, values 32 w + 8 t ..
         uint32_t qf[NT][D / 8];
         [[maybe_unused]] uint32_t qb[NT][3];
+        float sc[NT][2];  // logits to base 2 (columns 2t, 2t + 1)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            sc[n][0] = sc[n][1] = p.scale;
             const int r = row_first + 8 * n + g;
             const bool ok = r < p.R;
             const int tk = ok ? r / p.G : 0, hd = ok ? r - tk * p.G : 0;
@@ -939,11 +948,32 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                 qf[n][4 * w + 3] = x.w;
             }
             if constexpr (Q4) {
-                // three bf16 parts hold the fp32 sum (8 bits each)
+                // The row times 2^e, its largest element in 2^14 .. 2^15, as fp16; what
+                // meets a code four bits higher is 16 times smaller.  Logits are then in
+                // units of 2^(24 - e), which mul takes back (in full below 2^115).
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    top = max(top, max(qf[n][i] & 0x7fffu, (qf[n][i] >> 16) & 0x7fffu));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int e = min(141 - (int)(top >> 7), 120);
+                const float f = pow2(e);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const float h = i & 1 ? f * 0.0625f : f;
+                    qf[n][i] = pack_f16(__uint_as_float(qf[n][i] << 16) * h,
+                                        __uint_as_float(qf[n][i] & 0xffff0000u) * h);
+                }
+                own = own * f * 0x1p-24f;
+                const float mul = fminf(fmaxf(p.scale * 4096.f * pow2(12 - e), 0x1p-120f), 0x1p127f);
+                sc[n][0] = __shfl_sync(0xffffffffu, mul, 8 * t);
+                sc[n][1] = __shfl_sync(0xffffffffu, mul, 8 * t + 4);
+                // the sum too, in three bf16 parts (8 bits each)
 #pragma unroll
                 for (int i = 0; i < 3; ++i) {
                     const float part = __bfloat162float(__float2bfloat16_rn(own));
-                    qb[n][i] = pack(-128.f * part, part);
+                    qb[n][i] = pack(0.f, part);
                     own -= part;
                 }
             }
@@ -1020,7 +1050,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
 #pragma unroll
                     for (int kt = 1; kt < KT; ++kt)
                         top[n][i] = fmaxf(top[n][i], fmaxf(x[kt][n][i], x[kt][n][i + 2]));
-                    grow |= top[n][i] > m[n][i] + p.slack;
+                    grow |= Q4 ? (top[n][i] - m[n][i]) * sc[n][i] > 8.f : top[n][i] > m[n][i] + p.slack;
                 }
             [[maybe_unused]] uint32_t most = 0;
             if constexpr (Q4) {
@@ -1044,7 +1074,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                         const float base =
-                            mx == -INFINITY ? 0.f : mx * p.scale + (Q4 ? (float)(bound - 7) : 0.f);
+                            mx == -INFINITY ? 0.f : mx * sc[n][i] + (Q4 ? (float)(bound - 7) : 0.f);
                         const float f = m[n][i] == -INFINITY ? 0.f : ex2(ref[n][i] - base);
                         m[n][i] = mx;
                         ref[n][i] = base;
@@ -1063,8 +1093,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int kt = 0; kt < KT; ++kt) {
-                        x[kt][n][i] = ex2(fmaf(x[kt][n][i], p.scale, -ref[n][i]));
-                        x[kt][n][i + 2] = ex2(fmaf(x[kt][n][i + 2], p.scale, -ref[n][i]));
+                        x[kt][n][i] = ex2(fmaf(x[kt][n][i], sc[n][i], -ref[n][i]));
+                        x[kt][n][i + 2] = ex2(fmaf(x[kt][n][i + 2], sc[n][i], -ref[n][i]));
                         l[n][i] += x[kt][n][i] + x[kt][n][i + 2];
                     }
             // rows that only some of the tokens see: an infinity or a NaN there must not reach

@@ -575,6 +575,43 @@ def test_q4_attention_of_any_magnitude():
     check_attention("q4", q, out, lse, rows, lens, 1 / math.sqrt(d), cache)
 
 
+def test_q4_attention_of_any_query():
+    """Queries far from 1 against keys as far the other way (the logits are the
+    same), rows of one call of different magnitudes, elements of a row 2^20
+    apart, and rows of zeros."""
+    lens, H, G, d, bs = [500, 37], 1, 3, 128, 16
+    cache, table, rows = make_cache(2, H, d, bs, lens, "q4", 26, junk=False)
+    q = rnd((2, 1, H * G, d), BF, 3)
+    q[..., 1::3] *= 2.0 ** -20
+    lens_d = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    keep = cache.K_scales.clone()
+    for k in (-100, -40, 60, 100):
+        cache.K_scales.copy_(keep * 2.0 ** -k)
+        out, lse = attend("q4", q * 2.0 ** k, cache, table, lens_d, lse=True)
+        check_attention("q4", q * 2.0 ** k, out, lse, [[x * 2.0 ** -k for x in rows[0]], rows[1]], lens, 1 / math.sqrt(d), cache)
+    cache.K_scales.copy_(keep)
+    mixed = q.clone()
+    mixed[:, :, 0] = 0
+    mixed[0, :, 1] *= 2.0 ** -110
+    mixed[1, :, 2] *= 4
+    out, lse = attend("q4", mixed, cache, table, lens_d, lse=True)
+    check_attention("q4", mixed, out, lse, rows, lens, 1 / math.sqrt(d), cache)
+    # a row of the largest numbers sees the key nearest to it alone, the others theirs
+    mixed[0, 0, 1] = q[0, 0, 1] * 2.0 ** 124
+    out, lse = attend("q4", mixed, cache, table, lens_d, lse=True)
+    best = (rows[0][0][0] @ mixed[0, 0, 1].double().cpu()).argmax()
+    e = rows[1][0][0][best]
+    # (p = 1: the output's rounding, and fp32 sums of scale * code, low and 8 * scale)
+    assert ((out[0, 0, 1].double().cpu() - e).abs() <= 2.0 ** -8 * e.abs() + 2.0 ** -20 * e.abs().amax()).all()
+    small = mixed.clone()
+    small[0, 0, 1] = 0
+    o2, l2 = attend("q4", small, cache, table, lens_d, lse=True)
+    check_attention("q4", small, o2, l2, rows, lens, 1 / math.sqrt(d), cache)
+    out[0, 0, 1] = o2[0, 0, 1]
+    # (each within 2^-8 of the values' magnitude and of the output, and less for the rest)
+    assert ((out - o2).abs() <= 2.0 ** -5 * max(float(x.abs().max()) for x in rows[1])).all()
+
+
 def test_attention_bad_blocks_and_lens():
     """Ids that name no block: recorded, their rows skipped.  lens past
     max_rows is recorded and cut, a negative one counts as none."""
