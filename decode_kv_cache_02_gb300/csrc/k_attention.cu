@@ -142,6 +142,18 @@ RKV_DEV uint32_t lds2(uint32_t a) {
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
     return v;
 }
+// Two 8 x 8 matrices of 16-bit values, rows of 16 bytes at the addresses of lanes
+// 0 .. 7 and 8 .. 15, as a fragment; transposed.
+RKV_DEV void ldm2(uint32_t (&r)[2], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];"
+                 : "=r"(r[0]), "=r"(r[1])
+                 : "r"(a));
+}
+RKV_DEV void ldm2t(uint32_t (&r)[2], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];"
+                 : "=r"(r[0]), "=r"(r[1])
+                 : "r"(a));
+}
 RKV_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 RKV_DEV void cp_wait() {
@@ -319,6 +331,13 @@ RKV_DEV void logits_bf16(uint32_t st, int base, const uint32_t (&qf)[NT][D / 8],
     }
 }
 
+// Where the scales of row lane % 16 of the 16 keys from base on lie (head_dim
+// 128: 16 bytes a row).
+RKV_DEV int scale_row(int base) {
+    const int lane = threadIdx.x & 31;
+    return (base + phys<true>(lane & 7) + (lane & 8)) * 16;
+}
+
 // The same for a 4-bit stage: sum over groups of scale * (q . c), and (scale,
 // low) against qb (the parts of (0, 1) * sum of q over the group).
 template <int D, int NT>
@@ -341,7 +360,6 @@ RKV_DEV void logits_q4(const Unpack& uk, uint32_t st, int base, const uint32_t (
             word[k][3] = __byte_perm(x.y, x.w, 0x7632);
             const uint4 y = lds16(srow);
             sc[k][0] = y.x; sc[k][1] = y.y; sc[k][2] = y.z; sc[k][3] = y.w;
-            own[k] = lds4(srow + 4 * t);
         } else {
             const uint2 x = lds8(row + t * 8);
             word[k][0] = __byte_perm(x.x, x.y, 0x5410);
@@ -351,6 +369,7 @@ RKV_DEV void logits_q4(const Unpack& uk, uint32_t st, int base, const uint32_t (
             own[k] = t == 0 ? y.x : (t == 1 ? y.y : 0u);
         }
     }
+    if constexpr (W == 4) ldm2(own, st + S::ks() + scale_row(base));
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -449,13 +468,12 @@ RKV_DEV bool unfinite(uint32_t st, int r) {
     return bad;
 }
 
-// The same for a 4-bit stage; p: probabilities of 16 keys as accumulators lie,
-// pb: as operand.  low: row w (W + w) of the accumulators collects sum of p *
-// low (scale) of group w.  MASKED: a hidden row's NaN stays out (some of the
-// queries do not see some of the rows).
+// The same for a 4-bit stage but for the lows; p: probabilities of 16 keys as
+// accumulators lie.  MASKED: a hidden row's NaN stays out (some of the queries do
+// not see some of the rows).
 template <int D, int NT, bool MASKED>
 RKV_DEV void values_q4(const Unpack& uk, uint32_t st, int base, const float (&p)[NT][4],
-                       const uint32_t (&pb)[NT][2], float (&o)[D / 16][NT][4]) {
+                       float (&o)[D / 16][NT][4]) {
     using S = Stage<D, true>;
     constexpr int W = S::W;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -511,25 +529,22 @@ RKV_DEV void values_q4(const Unpack& uk, uint32_t st, int base, const float (&p)
     }
 }
 
-// (low, scale) of the 16 keys as operand rows: row w low, row W + w scale.
+// (scale, low) of the 16 keys as operand rows: row 2 w scale, row 2 w + 1 low.
 template <int D>
 RKV_DEV void low_rows(uint32_t st, int base, uint32_t (&a)[2]) {
     using S = Stage<D, true>;
-    constexpr int W = S::W;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int half = g < W ? 2 * g + 1 : (g < 2 * W ? 2 * (g - W) : 0);
-    const uint32_t keep = g < 2 * W ? 0xffffffffu : 0u;
-    uint32_t x[4];
+    if constexpr (S::W == 4) {
+        ldm2t(a, st + S::vs() + scale_row(base));
+    } else {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        uint32_t x[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int pr = base + phys<true>(2 * t + (k & 1) + 8 * (k >> 1));
-        x[k] = lds2(st + S::vs() + pr * S::SROW + 2 * half);
-    }
-    a[0] = __byte_perm(x[0], x[1], 0x5410);
-    a[1] = __byte_perm(x[2], x[3], 0x5410);
-    if constexpr (W < 4) {  // (rows past 2 W stand for nothing)
-        a[0] &= keep;
-        a[1] &= keep;
+        for (int k = 0; k < 4; ++k) {
+            const int pr = base + phys<true>(2 * t + (k & 1) + 8 * (k >> 1));
+            x[k] = lds2(st + S::vs() + pr * S::SROW + 2 * (g & 3));
+        }
+        a[0] = g < 4 ? __byte_perm(x[0], x[1], 0x5410) : 0u;  // (rows past 2 W stand for nothing)
+        a[1] = g < 4 ? __byte_perm(x[2], x[3], 0x5410) : 0u;
     }
 }
 
@@ -1121,13 +1136,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
                             mma(low[n], la[0], 0u, la[1], 0u, pb[n][0], pb[n][1]);
-                        values_q4<D, NT, false>(uk, st, kt * 16, x[kt], pb, o);
+                        values_q4<D, NT, false>(uk, st, kt * 16, x[kt], o);
                     } else {
                         values_bf16<D, NT, false>(st, kt * 16, pb, ~0u, ~0u, ~0u, o);
                     }
                     continue;
                 }
-                if constexpr (Q4) values_q4<D, NT, true>(uk, st, kt * 16, x[kt], pb, o);
+                if constexpr (Q4) values_q4<D, NT, true>(uk, st, kt * 16, x[kt], o);
                 // one token at a time
                 const int t0 = row_first / p.G;
                 const int t1 = (min(p.R, row_first + ROWS) - 1) / p.G;
@@ -1193,8 +1208,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                 if constexpr (Q4)
 #pragma unroll
                     for (int w = 0; w < W; ++w)
-                        add[w] = __shfl_sync(0xffffffffu, low[n][i], 4 * w + t) +
-                                 8.f * __shfl_sync(0xffffffffu, low[n][i], 4 * (W + w) + t);
+                        add[w] = __shfl_sync(0xffffffffu, low[n][i], 4 * (2 * w + 1) + t) +
+                                 8.f * __shfl_sync(0xffffffffu, low[n][i], 4 * (2 * w) + t);
 #pragma unroll
                 for (int e = 0; e < D / 16; ++e) {
                     // the pair of dimensions this accumulator's rows g and g + 8 stand for
