@@ -812,6 +812,67 @@ def test_streams_graphs_and_two_calls_at_once(S):
     assert torch.equal(one, a) and torch.equal(two, b) and status(ws) == 0 and status(w2) == 0
 
 
+@pytest.mark.parametrize("kind", ["bf16", "q4"])
+@pytest.mark.parametrize("S", [3, 45])
+def test_calls_that_depend_on_the_one_before(S, kind):
+    """Each call's queries are the last one's output, its lengths and its cache
+    just written: on a stream and captured (behind a memset, and where two
+    streams meet) the bits of calls waited for one by one."""
+    H, G, d, bs, n = 2, 4, 128, 16, 400
+    cache, table, rows = make_cache(S, H, d, bs, [n] * S, kind, 3, junk=False)
+    q = rnd((S, 1, H * G, d), BF, 7)
+    x = [torch.empty_like(q) for _ in range(6)]
+    k, v = rnd((S, 1, H, d), BF, 5), rnd((S, 1, H, d), BF, 6)
+    lens = torch.empty(S, dtype=torch.int32, device=DEV)
+    ws = pkg.alloc_attention_workspace(q, H, n)
+    append = pkg.rkv_q4_append if kind == "q4" else pkg.rkv_paged_append
+    side = torch.cuda.Stream()
+
+    def run(wait):
+        for i, out in enumerate(x):
+            lens.zero_()
+            lens.add_(n - 60 * i)
+            if i % 2:
+                append(*((cache,) if kind == "q4" else cache), k, v, table, lens, workspace=ws)
+            wait()
+            if i == 4:  # two streams meet before the call
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(side):
+                    lens.sub_(7)
+                torch.cuda.current_stream().wait_stream(side)
+            out.fill_(3.0)
+            attend(kind, q if i == 0 else x[i - 1], cache, table, lens, max_rows=n, out=out, workspace=ws)
+            wait()
+    run(torch.cuda.synchronize)  # (its appends change rows that its first call read)
+    run(torch.cuda.synchronize)
+    want = [t.clone() for t in x]
+    run(lambda: None)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(x, want)) and status(ws) == 0
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(lambda: None)
+    for _ in range(3):
+        for t in x:
+            t.zero_()
+        g.replay()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(x, want)) and status(ws) == 0
+    # the memset right before the call
+    g2 = torch.cuda.CUDAGraph()
+    lens.fill_(n)
+    torch.cuda.synchronize()
+    a = attend(kind, q, cache, table, lens, max_rows=n, workspace=ws).clone()
+    out = torch.empty_like(a)
+    with torch.cuda.graph(g2):
+        out.zero_()
+        attend(kind, q, cache, table, lens, max_rows=n, out=out, workspace=ws)
+    g2.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a, out)
+
+
 def test_same_result_every_time():
     for kind in ("bf16", "q4", "fp32"):
         lens = [3000, 17]
