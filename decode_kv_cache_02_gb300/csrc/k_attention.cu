@@ -879,7 +879,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
 
     [[maybe_unused]] Unpack uk;
     if constexpr (Q4) uk = unpack_constants();
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // what came before on the stream is done
+    wait_for_last();
 
     Place place{};
     Piece c{};
@@ -1180,7 +1180,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
             st = st == ring + (S::DEPTH - 1) * S::BYTES ? ring : st + S::BYTES;
         }
         cp_wait<0>();
-        if (place.u0 >= place.u1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if (place.u0 >= place.u1) let_next_begin();
 
         // sums over the lanes that share a query
 #pragma unroll
@@ -1259,6 +1259,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
     const float* q32 = reinterpret_cast<const float*>(p.q);
     const float sign = p.flip ? -1.f : 1.f;
     uint8_t* ring = smem + warp * (S::DEPTH * S::BYTES);
+    wait_for_last();
 
     Place place = find_place<kWarps * 32>(p, UNIT, run);
     Piece c{};
@@ -1435,7 +1436,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = blockIdx.x % p.groups;
     const int run = blockIdx.x / p.groups;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
+    wait_for_last();  // the pieces are written
     const int4 job = p.joins[blockIdx.x];
     const int s = job.x, h = job.y, parts = job.z;
     if (parts == 0) return;
@@ -1561,9 +1562,7 @@ cudaError_t go(const Params& p, unsigned ctas, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kern, bytes, done);
     if (e != cudaSuccess) return e;
-    // the launch overlaps the end of the stream's last kernel; the blocks wait for it before
-    // their first look at memory (an append and an attention of 16 sequences of 1152, call
-    // after call: 28.0 -> 26.0 us; in a captured graph no change)
+    // as launch_early, with a cluster
     cudaLaunchAttribute at[2]{};
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1593,8 +1592,7 @@ cudaError_t go32(const Params& p, unsigned ctas, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kern, bytes, done);
     if (e != cudaSuccess) return e;
-    kern<<<ctas, kWarps * 32, bytes, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(kern, ctas, kWarps * 32, bytes, s, p);
 }
 
 bool is_f32(const AttnArgs& a) { return !a.q4 && a.dtype == RKV_DTYPE_FP32; }
@@ -1655,23 +1653,15 @@ cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& pl, cudaStream_t
 
 template <typename T, int D>
 cudaError_t go_join(const Params& p, const AttnPlan& pl, cudaStream_t s) {
-    // may begin while the pieces are still being written; it waits for them itself
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
     // most blocks find nothing to join.  With about as many problems as runs, or
     // more, the pieces of one are few and a block's warps take a query each;
     // otherwise a block takes a query.
     const int blocks = pl.runs * pl.groups, used = p.R < pl.rows ? p.R : pl.rows;
     const bool few = (int64_t)p.num_seqs * p.H * 8 >= pl.runs;
     const int y = few ? (used + kJoinWarps - 1) / kJoinWarps : used;
-    cfg.gridDim = dim3((unsigned)blocks, (unsigned)y);
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = s;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, D>, p, pl.rows);
+    // begins while the pieces are still being written and waits for them itself
+    return launch_early(attn_combine_kernel<T, D>, dim3((unsigned)blocks, (unsigned)y), kJoinWarps * 32,
+                        0, s, p, pl.rows);
 }
 
 cudaError_t launch_attention_combine(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {

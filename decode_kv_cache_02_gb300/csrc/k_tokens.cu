@@ -338,6 +338,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
     __shared__ uint64_t turns[kTurns];
     constexpr int HG = kHeads<T>, PAIRS = VEC ? (INTER ? 4 : 8) : 1;
     const TokenArgs& a = p.a;
+    let_next_begin();
+    wait_for_last();
     const int tid = threadIdx.x;
     const bool append = a.pg.table != nullptr;
     bool is_q;
@@ -532,12 +534,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
 template <typename T, bool VEC, bool INTER>
 cudaError_t go(const Params& p, unsigned grid, size_t smem, cudaStream_t s) {
     if (!p.a.q4)
-        tokens_kernel<T, VEC, INTER, false, 2><<<grid, kThreads, smem, s>>>(p);
-    else if (p.a.d == 128)
-        tokens_kernel<T, VEC, INTER, true, 4><<<grid, kThreads, smem, s>>>(p);
-    else
-        tokens_kernel<T, VEC, INTER, true, 2><<<grid, kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+        return launch_early(tokens_kernel<T, VEC, INTER, false, 2>, grid, kThreads, smem, s, p);
+    return p.a.d == 128 ? launch_early(tokens_kernel<T, VEC, INTER, true, 4>, grid, kThreads, smem, s, p)
+                        : launch_early(tokens_kernel<T, VEC, INTER, true, 2>, grid, kThreads, smem, s, p);
 }
 template <typename T>
 cudaError_t go(Params& p, cudaStream_t s) {
@@ -584,6 +583,8 @@ template <typename T, int W>
 __global__ void __launch_bounds__(kThreads) q4_read_kernel(const __grid_constant__ Q4ReadArgs a,
                                                            int64_t total, int both, Div by_rows,
                                                            Div by_heads) {
+    let_next_begin();
+    wait_for_last();
     const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (e >= total) return;
     const int t = (int)(e & 3);
@@ -652,13 +653,11 @@ cudaError_t launch_q4_read(const Q4ReadArgs& a, cudaStream_t s) {
     const unsigned g = (unsigned)blocks;
     const Div rows = make_div((uint32_t)a.n_rows), heads = make_div((uint32_t)a.pg.H);
     if (a.dtype == RKV_DTYPE_BF16) {
-        if (a.d == 128) q4_read_kernel<__nv_bfloat16, 4><<<g, kThreads, 0, s>>>(a, total, both, rows, heads);
-        else q4_read_kernel<__nv_bfloat16, 2><<<g, kThreads, 0, s>>>(a, total, both, rows, heads);
-    } else {
-        if (a.d == 128) q4_read_kernel<float, 4><<<g, kThreads, 0, s>>>(a, total, both, rows, heads);
-        else q4_read_kernel<float, 2><<<g, kThreads, 0, s>>>(a, total, both, rows, heads);
+        return launch_early(a.d == 128 ? q4_read_kernel<__nv_bfloat16, 4> : q4_read_kernel<__nv_bfloat16, 2>,
+                            g, kThreads, 0, s, a, total, both, rows, heads);
     }
-    return cudaGetLastError();
+    return launch_early(a.d == 128 ? q4_read_kernel<float, 4> : q4_read_kernel<float, 2>, g, kThreads,
+                        0, s, a, total, both, rows, heads);
 }
 
 }  // namespace rkv

@@ -72,4 +72,29 @@ RKV_DEV float warp_max(float v) {
     return v;
 }
 
+// A launch that may begin while the stream's last kernel ends (launch_early)
+// waits for that kernel before its first look at memory, and may let the launch
+// behind it begin, which waits in turn.  Call after call on a stream this takes
+// 2 us off each (16384 tokens rotated: 53.8 -> 51.2 us, appended 64.9 -> 62.6);
+// captured, an append and an attention of one sequence of 1152 take 9.4 us
+// instead of 10.2.  The join of an attention lets nothing begin: what began there
+// would hold its SMs up (16 sequences of 16384 at 4 bits 57.4 -> 58.4 us).
+RKV_DEV void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+RKV_DEV void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                         A&&... args) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 }  // namespace rkv

@@ -873,6 +873,50 @@ def test_calls_that_depend_on_the_one_before(S, kind):
     assert torch.equal(a, out)
 
 
+def test_token_calls_that_depend_on_the_one_before():
+    """Rotations of a rotation's output, written to a 4-bit cache and read back
+    as the next one's input, over tokens that fill the device several times: the
+    bits of calls waited for one by one, on a stream and captured."""
+    S, n, H, d, bs = 4, 2048, 4, 128, 64
+    plan = pkg.RopePlan(d)
+    pos = torch.arange(S * n, dtype=torch.int32, device=DEV)
+    table = torch.arange(S * n // bs, dtype=torch.int32, device=DEV).view(S, -1)
+    lens = torch.full((S,), n, dtype=torch.int32, device=DEV)
+    c = pkg.alloc_q4_cache(S * n // bs, H, bs, d)
+    start = rnd((S * n, H, d), BF, 4)
+    x = [torch.empty_like(start) for _ in range(2)]
+    k, v = (torch.empty(S * H, n, d, dtype=BF, device=DEV) for _ in range(2))
+
+    def run(wait):
+        x[0].copy_(start)
+        for i in range(3):
+            pkg.rkv_rope_apply(plan, pos, x[0], out_q=x[1])
+            wait()
+            pkg.rkv_rope_apply(plan, pos, x[1], out_q=x[1], inverse=i == 1)
+            wait()
+            pkg.rkv_q4_append(c, x[1].view(S, n, H, d), x[0].view(S, n, H, d), table, lens)
+            wait()
+            pkg.rkv_q4_read(c, table, lens, n, out_K=k, out_V=v)
+            wait()
+            rows = lambda t: t.view(S, H, n, d).transpose(1, 2)  # noqa: E731
+            pkg.rkv_rope_apply(plan, pos, rows(k), rows(v), out_q=x[0].view(S, n, H, d), out_k=x[1].view(S, n, H, d))
+            wait()
+    run(torch.cuda.synchronize)
+    want = [t.clone() for t in (*x, k, v)]
+    for _ in range(3):
+        run(lambda: None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*x, k, v), want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(lambda: None)
+    for t in (*x, k, v):
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((*x, k, v), want))
+
+
 def test_same_result_every_time():
     for kind in ("bf16", "q4", "fp32"):
         lens = [3000, 17]
