@@ -217,6 +217,27 @@ RKV_DEV Token place_token(const TokenArgs& a, int64_t j) {
     return t;
 }
 
+// Smallest and largest; NaN where any is NaN.
+RKV_DEV float min_of(float a, float b, float c) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+RKV_DEV float max_of(float a, float b, float c) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+// x / 15 rounded to nearest for 0 <= x < infinity (NaN for infinity): a quotient
+// by the divisor's reciprocal and one correction by its remainder (division by a
+// divisor known in advance, Brisebarre, Muller and Raina, 2004; compared with the
+// division for every such x).
+RKV_DEV float fifteenth(float x) {
+    constexpr float c = 1.f / 15.f;
+    const float q = x * c;
+    return fmaf(fmaf(-15.f, q, x), c, q);
+}
+
 // One 4-bit row's share of a lane: values of W groups.  The four lanes of the
 // row take part.
 template <int W>
@@ -226,24 +247,22 @@ RKV_DEV void quantise_store(const float (&v)[W][8], int t, bool write, uint8_t* 
     uint32_t h[W][2], pair = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-        float mn = v[w][0], mx = v[w][0], bad = v[w][0] * 0.f;
-#pragma unroll
-        for (int i = 1; i < 8; ++i) {
-            mn = fminf(mn, v[w][i]);
-            mx = fmaxf(mx, v[w][i]);
-            bad += v[w][i] * 0.f;  // NaN once any value is NaN or infinite
-        }
+        float mn = min_of(v[w][0], v[w][1], v[w][2]), mx = max_of(v[w][0], v[w][1], v[w][2]);
+        mn = min_of(min_of(mn, v[w][3], v[w][4]), v[w][5], v[w][6]);
+        mx = max_of(max_of(mx, v[w][3], v[w][4]), v[w][5], v[w][6]);
+        mn = min_of(mn, mn, v[w][7]);
+        mx = max_of(mx, mx, v[w][7]);
 #pragma unroll
         for (int o = 1; o <= 2; o <<= 1) {
-            mn = fminf(mn, __shfl_xor_sync(quad, mn, o));
-            mx = fmaxf(mx, __shfl_xor_sync(quad, mx, o));
-            bad += __shfl_xor_sync(quad, bad, o);
+            mn = min_of(mn, mn, __shfl_xor_sync(quad, mn, o));
+            mx = max_of(mx, mx, __shfl_xor_sync(quad, mx, o));
         }
         __nv_bfloat16 lo = __float2bfloat16_rd(mn);
         float lof = __bfloat162float(lo);
-        __nv_bfloat16 sc = __float2bfloat16_ru(__fdiv_rn(mx - lof, 15.f));
+        __nv_bfloat16 sc = __float2bfloat16_ru(fifteenth(mx - lof));
         float sf = __bfloat162float(sc);
-        if (bad != 0.f || !(sf <= FLT_MAX) || !(lof >= -FLT_MAX)) {
+        // (an infinity is the smallest or the largest and makes the difference one, or NaN)
+        if (!(sf <= FLT_MAX)) {
             sc = lo = __ushort_as_bfloat16(0x7fff);
             sf = 0.f;
         }
