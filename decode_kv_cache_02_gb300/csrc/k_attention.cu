@@ -38,12 +38,11 @@
 // p stays below 2^8 and the rescaling almost never runs.
 //
 // Measured (one GB300, KV heads 8): 64 ragged sequences to 4224 rows, G = 5,
-// head_dim 128: 94 us, 6.1 TB/s (copies alone 90); 256 of 1152, G = 4: 185 us,
-// 6.5 TB/s; 16 ragged to 16389 with 8 new tokens, head_dim 64: 61 us, 5.0 TB/s
-// (copies alone 55); one of 1152: 6.7 us.  4 bits: one of 131071, G = 5: 48.5
-// us, 3.5 TB/s, 387 instructions a warp for 16 rows at 0.58 a cycle of an SM
-// quarter, 168 of them logic, shifts and permutes at half rate (with a ring of
-// three: copies alone 39, no copies 45).
+// head_dim 128: 91.5 us, 6.3 TB/s; 256 of 1152, G = 4: 183 us, 6.6 TB/s; 16 ragged
+// to 16389 with 8 new tokens, head_dim 64: 59.5 us, 5.2 TB/s (copies alone, before
+// its launch overlapped what was there: 55); one of 1152: 6.1 us.  4 bits: one
+// of 131071, G = 5: 43.6 us, 3.9 TB/s, 365 instructions a warp for 16 rows at 0.59
+// a cycle of an SM quarter, of whose cycles the logic pipe takes 47 in a hundred.
 #include <cuda_fp16.h>
 
 #include <atomic>

@@ -13,17 +13,17 @@
 // its loads first, then finds the position (and, with an append, the row: a
 // warp searches the ragged sequences 32 ways) and computes eight sines once for
 // its heads; nothing waits on a table of sines.  Measured (one GB300): 16384
-// tokens of 48 heads, 403 MB: 64.5 us, 6.2 TB/s; 28.9 thousand ragged tokens
-// appended with their queries, 730 MB: 111 us, 6.6 TB/s; 64 tokens of 40 heads
-// 3.2 us, appended 3.8 us.
+// tokens of 48 heads, 403 MB: 62.5 us, 6.4 TB/s; 28.9 thousand ragged tokens
+// appended with their queries, 730 MB: 108.5 us, 6.7 TB/s; 64 tokens of 40 heads
+// 3.1 us, appended 3.7 us (one after the other in a captured graph).
 //
 // 4 bits: four neighbouring lanes own one row; lane t holds values 32 w + 8 t
 // .. + 7 of every group w, so a group's minimum and maximum take two shuffles
 // and the lane's codes of all groups are one store of 16 bytes (8 at head_dim
 // 64).  (x - low) * r + 1.5 * 2^23 in one FMA rounds the exact product to a
 // whole number (halves to even) and leaves it in the low mantissa bits.  16.8
-// thousand tokens with their queries, written and read back, 473 MB: 87.5 us,
-// 5.4 TB/s (the blocks wait for their rows' places).
+// thousand tokens with their queries, written and read back, 473 MB: 82 us,
+// 5.8 TB/s (the blocks wait for their rows' places).
 #include <float.h>
 
 #include "rkv_common.cuh"
