@@ -292,12 +292,32 @@ RKV_DEV void quantise_store(const float (&v)[W][8], int t, bool write, uint8_t* 
 }
 
 // The lane's part of a K row turned in place: values 32 w + 8 t .. of group w;
-// cs, sn: the token's cosines and sines, x: the row (partners that lie in
+// cs, sn: the token's cosines and sines, x: the row (partners that may lie in
 // another lane are read again).
 template <typename T, bool VEC, bool INTER, int W>
 RKV_DEV void turn_row(float (&v)[W][8], const T* x, int t, const Params& p, const float* cs,
                       const float* sn) {
     const int rot = p.a.rot, half = p.half;
+    if constexpr (VEC && !INTER) {
+        // halves that are whole groups: both elements of a pair are the lane's own
+        const auto pairs = [&](float (&x)[8], float (&y)[8], int i0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float c = cs[i0 + i], s = sn[i0 + i], a = x[i], b = y[i];
+                x[i] = a * c - b * s;
+                y[i] = b * c + a * s;
+            }
+        };
+        if (half == 16 * W) {
+#pragma unroll
+            for (int w = 0; w < W / 2; ++w) pairs(v[w], v[w + W / 2], 32 * w + 8 * t);
+            return;
+        }
+        if (W == 4 && half == 32) {
+            pairs(v[0], v[1], 8 * t);
+            return;
+        }
+    }
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         const int e = 32 * w + 8 * t;
