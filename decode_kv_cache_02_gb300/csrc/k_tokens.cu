@@ -13,8 +13,8 @@
 // its loads first, then finds the position (and, with an append, the row: a
 // warp searches the ragged sequences 32 ways) and computes eight sines once for
 // its heads; nothing waits on a table of sines.  Measured (one GB300): 16384
-// tokens of 48 heads, 403 MB: 62.5 us, 6.4 TB/s; 28.9 thousand ragged tokens
-// appended with their queries, 730 MB: 108.5 us, 6.7 TB/s; 64 tokens of 40 heads
+// tokens of 48 heads, 403 MB: 61 us, 6.6 TB/s; 28.9 thousand ragged tokens
+// appended with their queries, 730 MB: 107 us, 6.8 TB/s; 64 tokens of 40 heads
 // 3.1 us, appended 3.7 us (one after the other in a captured graph).
 //
 // 4 bits: four neighbouring lanes own one row; lane t holds values 32 w + 8 t
@@ -22,8 +22,8 @@
 // and the lane's codes of all groups are one store of 16 bytes (8 at head_dim
 // 64).  (x - low) * r + 1.5 * 2^23 in one FMA rounds the exact product to a
 // whole number (halves to even) and leaves it in the low mantissa bits.  16.8
-// thousand tokens with their queries, written and read back, 473 MB: 82 us,
-// 5.8 TB/s (the blocks wait for their rows' places).
+// thousand tokens with their queries, written and read back, 473 MB: 80 us,
+// 5.9 TB/s (the blocks wait for their rows' places).
 #include <float.h>
 
 #include "rkv_common.cuh"
@@ -32,7 +32,11 @@
 namespace rkv {
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a block: few enough that its tokens' places and sines hold up few
+// others (16384 tokens appended: 61.6 us, at 4 bits 62.1; 256 threads: 62.6 and
+// 64.5; 64: 61.9 and 64.5), and as many as a plan has pairs.
+constexpr int kThreads = 128;
+static_assert(kThreads >= RKV_MAX_ROT_DIM / 2, "a thread per pair of the plan");
 
 struct Div {  // n / d for 0 <= n < 2^31
     uint32_t d, mul, shift;
@@ -62,7 +66,7 @@ struct Params {
     uint32_t minor, q_blocks;
     int minor_q;
     int64_t total_q, total_kv;
-    Div div_q, div_kv, div_iph, div_ipv, div_seq, period;
+    Div div_q, div_kv, div_iph, div_ipv, div_seq, div_half, period;
 };
 
 // What a block knows of each of its tokens.
@@ -363,12 +367,12 @@ template <typename T> constexpr int kHeads = sizeof(T) == 2 ? 4 : 2;
 // VEC: the rotated part splits into whole steps of eight.  A unit is one item
 // (the eight pairs, or eight elements, that a thread holds; without VEC one
 // pair or element) of kHeads heads, or a lane of a 4-bit row.
-// Four blocks an SM where the registers would allow three (28.9 thousand tokens
-// appended: 127 -> 122 us; 16.8 thousand at 4 bits and read back: 105 -> 96 us;
-// five: 103 us); the others are left to the compiler (67.5 us at 16384 x 48 heads, 69.6
-// with a bound of three).
+// 64 registers, eight blocks an SM, where the compiler would take more (28.9
+// thousand tokens appended at 80: 127 us against 122; 16384 at 4 bits 72 against
+// 64.5; at 56 and less these spill: 81 and 78); the others are left to it (the
+// interleaved rotation of 16384 x 48 heads 67.5 us, 69.6 bounded).
 template <typename T, bool INTER, bool Q4>
-constexpr int kBlocks = Q4 || (sizeof(T) == 2 && !INTER) ? 4 : 0;
+constexpr int kBlocks = Q4 || (sizeof(T) == 2 && !INTER) ? 8 : 0;
 template <typename T, bool VEC, bool INTER, bool Q4, int W>
 __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -472,8 +476,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
         __syncthreads();
         if constexpr (Q4) {
             if (!is_q) {
+#pragma unroll 1  // (unrolled, the append takes 78 us instead of 64.5)
                 for (int q = tid; q < n * p.half; q += kThreads) {
-                    const int i = q / p.half, k = q - i * p.half;
+                    const int i = div_by(q, p.div_half), k = q - i * p.half;
                     float c, s;
                     turn_of<PAIRS>(a, turns, tok[i].pos, k, c, s);
                     sines[i * 2 * p.half + k] = c;
@@ -599,6 +604,7 @@ cudaError_t go(Params& p, cudaStream_t s) {
     p.div_iph = make_div(p.iph);
     p.div_ipv = make_div(p.ipv);
     p.div_seq = make_div((uint32_t)a.per_seq);
+    p.div_half = make_div(p.half > 0 ? p.half : 1);
     const int64_t qb = (p.total_q + kThreads - 1) / kThreads;
     const int64_t kb = (p.total_kv + kThreads - 1) / kThreads, blocks = qb + kb;
     if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
