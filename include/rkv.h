@@ -317,7 +317,11 @@ int rkv_paged_compress(const rkv_paged_desc* desc, void* K_pool, void* V_pool,
  * number of tokens for every sequence, of token i of sequence s at
  * data[s * seq_stride + i * token_stride + h * head_stride + d].  Strides
  * count elements; data and every stride used are multiples of 16 bytes, so a
- * slice of a fused projection is taken as it is. */
+ * slice of a fused projection is taken as it is.
+ *
+ * The launches of these calls may begin while the stream's last kernel ends
+ * (programmatic dependent launch) and wait for it before they read or write
+ * anything: results are in stream order as ever, also in captured graphs. */
 typedef struct {
     void* data;
     int64_t seq_stride;   /* unused where tokens are numbered through */
