@@ -32,10 +32,11 @@
 // 1) times the queries' sums over the group, those in three bf16 parts (K); low
 // and scale against the probabilities (V).  So the products are exact up to the
 // rounding of p * scale to fp16 and, for the lows, of p to bf16; a query's
-// elements below 2^-27 of its row's largest are off by up to 2^-35 of that.
+// elements below 2^-27 of its row's largest are off by up to 2^-35 of that.  What
+// the fp16 steps are relative to is the query's own (kSpread).
 //
 // The running maximum moves only when a logit passes it by more than 8 (log2):
-// p stays below 2^8 and the rescaling almost never runs.
+// p stays below 2^8 and the rescaling almost never runs.  (4 bits: by more than 4.)
 //
 // Measured (one GB300, KV heads 8): 64 ragged sequences to 4224 rows, G = 5,
 // head_dim 128: 91.5 us, 6.3 TB/s; 256 of 1152, G = 4: 183 us, 6.6 TB/s; 16 ragged
@@ -77,6 +78,22 @@ template <int D>
 struct Stage32 {
     static constexpr int KEYS = 16, DEPTH = 2, ROW = D * 4, V = KEYS * ROW, BYTES = 2 * V;
 };
+
+// 4 bits: a probability times a scale goes to fp16, which holds 2^-14 .. 2^15 with
+// eleven bits.  So each query's sums are relative to its largest probability times
+// 2^e, e the exponent of the row's V (its largest |scale| or |low| is below 2^e), which
+// kAbove and kSlack keep between 2^11 and 2^15: what a row holds that the query
+// gives no weight, or does not see, counts nothing.  Where a row's groups are
+// no further apart than 2^kSpread (in bf16 bits), every group then has its largest
+// product above 2^2, and what fp16 cuts off below 2^-25 is 2^-24 of the group's
+// numbers a row, as much as an fp32 sum loses.  From a row on whose groups
+// are further apart (zeros, say), or whose exponent is not within kLeast ..
+// kMost, the queries that see it take the products in two bf16 parts, at any size.
+// (kMost - kLeast leaves the exponentials that join the warps' sums 2^-30 above what
+// they flush.)
+constexpr float kSlack = 4.f, kAbove = 11.f;
+constexpr uint32_t kSpread = 8 << 7;
+constexpr int kLeast = -40, kMost = 56;
 
 struct Params {
     const uint8_t* k;
@@ -241,6 +258,16 @@ RKV_DEV void centred(const Unpack& k, uint32_t w, uint32_t (&c)[4]) {
         c[2 * i] = *reinterpret_cast<const uint32_t*>(&lo);
         c[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&hi);
     }
+}
+
+// Small whole numbers in fp16 as bf16.
+RKV_DEV uint32_t f16_as_bf16(uint32_t x) {
+    const float2 f = __half22float2(as_half2(x));
+    return pack(f.x, f.y);
+}
+// What bf16 leaves of two numbers, as bf16: h is pack(lo, hi).
+RKV_DEV uint32_t pack_rest(float lo, float hi, uint32_t h) {
+    return pack(lo - __uint_as_float(h << 16), hi - __uint_as_float(h & 0xffff0000u));
 }
 
 // Physical row (within 16) of row r of a key fragment.  Quarter-warp reads of
@@ -437,18 +464,28 @@ RKV_DEV void values_bf16(uint32_t st, int base, const uint32_t (&pb)[NT][2], uin
     }
 }
 
-// The largest scale of row r of a 4-bit stage's V: its bf16 bits without sign.
+// The sizes of row r of a 4-bit stage's V, a group's being the larger of |scale|
+// and |low|: the bits of the largest (as bf16) and how far the smallest lies below.
 template <int D>
-RKV_DEV uint32_t top_scale(uint32_t st, int r) {
+RKV_DEV void row_sizes(uint32_t st, int r, uint32_t& top, uint32_t& spread) {
     using S = Stage<D, true>;
     const uint32_t row = st + S::vs() + r * S::SROW;
+    uint32_t most, least;  // of the groups with even and with odd numbers
     if constexpr (S::W == 4) {
         const uint4 x = lds16(row);
-        return max(max(x.x & 0x7fffu, x.y & 0x7fffu), max(x.z & 0x7fffu, x.w & 0x7fffu));
+        const uint32_t a = x.x & 0x7fff7fffu, b = x.y & 0x7fff7fffu;
+        const uint32_t c = x.z & 0x7fff7fffu, d = x.w & 0x7fff7fffu;
+        const uint32_t e = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+        const uint32_t f = __vmaxu2(__byte_perm(c, d, 0x5410), __byte_perm(c, d, 0x7632));
+        most = __vmaxu2(e, f);
+        least = __vminu2(e, f);
     } else {
         const uint2 x = lds8(row);
-        return max(x.x & 0x7fffu, x.y & 0x7fffu);
+        const uint32_t a = x.x & 0x7fff7fffu, b = x.y & 0x7fff7fffu;
+        most = least = __vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
     }
+    top = max(most & 0xffffu, most >> 16);
+    spread = top - min(least & 0xffffu, least >> 16);
 }
 
 // Whether row r of a stage holds an infinity or a NaN in V (4 bits: in its
@@ -468,11 +505,13 @@ RKV_DEV bool unfinite(uint32_t st, int r) {
 }
 
 // The same for a 4-bit stage but for the lows; p: probabilities of 16 keys as
-// accumulators lie.  MASKED: a hidden row's NaN stays out (some of the queries do
-// not see some of the rows).
-template <int D, int NT, bool MASKED>
+// accumulators lie.  MIXED: probabilities times scales in two bf16 parts instead of
+// fp16 (see kSpread) for the queries (columns) in `wide` (bit 2 n + i; every: for all
+// of the warp's), and a hidden row's NaN stays out (some of the queries do not see
+// some of the rows).
+template <int D, int NT, bool MIXED>
 RKV_DEV void values_q4(const Unpack& uk, uint32_t st, int base, const float (&p)[NT][4],
-                       float (&o)[D / 16][NT][4]) {
+                       uint32_t wide, bool every, float (&o)[D / 16][NT][4]) {
     using S = Stage<D, true>;
     constexpr int W = S::W;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -512,18 +551,44 @@ RKV_DEV void values_q4(const Unpack& uk, uint32_t st, int base, const float (&p)
         centred(uk, u, a);
         centred(uk, v, b);
         const float s[2] = {__uint_as_float(sc[0][w] * uk.up), __uint_as_float(sc[1][w] * uk.up)};
+        if (!MIXED || !every) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float y[4];
+            for (int n = 0; n < NT; ++n) {
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    y[i] = p[n][i] * s[i >> 1];
+                    if (MIXED && (p[n][i] == 0.f || ((wide >> (2 * n + (i & 1))) & 1u))) y[i] = 0.f;
+                }
+                const uint32_t b0 = transpose8x8(pack_f16(y[0], y[1]));
+                const uint32_t b1 = transpose8x8(pack_f16(y[2], y[3]));
+                mma_f16(o[2 * w][n], a[0], a[1], b[0], b[1], b0, b1);
+                mma_f16(o[2 * w + 1][n], a[2], a[3], b[2], b[3], b0, b1);
+            }
+        }
+        if constexpr (MIXED) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                y[i] = p[n][i] * s[i >> 1];
-                if (MASKED && p[n][i] == 0.f) y[i] = 0.f;
+                a[i] = f16_as_bf16(a[i]);
+                b[i] = f16_as_bf16(b[i]);
             }
-            const uint32_t b0 = transpose8x8(pack_f16(y[0], y[1]));
-            const uint32_t b1 = transpose8x8(pack_f16(y[2], y[3]));
-            mma_f16(o[2 * w][n], a[0], a[1], b[0], b[1], b0, b1);
-            mma_f16(o[2 * w + 1][n], a[2], a[3], b[2], b[3], b0, b1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    y[i] = p[n][i] * s[i >> 1];
+                    if (p[n][i] == 0.f || !((wide >> (2 * n + (i & 1))) & 1u)) y[i] = 0.f;
+                }
+                const uint32_t h0 = pack(y[0], y[1]), h1 = pack(y[2], y[3]);
+                const uint32_t b0 = transpose8x8(h0), b1 = transpose8x8(h1);
+                const uint32_t r0 = transpose8x8(pack_rest(y[0], y[1], h0));
+                const uint32_t r1 = transpose8x8(pack_rest(y[2], y[3], h1));
+                mma(o[2 * w][n], a[0], a[1], b[0], b[1], b0, b1);
+                mma(o[2 * w][n], a[0], a[1], b[0], b[1], r0, r1);
+                mma(o[2 * w + 1][n], a[2], a[3], b[2], b[3], b0, b1);
+                mma(o[2 * w + 1][n], a[2], a[3], b[2], b[3], r0, r1);
+            }
         }
     }
 }
@@ -1005,11 +1070,15 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
         const int all_see = len - p.T + row_first / p.G;  // rows up to this one are seen by all
 
         // m: running maximum of q . k; sums are relative to 2^ref: m * scale (0 while there is
-        // none).  4 bits: and to 2^(bound - 7), V's scales so far being below 2^bound, so that p *
-        // scale stays below 2^15 in fp16 and keeps eleven bits down to 2^-29 of that.
+        // none).  4 bits: of the logit, to base 2, plus the exponent of the row's V, and ref is
+        // m - kAbove, so that p * scale stays below 2^15 in fp16 (see kSpread).
         float m[NT][2], ref[NT][2], l[NT][2], o[D / 16][NT][4];
         [[maybe_unused]] float low[NT][4];
-        [[maybe_unused]] int bound = -60;
+        // the lane's queries whose products take two bf16 parts (bit 2 n + i), and whether some
+        // or all of the warp's do
+        constexpr uint32_t kMine = (1u << (2 * NT)) - 1u;
+        [[maybe_unused]] uint32_t wide = 0;
+        [[maybe_unused]] bool some = false, every = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -1055,30 +1124,52 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                                 x[kt][n][i] = -INFINITY;
                         }
             }
-            bool grow = false;
+            [[maybe_unused]] float ve[KT][2];  // 4 bits: exponents of V's rows g and g + 8
+            [[maybe_unused]] bool far = false;
+            if constexpr (Q4) {
+                uint32_t most, spread;
+                row_sizes<D>(st, lane, most, spread);
+                const int e = (int)(most >> 7) - 126;  // below 2^e
+                const float mine = (float)min(max(e, kLeast), kMost);
+                far = ((ok >> lane) & 1u) && (spread > kSpread || e < kLeast || e > kMost);
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        ve[kt][k] = __shfl_sync(0xffffffffu, mine, kt * 16 + phys<Q4>(g) + 8 * k);
+            }
+            bool grow = Q4 && far && !every;
             float top[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    top[n][i] = fmaxf(x[0][n][i], x[0][n][i + 2]);
+                    float y[KT][2];
+#pragma unroll
+                    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            y[kt][k] = Q4 ? fmaf(x[kt][n][i + 2 * k], sc[n][i], ve[kt][k])
+                                          : x[kt][n][i + 2 * k];
+                    top[n][i] = fmaxf(y[0][0], y[0][1]);
 #pragma unroll
                     for (int kt = 1; kt < KT; ++kt)
-                        top[n][i] = fmaxf(top[n][i], fmaxf(x[kt][n][i], x[kt][n][i + 2]));
-                    grow |= Q4 ? (top[n][i] - m[n][i]) * sc[n][i] > 8.f : top[n][i] > m[n][i] + p.slack;
+                        top[n][i] = fmaxf(top[n][i], fmaxf(y[kt][0], y[kt][1]));
+                    grow |= top[n][i] > m[n][i] + (Q4 ? kSlack : p.slack);
                 }
-            [[maybe_unused]] uint32_t most = 0;
-            if constexpr (Q4) {
-                most = top_scale<D>(st, lane);
-                grow |= (int)most >= ((bound + 127) << 7);
-            }
             if (__any_sync(0xffffffffu, grow)) {
                 if constexpr (Q4) {
-                    // (a scale that is not finite makes its own group's output NaN, no more)
-                    int e = most >= 0x7f80u ? 0 : (int)(most >> 7);
+                    const uint32_t rows = __ballot_sync(0xffffffffu, far);
+                    if (rows) {  // the queries that see one of them
+                        const int first = row0 + __ffs(rows) - 1;
 #pragma unroll
-                    for (int sh = 1; sh <= 16; sh <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, sh));
-                    bound = max(bound, min(e - 126, 100));
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (last[n][i] >= first) wide |= 1u << (2 * n + i);
+                        some = __any_sync(0xffffffffu, wide != 0);
+                        every = __all_sync(0xffffffffu, wide == kMine);
+                    }
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -1089,8 +1180,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                         const float base =
-                            mx == -INFINITY ? 0.f : mx * sc[n][i] + (Q4 ? (float)(bound - 7) : 0.f);
+                            mx == -INFINITY ? 0.f : (Q4 ? mx - kAbove : mx * sc[n][i]);
                         const float f = m[n][i] == -INFINITY ? 0.f : ex2(ref[n][i] - base);
+                        // 4 bits: a query's numbers are the same whatever the others see
+                        if (Q4 && !(mx > m[n][i] + kSlack)) continue;
                         m[n][i] = mx;
                         ref[n][i] = base;
                         l[n][i] *= f;
@@ -1131,18 +1224,22 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                 }
                 [[maybe_unused]] uint32_t la[2];
                 if constexpr (Q4) low_rows<D>(st, kt * 16, la);
+                if constexpr (Q4) {
+                    if (some || apart)
+                        values_q4<D, NT, true>(uk, st, kt * 16, x[kt], wide, every, o);
+                    else
+                        values_q4<D, NT, false>(uk, st, kt * 16, x[kt], 0u, false, o);
+                }
                 if (!apart) {
                     if constexpr (Q4) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
                             mma(low[n], la[0], 0u, la[1], 0u, pb[n][0], pb[n][1]);
-                        values_q4<D, NT, false>(uk, st, kt * 16, x[kt], o);
                     } else {
                         values_bf16<D, NT, false>(st, kt * 16, pb, ~0u, ~0u, ~0u, o);
                     }
                     continue;
                 }
-                if constexpr (Q4) values_q4<D, NT, true>(uk, st, kt * 16, x[kt], o);
                 // one token at a time
                 const int t0 = row_first / p.G;
                 const int t1 = (min(p.R, row_first + ROWS) - 1) / p.G;

@@ -454,9 +454,12 @@ int rkv_q4_read(const rkv_paged_desc* desc, const rkv_q4_cache* cache,
  * no block are recorded and skipped.  Sums, the softmax's statistics and the
  * output before its one rounding are fp32; for the second product a bf16 cache
  * rounds the probabilities to bf16, a 4-bit one probability times scale to
- * fp16 (scales from 2^-80 to 2^100 at full accuracy) and takes a query's
- * elements relative to its row's largest (exact down to 2^-27 of it, the others
- * to 2^-35 of it; magnitudes below 2^115).
+ * fp16 (in steps that follow the query's own largest such products; to two bf16
+ * parts where a row's groups lie more than 2^8 apart), so that a row which a
+ * query gives no weight, or does not see, may hold numbers of any size.  V's
+ * scales and lows count in full from 2^-100 to 2^100.  A 4-bit cache takes a
+ * query's elements relative to its row's largest (exact down to 2^-27 of it, the
+ * others to 2^-35 of it; magnitudes below 2^115).
  * q, out: rkv_rows by sequence and token (bf16 for 4-bit caches). */
 #define RKV_MAX_NEW_TOKENS 64
 size_t rkv_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int max_rows);

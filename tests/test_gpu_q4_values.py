@@ -1,0 +1,172 @@
+"""4-bit attention where the values of a sequence's rows are of very different
+sizes: each query's output follows the rows that have its weight, whatever the
+others hold (visible with hardly any weight, or seen by later tokens only).
+Bounds: tests/q4_ref.py."""
+import math
+
+import pytest
+import torch
+
+import decode_kv_cache_02_gb300 as pkg
+from decode_kv_cache_02_gb300 import rkv
+from tests import q4_ref
+from tests.test_gpu_cache import BF, DEV, gen, make_cache, rnd
+
+pytestmark = pytest.mark.gpu
+
+
+def scaled(cache, table, lens, exps):
+    """V's (scale, low) of row r of sequence s times 2^exps[s][r] (a number, or
+    one per group); every head alike."""
+    bs = cache.V_scales.shape[2]
+    sc = cache.V_scales.cpu().double()
+    tab = table.cpu()
+    for s, n in enumerate(lens):
+        for r in range(n):
+            f = 2.0 ** torch.as_tensor(exps[s][r], dtype=torch.float64)
+            sc[int(tab[s, r // bs]), :, r % bs] *= f.reshape(-1, 1)
+    cache.V_scales.copy_(sc.to(BF).to(DEV))
+
+
+def run(q, cache, table, lens, scale=None, max_rows=None):
+    """One call, checked; its output."""
+    d = q.shape[-1]
+    lens_d = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    ws = pkg.alloc_attention_workspace(q, cache.shape[1], max_rows or max(max(lens), 1))
+    out, lse = pkg.rkv_q4_attention(q, cache, table, lens_d, max_rows=max_rows or max(max(lens), 1),
+                                    scale=scale, lse=True, workspace=ws)
+    assert rkv.rkv_get_device_status(ws) == 0
+    q4_ref.check(q, cache, table, lens, 1 / math.sqrt(d) if scale is None else scale, out, lse)
+    return out
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_row_without_weight_may_be_large(d):
+    """One row with all of the weight and values around 1, one with weight 2^-200
+    (and 2^-40) and scales 2^30: the first row's values come out."""
+    cache, table, _ = make_cache(1, 1, d, 16, [2], "q4", 3, junk=False)
+    for far, big in ((-200.0, 2.0 ** 30), (-40.0, 2.0 ** 30), (-100.0, 2.0 ** 60)):
+        for order in (0, 1):
+            blk = int(table[0, 0])
+            cache.K_codes[blk] = 0
+            cache.K_scales[blk] = 0
+            cache.K_scales[blk, 0, 1 - order, 0, 1] = far  # low of group 0
+            cache.V_scales[blk, 0, order] = torch.tensor([2.0 ** -3, -1.0], dtype=BF, device=DEV)
+            cache.V_scales[blk, 0, 1 - order] = torch.tensor([big, -8 * big], dtype=BF, device=DEV)
+            q = torch.zeros(1, 1, 1, d, dtype=BF, device=DEV)
+            q[..., 0] = 1.0
+            run(q, cache, table, [2], scale=math.log(2.0))
+
+
+@pytest.mark.parametrize("case", [(64, 1, 3, 1), (128, 1, 5, 2), (128, 2, 16, 1), (64, 1, 32, 1),
+                                  (64, 8, 4, 2), (128, 4, 5, 1)],
+                         ids=lambda c: f"d{c[0]}T{c[1]}G{c[2]}H{c[3]}")
+@pytest.mark.parametrize("kind", ["rows", "groups", "hidden"])
+def test_values_of_any_size_side_by_side(case, kind):
+    """rows: each row's values times its own power of two, 2^-30 .. 2^30, with
+    logits as far apart; groups: each group's; hidden: what only later tokens see
+    is 2^20 .. 2^90 times larger."""
+    d, T, G, H = case
+    if kind == "hidden" and T == 1:
+        T, G = 4, min(G, 16)
+    G = min(G, 16)
+    lens = [300, 37, 5, 1700]
+    cache, table, _ = make_cache(len(lens), H, d, 16, lens, "q4", 40 + d, junk=False)
+    g = gen(d + T)
+    W = d // 32
+    if kind == "rows":
+        exps = [torch.randint(-30, 31, (n,), generator=g) for n in lens]
+    elif kind == "groups":
+        exps = [torch.randint(-20, 21, (n, W), generator=g) for n in lens]
+    else:
+        exps = []
+        for n in lens:
+            e = torch.zeros(n)
+            for i in range(1, T):
+                if n - i >= 0:
+                    e[n - i] = (20, 30, 40, 90)[i % 4]
+            exps.append(e)
+    scaled(cache, table, lens, exps)
+    q = rnd((len(lens), T, H * G, d), BF, 3)
+    if kind != "hidden":
+        q[:, :, ::2] *= 12  # half of the queries spread their logits over +-30 (base 2)
+    out = run(q, cache, table, lens)
+    if kind == "hidden":  # the first token sees none of them: ordinary numbers
+        assert (out[:, 0].abs() <= 64).all()
+
+
+def test_zero_rows_and_zero_groups():
+    """Rows and groups of zeros, and groups zero in all rows but some whose
+    weight is small."""
+    d, G, lens = 128, 4, [500, 64, 1]
+    cache, table, _ = make_cache(3, 2, d, 16, lens, "q4", 9, junk=False)
+    exps = [torch.zeros(n, 4) for n in lens]
+    scaled(cache, table, lens, exps)
+    sc = cache.V_scales
+    sc[:, :, ::3] = 0
+    sc[:, :, 1::3, 2] = 0
+    sc[:, :, :, 3] = 0
+    sc[int(table[0, 3]), :, 5, 3] = torch.tensor([0.5, -4.0], dtype=BF, device=DEV)
+    q = rnd((3, 1, 2 * G, d), BF, 3)
+    q[:, :, ::2] *= 10
+    run(q, cache, table, lens)
+
+
+@pytest.mark.parametrize("lens", [[500, 37], [9001], [8200, 3]], ids=lambda n: f"n{max(n)}")
+def test_all_values_large_or_small(lens):
+    """All rows' values at the ends of the stated range, alone or with a few rows
+    far from the rest; large constants."""
+    d, G = 128, 3
+    cache, table, _ = make_cache(len(lens), 1, d, 16, lens, "q4", 25, junk=False)
+    keep = cache.V_scales.clone()
+    q = rnd((len(lens), 1, G, d), BF, 3)
+    q[:, :, 0] *= 8
+    for k in (-100, -66, 60, 100):
+        cache.V_scales.copy_(keep)
+        scaled(cache, table, lens, [torch.full((n,), float(k)) for n in lens])
+        run(q, cache, table, lens)
+    for few, rest in ((50, -10), (-50, 10)):
+        cache.V_scales.copy_(keep)
+        scaled(cache, table, lens, [torch.where(torch.arange(n) % 97 == 5, few, rest) for n in lens])
+        run(q, cache, table, lens)
+    cache.V_scales.copy_(keep)
+    cache.V_scales[..., 0] = 0  # groups of one value each
+    cache.V_scales[..., 1] *= 2.0 ** 80
+    run(q, cache, table, lens)
+
+
+def test_few_rows_with_weight_among_many():
+    """One key with most of the weight and 4095 each 2^-11.6 as likely, at every
+    size of the values."""
+    d, n = 64, 4096
+    cache, table, _ = make_cache(1, 1, d, 64, [n], "q4", 31, junk=False)
+    cache.K_codes.zero_()
+    cache.K_scales.zero_()
+    blk, r = int(table[0, 2]), 7
+    cache.K_scales[blk, 0, r, 0, 1] = 11.625
+    q = torch.zeros(1, 1, 2, d, dtype=BF, device=DEV)
+    q[..., 0] = 1.0
+    keep = cache.V_scales.clone()
+    for k in (-100, -80, -60, 0, 60, 90):
+        cache.V_scales.copy_((keep.float() * 2.0 ** k).to(BF))
+        run(q, cache, table, [n], scale=math.log(2.0))
+
+
+@pytest.mark.parametrize("T", [2, 5, 8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_earlier_tokens_and_large_hidden_rows(d, T):
+    """The earlier tokens' outputs beside what only later ones see, ordinary or
+    2^20 .. 2^100 times larger: the same bits."""
+    lens, G = [37, 5, 130], 4
+    cache, table, _ = make_cache(3, 1, d, 16, lens, "q4", 5)
+    q = rnd((3, T, G, d), BF, 3)
+    clean = run(q, cache, table, lens)
+    keep = cache.V_scales.clone()
+    for k in (20, 30, 40, 100):
+        cache.V_scales.copy_(keep)
+        for s, n in enumerate(lens):
+            for r in (n - 1, n - 2)[:T - 1]:
+                cache.V_scales[int(table[s, r // 16]), :, r % 16] *= 2.0 ** k
+        out = run(q, cache, table, lens)
+        first = T - min(T - 1, 2)  # tokens that see none of them
+        assert torch.equal(clean[:, :first], out[:, :first])
