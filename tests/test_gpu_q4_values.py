@@ -10,7 +10,7 @@ import torch
 import decode_kv_cache_02_gb300 as pkg
 from decode_kv_cache_02_gb300 import rkv
 from tests import q4_ref
-from tests.test_gpu_cache import BF, DEV, gen, make_cache, rnd
+from tests.test_gpu_cache import ATTN_CASES, BF, DEV, gen, make_cache, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -170,3 +170,15 @@ def test_earlier_tokens_and_large_hidden_rows(d, T):
         out = run(q, cache, table, lens)
         first = T - min(T - 1, 2)  # tokens that see none of them
         assert torch.equal(clean[:, :first], out[:, :first])
+
+
+@pytest.mark.parametrize("case", ATTN_CASES, ids=lambda c: f"S{len(c[0])}n{max(c[0])}-T{c[1]}H{c[2]}G{c[3]}d{c[4]}bs{c[5]}")
+def test_attention_within_its_roundings(case):
+    """Ordinary numbers at every shape, each output against its own sum of
+    roundings (tests/test_q4_reference.py: a lost code bit or a lost share of the
+    rows is outside, at the long lengths too)."""
+    lens, T, H, G, d, bs = case
+    cache, table, _ = make_cache(len(lens), H, d, bs, lens, "q4", 11 + d)
+    q = rnd((len(lens), T, H * G, d), BF, 3, scale=1.5)
+    run(q, cache, table, lens, max_rows=(table.shape[1] - 1) * bs)
+    run(q, cache, table, lens, scale=0.3)
