@@ -406,11 +406,13 @@ int rkv_paged_append(const rkv_paged_desc* desc, const rkv_rope_plan* rope, void
                      const rkv_rows* q, const rkv_rows* out_q, void* workspace, void* stream);
 
 /* A paged cache held in 4 bits.  Each row of head_dim values is stored in
- * groups of 32 neighbours as x ~ scale * code + low:
+ * groups of 32 neighbours as x ~ scale * code + low, with t(x) the fp32 nearest
+ * to x - low:
  *   low   the largest bf16 that is not above the group's smallest value,
- *   scale the smallest bf16 that is not below (largest - low) / 15,
- *   code  the whole number nearest to (x - low) * r, r the fp32 nearest to
- *         1 / scale (0 where the scale is below 2^-126); halves go to even.
+ *   scale the smallest bf16 that is not below the fp32 nearest to
+ *         t(largest) / 15,
+ *   code  the whole number nearest to t(x) * r, r the fp32 nearest to 1 / scale
+ *         (0 where the scale is below 2^-126); halves go to even.
  * A group that holds a NaN or an infinity, or whose range passes the largest
  * float, reads as NaN.  codes [num_blocks, num_kv_heads, block_size,
  * head_dim / 2] bytes: with W = head_dim / 32, 16-bit word g * W + w of a row
