@@ -31,7 +31,7 @@
 // values enter through one more product each: (scale, low) as stored against (0,
 // 1) times the queries' sums over the group, those in three bf16 parts (K); low
 // and scale against the probabilities (V).  So the products are exact up to the
-// rounding of p * scale to fp16 and, for the lows, of p to bf16; a query's
+// rounding of p * scale to fp16 and, for the lows, of p (kTwoParts); a query's
 // elements below 2^-27 of its row's largest are off by up to 2^-35 of that.  What
 // the fp16 steps are relative to is the query's own (kSpread).
 //
@@ -94,6 +94,14 @@ struct Stage32 {
 constexpr float kSlack = 4.f, kAbove = 11.f;
 constexpr uint32_t kSpread = 8 << 7;
 constexpr int kLeast = -40, kMost = 56;
+
+// The probabilities meet a bf16 V, and the lows of a 4-bit one, as two bf16 parts,
+// 2^-16 of them off (one part: 2^-8), where a warp holds up to 16 queries: that costs
+// hardly anything there (us, one part against two: 64 ragged of 4224 92.5 / 92.6, 256
+// of 1152 182.4 / 183.6, 4 new tokens at head_dim 128 55.5 / 57.4, 4 bits 46.6 / 47.2).
+// With 32 queries it would cost an eighth (8 new tokens at head_dim 64 58.5 / 65.7, 64
+// sequences of them 59.0 / 70.5), and one part stays.
+template <int NT> constexpr bool kTwoParts = NT <= 2;
 
 struct Params {
     const uint8_t* k;
@@ -420,12 +428,14 @@ RKV_DEV void logits_q4(const Unpack& uk, uint32_t st, int base, const uint32_t (
     }
 }
 
-// O^T += V^T P^T for 16 keys of a bf16 stage; pb: P^T as operand.  ONE: only
-// for the queries (columns) in `cols` (bit 2 n + i), with the key pairs (2t,
-// 2t+1) and (2t+8, 2t+9) masked by keep0 and keep1 (a half each).
+// O^T += V^T P^T for 16 keys of a bf16 stage; pb: P^T as operand, pr: what bf16
+// leaves of it (kTwoParts).  ONE: only for the queries (columns) in `cols` (bit
+// 2 n + i), with the key pairs (2t, 2t+1) and (2t+8, 2t+9) masked by keep0 and
+// keep1 (a half each).
 template <int D, int NT, bool ONE>
-RKV_DEV void values_bf16(uint32_t st, int base, const uint32_t (&pb)[NT][2], uint32_t keep0,
-                         uint32_t keep1, uint32_t cols, float (&o)[D / 16][NT][4]) {
+RKV_DEV void values_bf16(uint32_t st, int base, const uint32_t (&pb)[NT][2],
+                         const uint32_t (&pr)[NT][2], uint32_t keep0, uint32_t keep1,
+                         uint32_t cols, float (&o)[D / 16][NT][4]) {
     using S = Stage<D, false>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t v = st + S::V;
@@ -451,14 +461,18 @@ RKV_DEV void values_bf16(uint32_t st, int base, const uint32_t (&pb)[NT][2], uin
                 for (int n = 0; n < NT; ++n) {
                     float y[4] = {0.f, 0.f, 0.f, 0.f};
                     mma(y, a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                    if constexpr (kTwoParts<NT>) mma(y, a0, a1, a2, a3, pr[n][0], pr[n][1]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if ((cols >> (2 * n + (i & 1))) & 1u) o[4 * j + e][n][i] += y[i];
                 }
             } else {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
                     mma(o[4 * j + e][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                    if constexpr (kTwoParts<NT>)
+                        mma(o[4 * j + e][n], a0, a1, a2, a3, pr[n][0], pr[n][1]);
+                }
             }
         }
     }
@@ -1217,11 +1231,16 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
                 uint32_t pb[NT][2];
+                [[maybe_unused]] uint32_t pr[NT][2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    pb[n][0] = transpose8x8(pack(x[kt][n][0], x[kt][n][1]));
-                    pb[n][1] = transpose8x8(pack(x[kt][n][2], x[kt][n][3]));
-                }
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float lo = x[kt][n][2 * i], hi = x[kt][n][2 * i + 1];
+                        const uint32_t h = pack(lo, hi);
+                        pb[n][i] = transpose8x8(h);
+                        if constexpr (kTwoParts<NT>) pr[n][i] = transpose8x8(pack_rest(lo, hi, h));
+                    }
                 [[maybe_unused]] uint32_t la[2];
                 if constexpr (Q4) low_rows<D>(st, kt * 16, la);
                 if constexpr (Q4) {
@@ -1233,10 +1252,13 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                 if (!apart) {
                     if constexpr (Q4) {
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                        for (int n = 0; n < NT; ++n) {
                             mma(low[n], la[0], 0u, la[1], 0u, pb[n][0], pb[n][1]);
+                            if constexpr (kTwoParts<NT>)
+                                mma(low[n], la[0], 0u, la[1], 0u, pr[n][0], pr[n][1]);
+                        }
                     } else {
-                        values_bf16<D, NT, false>(st, kt * 16, pb, ~0u, ~0u, ~0u, o);
+                        values_bf16<D, NT, false>(st, kt * 16, pb, pr, ~0u, ~0u, ~0u, o);
                     }
                     continue;
                 }
@@ -1264,12 +1286,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                         for (int n = 0; n < NT; ++n) {
                             float y[4] = {0.f, 0.f, 0.f, 0.f};
                             mma(y, la[0] & keep[0], 0u, la[1] & keep[1], 0u, pb[n][0], pb[n][1]);
+                            if constexpr (kTwoParts<NT>)
+                                mma(y, la[0] & keep[0], 0u, la[1] & keep[1], 0u, pr[n][0], pr[n][1]);
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
                                 if ((cols >> (2 * n + i)) & 1u) low[n][i] += y[i];
                         }
                     } else {
-                        values_bf16<D, NT, true>(st, kt * 16, pb, keep[0], keep[1], cols, o);
+                        values_bf16<D, NT, true>(st, kt * 16, pb, pr, keep[0], keep[1], cols, o);
                     }
                 }
             }
