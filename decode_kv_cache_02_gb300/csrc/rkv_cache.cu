@@ -1,7 +1,9 @@
 // rkv_cache.cu -- the C ABI of the cache in use (declared in include/rkv.h):
 // rotary plans, appends to paged and 4-bit caches, and attention over them.
 // Argument checks and the launch of k_tokens.cu and k_attention.cu; nothing
-// here allocates or synchronises, and no state is kept between calls.
+// here allocates or synchronises, and no state is kept between calls but on
+// which devices an attention kernel's shared memory has been asked for (the
+// runtime keeps that for every context of the device, also after a reset).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
