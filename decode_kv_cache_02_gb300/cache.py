@@ -364,7 +364,10 @@ def rkv_q4_read(cache: Q4Cache, block_table, lens, n_rows: int, first=None, out_
 
 def rkv_attention_workspace_size(q, num_kv_heads: int, max_rows: int) -> int:
     """Workspace bytes of rkv_paged_attention and rkv_q4_attention for q [S,
-    n_new, heads, d] over at most max_rows rows a sequence."""
+    n_new, heads, d] over at most max_rows rows a sequence, on q's device."""
+    if q.is_cuda and q.get_device() != _current_device():
+        with torch.cuda.device(q.device):
+            return rkv_attention_workspace_size(q, num_kv_heads, max_rows)
     H = int(num_kv_heads)
     if q.dim() != 4 or H < 1 or q.shape[2] == 0 or q.shape[2] % H:
         raise ValueError("q must be [num_seqs, n_new, H * gqa_group, d]")

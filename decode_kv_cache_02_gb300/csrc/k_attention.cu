@@ -1737,12 +1737,13 @@ AttnPlan attn_plan(const AttnArgs& a) {
     pl.unit = kWarps * (is_f32(a) ? 16 : (a.q4 ? Stage<128, true>::KEYS
                                                : (a.d == 128 ? Stage<128, false>::KEYS
                                                              : Stage<64, false>::KEYS)));
-    // as many blocks as 152 SMs hold at once: shared memory for two (one with
+    // as many blocks as the device's SMs hold at once: shared memory for two (one with
     // fp32 rows of 128), with 4-bit rows registers for three
-    const int blocks = 152 * (is_f32(a) && a.d == 128 ? 1 : (a.q4 && pl.rows == 8 ? 3 : 2));
+    const int sms = tc::sm_count();
+    const int blocks = sms * (is_f32(a) && a.d == 128 ? 1 : (a.q4 && pl.rows == 8 ? 3 : 2));
     const int64_t per = ((int64_t)a.max_rows + pl.unit - 1) / pl.unit, problems = a.num_seqs * a.pg.H;
     // a few short sequences: a cluster for each problem, one launch
-    if (!is_f32(a) && per > 1 && per <= kClusterUnits && problems * pl.groups * kCluster <= 304) {
+    if (!is_f32(a) && per > 1 && per <= kClusterUnits && problems * pl.groups * kCluster <= 2 * sms) {
         pl.cluster = per >= 5 ? 8 : (per >= 3 ? 4 : 2);
         pl.runs = (int)problems;
         return pl;

@@ -233,13 +233,17 @@ int check_attention(const rkv_paged_desc* desc, const int32_t* table, int n_new,
     return RKV_OK;
 }
 
+struct AttnCall {
+    AttnArgs args;
+    AttnPlan plan;
+};
 cudaError_t run_attention(const void* x, cudaStream_t s) {
-    const AttnArgs& a = *static_cast<const AttnArgs*>(x);
-    return rkv::launch_attention(a, rkv::attn_plan(a), s);
+    const AttnCall& c = *static_cast<const AttnCall*>(x);
+    return rkv::launch_attention(c.args, c.plan, s);
 }
 cudaError_t run_combine(const void* x, cudaStream_t s) {
-    const AttnArgs& a = *static_cast<const AttnArgs*>(x);
-    return rkv::launch_attention_combine(a, rkv::attn_plan(a), s);
+    const AttnCall& c = *static_cast<const AttnCall*>(x);
+    return rkv::launch_attention_combine(c.args, c.plan, s);
 }
 
 size_t attention_bytes(const AttnPlan& p) {
@@ -250,11 +254,13 @@ int attend(const rkv_paged_desc* desc, int n_new, const rkv_rows* q, const void*
            const void* V_pool, const rkv_q4_cache* cache, const int32_t* table,
            const int32_t* lens, int max_rows, float scale, const rkv_rows* out, float* lse,
            void* workspace, size_t workspace_bytes, void* stream, bool q4) {
-    AttnArgs a;
+    AttnCall call;
+    AttnArgs& a = call.args;
     int rc = check_attention(desc, table, n_new, max_rows, q4, &a);
     if (rc) return rc;
     if (!isfinite(scale)) return RKV_ERR_INVALID_ARG;
-    const AttnPlan pl = rkv::attn_plan(a);
+    call.plan = rkv::attn_plan(a);
+    const AttnPlan& pl = call.plan;
     // the kernel counts units and pool rows in 32 bits
     if (a.num_seqs * a.pg.H * ((int64_t)(max_rows - 1) / pl.unit + 1 + pl.lead) >=
             ((int64_t)1 << 31) ||
@@ -290,9 +296,9 @@ int attend(const rkv_paged_desc* desc, int n_new, const rkv_rows* q, const void*
     a.status = static_cast<DeviceStatus*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = rkv::timed_cache(q4 ? rkv::kCacheAttnQ4 : rkv::kCacheAttn, s, run_attention, &a);
+    cudaError_t e = rkv::timed_cache(q4 ? rkv::kCacheAttnQ4 : rkv::kCacheAttn, s, run_attention, &call);
     if (e == cudaSuccess && pl.join)
-        e = rkv::timed_cache(rkv::kCacheAttnCombine, s, run_combine, &a);
+        e = rkv::timed_cache(rkv::kCacheAttnCombine, s, run_combine, &call);
     return rc_of(e);
 }
 

@@ -102,6 +102,10 @@ private:
     bool pushed_;
 };
 
+namespace tc {
+int sm_count();  // of the current device
+}
+
 cudaError_t launch_key_stats(const ScoreArgs& a, cudaStream_t s);
 cudaError_t launch_importance(const ScoreArgs& a, cudaStream_t s);
 // *_shape_ok: the sizes and parameters a tensor-core kernel takes;

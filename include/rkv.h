@@ -466,6 +466,8 @@ int rkv_q4_read(const rkv_paged_desc* desc, const rkv_q4_cache* cache,
  * others to 2^-35 of it; magnitudes below 2^115).
  * q, out: rkv_rows by sequence and token (bf16 for 4-bit caches). */
 #define RKV_MAX_NEW_TOKENS 64
+/* Bytes for the current device (the work is cut for its SMs) and either cache;
+ * 0: invalid sizes. */
 size_t rkv_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int max_rows);
 int rkv_paged_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
                         const void* K_pool, const void* V_pool, const int32_t* block_table,
