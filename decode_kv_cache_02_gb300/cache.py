@@ -9,6 +9,9 @@ given, on that device's current stream.
 These calls run for every layer of every token, and a decode step's kernels
 take a few microseconds, so the common case (tensors on the current device, the
 current stream) takes no context manager, and descriptors are packed bytes.
+
+``rkv_rope_apply`` takes part in autograd.  The other calls have no gradient:
+what they write or return carries no history, whatever their inputs require.
 """
 from __future__ import annotations
 
@@ -144,13 +147,59 @@ class RopePlan:
         self.rot_dim = int(rot_dim)
 
 
+def _aligned(g):
+    """A gradient as rows the library takes (autograd hands out expanded ones)."""
+    if g.numel() == 0:
+        return g.new_empty(g.shape)
+    unit = 16 // g.element_size()
+    st = g.stride()
+    if st[-1] != 1 or any(x % unit for x in st[:-1]):
+        g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone(memory_format=torch.contiguous_format)
+
+
+class _Rotation(torch.autograd.Function):
+    """rkv_rope_apply with its gradient, which turns back (and has the same)."""
+
+    @staticmethod
+    def forward(ctx, rope, positions, inverse, q, k):
+        ctx.set_materialize_grads(False)
+        ctx.rope, ctx.inverse = rope, inverse
+        ctx.save_for_backward(positions)
+        out = rkv_rope_apply(rope, positions, q, k, inverse=inverse)
+        if k is not None and not q.requires_grad:
+            ctx.mark_non_differentiable(out[0])
+        elif k is not None and not k.requires_grad:
+            ctx.mark_non_differentiable(out[1])
+        return out
+
+    @staticmethod
+    def backward(ctx, gq, gk=None):
+        positions, = ctx.saved_tensors
+        gs = [_aligned(g) for g in (gq, gk) if g is not None]
+        if not gs:
+            return None, None, None, None, None
+        out = rkv_rope_apply(ctx.rope, positions, *gs, inverse=not ctx.inverse)
+        out = list(out) if len(gs) == 2 else [out]
+        return (None, None, None, None if gq is None else out.pop(0),
+                None if gk is None else out.pop(0))
+
+
 def rkv_rope_apply(rope: RopePlan, positions, q, k=None, out_q=None, out_k=None,
                    inverse: bool = False, stream=None):
     """q (and k) [tokens, heads, d] or [seqs, n, heads, d] turned by positions
     (int32, one per token); inverse=True turns back, the map of the gradients.
-    Outputs may be the inputs.  Returns out_q, or (out_q, out_k) with k."""
+    Outputs may be the inputs.  Returns out_q, or (out_q, out_k) with k.
+
+    Takes part in autograd where q or k requires a gradient (to q and k);
+    outputs of the caller's own are refused then (torch.no_grad() allows them)."""
     if _away(q, stream):
         return _elsewhere(rkv_rope_apply, q, stream, rope, positions, q, k, out_q, out_k, inverse)
+    if (q.requires_grad or (k is not None and k.requires_grad)) and torch.is_grad_enabled():
+        if out_q is not None or out_k is not None:
+            raise ValueError("out_q and out_k take no gradient: leave them out, or call under "
+                             "torch.no_grad()")
+        return _Rotation.apply(rope, positions, bool(inverse), q, k)
     dev = q.get_device()
     sh = q.shape
     if len(sh) == 3:
