@@ -25,6 +25,7 @@ from . import rkv as _rkv
 from .rkv import RKV_DTYPE_BF16, RKV_DTYPE_FP32, _Q4Cache, _RopeConfig, _RopePlan, _check
 
 RKV_MAX_NEW_TOKENS = 64
+_MAX_ROWS = 1 << 30  # of a sequence in an attention (past 31 bits an int would wrap on its way to C)
 _DTYPE = {torch.bfloat16: RKV_DTYPE_BF16, torch.float32: RKV_DTYPE_FP32}
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
@@ -421,7 +422,9 @@ def rkv_attention_workspace_size(q, num_kv_heads: int, max_rows: int) -> int:
     if q.dim() != 4 or H < 1 or q.shape[2] == 0 or q.shape[2] % H:
         raise ValueError("q must be [num_seqs, n_new, H * gqa_group, d]")
     S, T, hq, d = q.shape
-    desc = _pack_desc(S, H, hq // H, d, 1, 1, max(int(max_rows), 1), _dtype(q))
+    if not 0 < max_rows <= _MAX_ROWS:
+        raise ValueError("max_rows must be 1 .. 2^30")
+    desc = _pack_desc(S, H, hq // H, d, 1, 1, int(max_rows), _dtype(q))
     n = int(load().rkv_attention_workspace_size(desc, T, int(max_rows)))
     if n == 0:
         raise ValueError("invalid workspace request")
@@ -449,6 +452,8 @@ def _attention(call, where, cache_args, dev, shape, q, block_table, lens, max_ro
     mb = block_table.shape[1]
     dt = q.dtype
     max_rows = mb * bs if max_rows is None else int(max_rows)
+    if not 0 < max_rows <= _MAX_ROWS:
+        raise ValueError("max_rows (by default the table's rows) must be 1 .. 2^30")
     if out is None:
         out = torch.empty(sh, dtype=dt, device=q.device)
     at = None
