@@ -1093,6 +1093,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
         constexpr uint32_t kMine = (1u << (2 * NT)) - 1u;
         [[maybe_unused]] uint32_t wide = 0;
         [[maybe_unused]] bool some = false, every = false;
+        [[maybe_unused]] int bound = kLeast;  // the largest exponent of V's rows so far
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -1138,41 +1139,52 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                                 x[kt][n][i] = -INFINITY;
                         }
             }
-            [[maybe_unused]] float ve[KT][2];  // 4 bits: exponents of V's rows g and g + 8
+            bool grow = false;
             [[maybe_unused]] bool far = false;
+            [[maybe_unused]] int mine = 0;  // 4 bits: V's exponent of the lane's row
             if constexpr (Q4) {
                 uint32_t most, spread;
                 row_sizes<D>(st, lane, most, spread);
                 const int e = (int)(most >> 7) - 126;  // below 2^e
-                const float mine = (float)min(max(e, kLeast), kMost);
-                far = ((ok >> lane) & 1u) && (spread > kSpread || e < kLeast || e > kMost);
-#pragma unroll
-                for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        ve[kt][k] = __shfl_sync(0xffffffffu, mine, kt * 16 + phys<Q4>(g) + 8 * k);
+                mine = min(max(e, kLeast), kMost);
+                far = ((ok >> lane) & 1u) && (spread > kSpread || mine != e);
+                grow = (far && !every) || mine > bound;
             }
-            bool grow = Q4 && far && !every;
             float top[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float y[KT][2];
+                    top[n][i] = fmaxf(x[0][n][i], x[0][n][i + 2]);
+#pragma unroll
+                    for (int kt = 1; kt < KT; ++kt)
+                        top[n][i] = fmaxf(top[n][i], fmaxf(x[kt][n][i], x[kt][n][i + 2]));
+                    // (4 bits: no row of the stage is above this)
+                    grow |= Q4 ? fmaf(top[n][i], sc[n][i], (float)bound) > m[n][i] + kSlack
+                               : top[n][i] > m[n][i] + p.slack;
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+                if constexpr (Q4) {
+                    bound = max(bound, __reduce_max_sync(0xffffffffu, mine));
+                    float ve[KT][2];  // the exponents of rows g and g + 8
 #pragma unroll
                     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            y[kt][k] = Q4 ? fmaf(x[kt][n][i + 2 * k], sc[n][i], ve[kt][k])
-                                          : x[kt][n][i + 2 * k];
-                    top[n][i] = fmaxf(y[0][0], y[0][1]);
+                            ve[kt][k] = (float)__shfl_sync(0xffffffffu, mine,
+                                                           kt * 16 + phys<Q4>(g) + 8 * k);
 #pragma unroll
-                    for (int kt = 1; kt < KT; ++kt)
-                        top[n][i] = fmaxf(top[n][i], fmaxf(y[kt][0], y[kt][1]));
-                    grow |= top[n][i] > m[n][i] + (Q4 ? kSlack : p.slack);
-                }
-            if (__any_sync(0xffffffffu, grow)) {
-                if constexpr (Q4) {
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            top[n][i] = -INFINITY;
+#pragma unroll
+                            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k)
+                                    top[n][i] = fmaxf(top[n][i], fmaf(x[kt][n][i + 2 * k], sc[n][i],
+                                                                      ve[kt][k]));
+                        }
                     const uint32_t rows = __ballot_sync(0xffffffffu, far);
                     if (rows) {  // the queries that see one of them
                         const int first = row0 + __ffs(rows) - 1;
