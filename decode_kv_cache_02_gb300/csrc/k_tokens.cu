@@ -4,8 +4,9 @@
 //
 // Rotation: pair i of a head is turned by pos * f_i.  The plan holds f_i /
 // (2 pi) as a 64-bit fixed-point part of a turn, so the low 64 bits of
-// pos * turns[i] are the angle modulo one turn, exactly; the upper 32 of them,
-// read as a signed number, go through sincospif.
+// pos * turns[i] are the angle modulo one turn, exactly; the upper 32 of them go to
+// the nearest quarter turn in whole numbers and from there, at most pi / 4, through
+// the Taylor series of sine and cosine (sine_of: within 2 ulp).
 //
 // Every value is read and written once, 16 bytes (eight bf16) a step, so many
 // tokens are bound by HBM and a decode step by launch and load latency.  A

@@ -340,8 +340,9 @@ typedef struct {
  *             f_i (g + (1 - g) / factor)
  * m = attn_factor (1 leaves lengths alone).  The plan is host memory, made
  * once: it holds each f_i as a 64-bit fixed-point part of a turn, so pos * f_i
- * is reduced exactly whatever the position (the angle is off by less than
- * 2^-22 turns at position 2^31, by less than 2^-24 below 2^27). */
+ * is reduced exactly whatever the position (with angles of at most 1 radian a
+ * position the result is off by less than 2^-22 turns at position 2^31, by less
+ * than 2^-24 below 2^27; larger angles of a caller's own in proportion). */
 enum {
     RKV_ROPE_NONE = 0,
     RKV_ROPE_LINEAR = 1,
@@ -447,7 +448,7 @@ int rkv_q4_read(const rkv_paged_desc* desc, const rkv_q4_cache* cache,
  * sequence over its cache: token t sees rows j <= lens[s] - n_new + t,
  *   out[s, t, head] = sum_j p_j V_j,  p = softmax_j(scale * q . K_j)
  * with query heads h * gqa_group .. of KV head h.  A token that sees no row
- * (lens[s] < n_new, or 0) gets zeros.  lse, unless NULL, receives
+ * (lens[s] < n_new, or 0), or only rows whose logits are -inf, gets zeros.  lse, unless NULL, receives
  * log(sum_j exp(scale * q . K_j)) [num_seqs, n_new, heads] fp32 (-inf where
  * nothing is seen).  Rows at or past lens[s] may hold anything, and what a row
  * holds that only the later of the new tokens see stays out of the earlier
