@@ -31,7 +31,7 @@
 // values enter through one more product each: (scale, low) as stored against (0,
 // 1) times the queries' sums over the group, those in three bf16 parts (K); low
 // and scale against the probabilities (V).  So the products are exact up to the
-// rounding of p * scale to fp16 and, for the lows, of p (kTwoParts); a query's
+// rounding of p * scale to fp16 and, for the lows, of p (kTwoQueries); a query's
 // elements below 2^-27 of its row's largest are off by up to 2^-35 of that.  What
 // the fp16 steps are relative to is the query's own (kSpread).
 //
@@ -39,11 +39,13 @@
 // p stays below 2^8 and the rescaling almost never runs.  (4 bits: by more than 4.)
 //
 // Measured (one GB300, KV heads 8): 64 ragged sequences to 4224 rows, G = 5,
-// head_dim 128: 91.5 us, 6.3 TB/s; 256 of 1152, G = 4: 183 us, 6.6 TB/s; 16 ragged
-// to 16389 with 8 new tokens, head_dim 64: 59.5 us, 5.2 TB/s (copies alone, before
-// its launch overlapped what was there: 55); one of 1152: 6.1 us.  4 bits: one
-// of 131071, G = 5: 43.6 us, 3.9 TB/s, 365 instructions a warp for 16 rows at 0.59
-// a cycle of an SM quarter, of whose cycles the logic pipe takes 47 in a hundred.
+// head_dim 128: 91.4 us, 6.3 TB/s; 256 of 1152, G = 4: 184 us, 6.6 TB/s; 16 ragged
+// to 16389 with 8 new tokens, head_dim 64: 59.6 us, 5.2 TB/s (copies alone, before
+// its launch overlapped what was there: 55); one of 1152: 6.0 us.  4 bits: one
+// of 131071, G = 5: 46.6 us, 3.6 TB/s.  In steady state a warp spends 378 instructions
+// and an SM quarter 591 cycles on 16 rows, where HBM's rate would allow 435: no pipe is
+// above 55 in a hundred of them (logic; issue slots 64), the twelve warps of an SM
+// wait for their own last instructions.
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -95,13 +97,14 @@ constexpr float kSlack = 4.f, kAbove = 11.f;
 constexpr uint32_t kSpread = 8 << 7;
 constexpr int kLeast = -40, kMost = 56;
 
-// The probabilities meet a bf16 V, and the lows of a 4-bit one, as two bf16 parts,
-// 2^-16 of them off (one part: 2^-8), where a warp holds up to 16 queries: that costs
-// hardly anything there (us, one part against two: 64 ragged of 4224 92.5 / 92.6, 256
-// of 1152 182.4 / 183.6, 4 new tokens at head_dim 128 55.5 / 57.4, 4 bits 46.6 / 47.2).
-// With 32 queries it would cost an eighth (8 new tokens at head_dim 64 58.5 / 65.7, 64
-// sequences of them 59.0 / 70.5), and one part stays.
-template <int NT> constexpr bool kTwoParts = NT <= 2;
+// The probabilities meet a bf16 V, and the lows of a 4-bit one, as two bf16 parts
+// (TWO), 2^-16 of them off (one part: 2^-8), where a KV head has up to 16 queries, so
+// that the rows are read once and waited for: that costs hardly anything (us, one
+// part against two: 64 ragged of 4224 92.5 / 92.6, 256 of 1152 182.4 / 183.6, 16
+// queries at head_dim 128 91.3 / 93.2, 4 bits 46.6 / 47.2).  With more queries the
+// products count: 8 new tokens at head_dim 64 58.5 / 65.7, at 128 99.7 / 120.7, 64 of
+// them 2550 / 3197, and one part stays.
+constexpr int kTwoQueries = 16;
 
 struct Params {
     const uint8_t* k;
@@ -429,10 +432,10 @@ RKV_DEV void logits_q4(const Unpack& uk, uint32_t st, int base, const uint32_t (
 }
 
 // O^T += V^T P^T for 16 keys of a bf16 stage; pb: P^T as operand, pr: what bf16
-// leaves of it (kTwoParts).  ONE: only for the queries (columns) in `cols` (bit
+// leaves of it (TWO).  ONE: only for the queries (columns) in `cols` (bit
 // 2 n + i), with the key pairs (2t, 2t+1) and (2t+8, 2t+9) masked by keep0 and
 // keep1 (a half each).
-template <int D, int NT, bool ONE>
+template <int D, int NT, bool TWO, bool ONE>
 RKV_DEV void values_bf16(uint32_t st, int base, const uint32_t (&pb)[NT][2],
                          const uint32_t (&pr)[NT][2], uint32_t keep0, uint32_t keep1,
                          uint32_t cols, float (&o)[D / 16][NT][4]) {
@@ -461,7 +464,7 @@ RKV_DEV void values_bf16(uint32_t st, int base, const uint32_t (&pb)[NT][2],
                 for (int n = 0; n < NT; ++n) {
                     float y[4] = {0.f, 0.f, 0.f, 0.f};
                     mma(y, a0, a1, a2, a3, pb[n][0], pb[n][1]);
-                    if constexpr (kTwoParts<NT>) mma(y, a0, a1, a2, a3, pr[n][0], pr[n][1]);
+                    if constexpr (TWO) mma(y, a0, a1, a2, a3, pr[n][0], pr[n][1]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if ((cols >> (2 * n + (i & 1))) & 1u) o[4 * j + e][n][i] += y[i];
@@ -470,7 +473,7 @@ RKV_DEV void values_bf16(uint32_t st, int base, const uint32_t (&pb)[NT][2],
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     mma(o[4 * j + e][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-                    if constexpr (kTwoParts<NT>)
+                    if constexpr (TWO)
                         mma(o[4 * j + e][n], a0, a1, a2, a3, pr[n][0], pr[n][1]);
                 }
             }
@@ -936,7 +939,7 @@ RKV_DEV void finish_cluster(const Params& p, float* acc, const float (&sh_m)[kWa
 }
 
 // NT * 8 queries of a KV head's group against a run of rows.
-template <int D, int NT, bool Q4>
+template <int D, int NT, bool Q4, bool TWO>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kernel(const __grid_constant__ Params p) {
     using S = Stage<D, Q4>;
     constexpr int ROWS = 8 * NT, W = D / 32, KT = S::KEYS / 16, UNIT = kWarps * S::KEYS;
@@ -1251,7 +1254,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                         const float lo = x[kt][n][2 * i], hi = x[kt][n][2 * i + 1];
                         const uint32_t h = pack(lo, hi);
                         pb[n][i] = transpose8x8(h);
-                        if constexpr (kTwoParts<NT>) pr[n][i] = transpose8x8(pack_rest(lo, hi, h));
+                        if constexpr (TWO) pr[n][i] = transpose8x8(pack_rest(lo, hi, h));
                     }
                 [[maybe_unused]] uint32_t la[2];
                 if constexpr (Q4) low_rows<D>(st, kt * 16, la);
@@ -1266,11 +1269,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             mma(low[n], la[0], 0u, la[1], 0u, pb[n][0], pb[n][1]);
-                            if constexpr (kTwoParts<NT>)
+                            if constexpr (TWO)
                                 mma(low[n], la[0], 0u, la[1], 0u, pr[n][0], pr[n][1]);
                         }
                     } else {
-                        values_bf16<D, NT, false>(st, kt * 16, pb, pr, ~0u, ~0u, ~0u, o);
+                        values_bf16<D, NT, TWO, false>(st, kt * 16, pb, pr, ~0u, ~0u, ~0u, o);
                     }
                     continue;
                 }
@@ -1298,14 +1301,14 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                         for (int n = 0; n < NT; ++n) {
                             float y[4] = {0.f, 0.f, 0.f, 0.f};
                             mma(y, la[0] & keep[0], 0u, la[1] & keep[1], 0u, pb[n][0], pb[n][1]);
-                            if constexpr (kTwoParts<NT>)
+                            if constexpr (TWO)
                                 mma(y, la[0] & keep[0], 0u, la[1] & keep[1], 0u, pr[n][0], pr[n][1]);
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
                                 if ((cols >> (2 * n + i)) & 1u) low[n][i] += y[i];
                         }
                     } else {
-                        values_bf16<D, NT, true>(st, kt * 16, pb, pr, keep[0], keep[1], cols, o);
+                        values_bf16<D, NT, TWO, true>(st, kt * 16, pb, pr, keep[0], keep[1], cols, o);
                     }
                 }
             }
@@ -1685,12 +1688,12 @@ cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
     return e;
 }
 
-template <int D, int NT, bool Q4>
+template <int D, int NT, bool Q4, bool TWO>
 cudaError_t go(const Params& p, unsigned ctas, cudaStream_t s) {
     using S = Stage<D, Q4>;
     constexpr int ring = kWarps * S::DEPTH * S::BYTES, join = kWarps * 8 * NT * D * 4;
     constexpr int bytes = ring > join ? ring : join;
-    auto kern = attn_kernel<D, NT, Q4>;
+    auto kern = attn_kernel<D, NT, Q4, TWO>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kern, bytes, done);
     if (e != cudaSuccess) return e;
@@ -1712,9 +1715,12 @@ cudaError_t go(const Params& p, unsigned ctas, cudaStream_t s) {
 }
 template <bool Q4>
 cudaError_t go(const Params& p, int d, int rows, unsigned ctas, cudaStream_t s) {
-    if (d == 128) return rows == 8 ? go<128, 1, Q4>(p, ctas, s) : go<128, 2, Q4>(p, ctas, s);
-    return rows == 8 ? go<64, 1, Q4>(p, ctas, s)
-                     : (rows == 16 ? go<64, 2, Q4>(p, ctas, s) : go<64, 4, Q4>(p, ctas, s));
+    if (d == 128 && p.R > kTwoQueries) return go<128, 2, Q4, false>(p, ctas, s);
+    if (d == 128)
+        return rows == 8 ? go<128, 1, Q4, true>(p, ctas, s) : go<128, 2, Q4, true>(p, ctas, s);
+    return rows == 8 ? go<64, 1, Q4, true>(p, ctas, s)
+                     : (rows == 16 ? go<64, 2, Q4, true>(p, ctas, s)
+                                   : go<64, 4, Q4, false>(p, ctas, s));
 }
 template <int D>
 cudaError_t go32(const Params& p, unsigned ctas, cudaStream_t s) {

@@ -457,7 +457,7 @@ int rkv_q4_read(const rkv_paged_desc* desc, const rkv_q4_cache* cache,
  * no block are recorded and skipped.  Sums, the softmax's statistics and the
  * output before its one rounding are fp32; for the second product a bf16 cache
  * takes the probabilities as two bf16 parts, to 2^-16 of them (as one, to 2^-8,
- * where head_dim is 64 and n_new * gqa_group above 16), a 4-bit one those of the
+ * where n_new * gqa_group is above 16), a 4-bit one those of the
  * lows too and probability times scale in
  * fp16 (in steps that follow the query's own largest such products; to two bf16
  * parts where a row's groups lie more than 2^8 apart), so that a row which a

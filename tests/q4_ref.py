@@ -14,8 +14,7 @@ With P_j the softmax's weights and a group's values s (c - 8) + (low + 8 s):
   largest, and that a factor 2 below its power of two, else the product takes
   two bf16 parts, 2^-16): N 2^-24 max_j P_j g_j with g_j = max(s, |low|).
 - the weights of (scale, low) are taken as two bf16 parts, 2^-16, or, with more
-  than 16 queries a KV head at head_dim 64, as one, half a step 2^-8; they meet
-  low + 8 s.
+  than 16 queries a KV head, as one, half a step 2^-8; they meet low + 8 s.
 - sums in fp32 over a warp's quarter of the rows, and their joins: each step off
   by 2^-23 (the tensor core's additions may cut), (rows / 2 + 128) 2^-24 of
   sum P (s |c - 8| + |low| + 8 s).
@@ -75,7 +74,7 @@ def attention(q, K, V, lens, scale):
             b = b + UH * (P @ codes)
             g = wide(torch.maximum(vs, vl.abs()))  # [H, see, d]
             b = b + see * 2.0 ** -24 * (P[..., None] * g[:, None]).amax(2)
-            b = b + (U16 if d == 64 and T * G > 16 else 2.0 ** -16) * (P @ wide((vl + 8 * vs).abs()))
+            b = b + (U16 if T * G > 16 else 2.0 ** -16) * (P @ wide((vl + 8 * vs).abs()))
             b = b + (see / 2 + 128) * U32 * (P @ (codes + wide(vl.abs() + 8 * vs)))
             b = b + U16 * (o.abs() + b) + 1e-37
             out[s, t], bound[s, t] = o.reshape(Hq, d), b.reshape(Hq, d)

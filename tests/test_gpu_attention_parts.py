@@ -20,7 +20,7 @@ CASES = [
     ([700, 1025, 64], 1, 3, 5, 128, 128),
     ([333, 40], 1, 2, 16, 128, 64),
     ([333, 1, 40], 1, 1, 16, 64, 256),
-    ([3, 0, 1, 257], 4, 1, 5, 128, 8),
+    ([3, 0, 1, 257], 3, 1, 5, 128, 8),
     ([9001], 4, 1, 4, 64, 16),
     ([8200, 3], 8, 2, 2, 128, 128),
 ]
