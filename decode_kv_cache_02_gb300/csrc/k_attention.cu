@@ -47,6 +47,7 @@
 // above 55 in a hundred of them (logic; issue slots 64), the twelve warps of an SM
 // wait for their own last instructions.
 #include <cuda_fp16.h>
+#include <float.h>
 
 #include <atomic>
 
@@ -59,6 +60,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNone = -FLT_MAX, kUnset = 1e30f;  // no maximum yet
+constexpr float kHuge = 0x1p20f;
 
 // Bytes and rows of one stage of a warp's ring.
 template <int D, bool Q4>
@@ -794,6 +797,53 @@ RKV_DEV float weight(float m, float l, float mx) {
     if (m == -INFINITY) return l != l ? 1.f : 0.f;
     return ex2(m - mx);
 }
+// The base-2 logit m * scale - up in fp32 (-inf: none), and 2^ what that rounding
+// left of it.  Where the product's own rounding is past 32 it is left out: it is the
+// same for the parts of a problem that found the same maximum, and others are as far
+// apart as it is coarse.
+RKV_DEV float base_of(float m, float scale, float up, float& fix) {
+    fix = 1.f;
+    if (m == kNone || up == kUnset) return -INFINITY;
+    const float z = __fmul_rn(m, scale), base = z - up, rest = fmaf(m, scale, -z);
+    if (fabsf(z) <= FLT_MAX) fix = ex2((z - base) - up + (fabsf(rest) <= 32.f ? rest : 0.f));
+    return base;
+}
+// 4 bits: logits q . k less their queries' m, after a step of m to the stage's maximum
+// where that is past kHuge from it (up with it, so that the sums keep their
+// reference).  Whether some query has an m.
+template <int KT, int NT>
+RKV_DEV bool take_m(float (&x)[KT][NT][4], const float (&top)[NT][2], const float (&sc)[NT][2],
+                    float (&m)[NT][2], float (&up)[NT][2], bool huge) {
+    bool past = huge;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float z = top[n][i] * sc[n][i];
+            past |= z > kHuge || (z < -kHuge && z >= -FLT_MAX && up[n][i] == kUnset);
+        }
+    if (!__any_sync(0xffffffffu, past)) return false;
+    past = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float mx = top[n][i] - m[n][i];
+#pragma unroll
+            for (int sh = 4; sh <= 16; sh <<= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+            const float z = mx * sc[n][i], old = m[n][i];
+            const bool step = fabsf(z) <= FLT_MAX && (up[n][i] == kUnset ? fabsf(z) : z) > kHuge;
+            if (step) m[n][i] = old + mx;
+            if (step && up[n][i] != kUnset) up[n][i] += (m[n][i] - old) * sc[n][i];
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) x[kt][n][i + 2 * k] -= m[n][i];
+            past |= m[n][i] != 0.f;
+        }
+    return __any_sync(0xffffffffu, past);
+}
 template <int ROWS>
 RKV_DEV float row_max(const float (&sh_m)[kWarps][ROWS], int r) {
     float mx = sh_m[0][r];
@@ -1086,23 +1136,30 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
             }
         const int all_see = len - p.T + row_first / p.G;  // rows up to this one are seen by all
 
-        // m: running maximum of q . k; sums are relative to 2^ref: m * scale (0 while there is
-        // none).  4 bits: of the logit, to base 2, plus the exponent of the row's V, and ref is
-        // m - kAbove, so that p * scale stays below 2^15 in fp16 (see kSpread).
-        float m[NT][2], ref[NT][2], l[NT][2], o[D / 16][NT][4];
+        // m: running maximum of q . k (kNone: none yet); sums are relative to 2^(m * scale).
+        // Differences of q . k are scaled, not scaled logits subtracted: those are as coarse as
+        // fp32 is at their size.  4 bits: sums are relative to 2^(m * scale - up), up being kAbove
+        // less the largest of (q . k - m) * scale plus the exponent of the row's V (kUnset: none
+        // yet), so that p * scale stays below 2^15 in fp16 (see kSpread); m is 0 but where
+        // logits past kHuge make a difference of it (the subtraction would cost 2 in a
+        // hundred).
+        float m[NT][2], l[NT][2], o[D / 16][NT][4];
+        [[maybe_unused]] float up[NT][2];
         [[maybe_unused]] float low[NT][4];
         // the lane's queries whose products take two bf16 parts (bit 2 n + i), and whether some
         // or all of the warp's do
         constexpr uint32_t kMine = (1u << (2 * NT)) - 1u;
         [[maybe_unused]] uint32_t wide = 0;
         [[maybe_unused]] bool some = false, every = false;
+        [[maybe_unused]] bool huge = false;  // some query of the warp's has an m
         [[maybe_unused]] int bound = kLeast;  // the largest exponent of V's rows so far
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                m[n][i] = -INFINITY;
-                ref[n][i] = l[n][i] = 0.f;
+                m[n][i] = Q4 ? 0.f : kNone;
+                l[n][i] = 0.f;
+                if constexpr (Q4) up[n][i] = kUnset;
             }
 #pragma unroll
             for (int e = 0; e < D / 16; ++e)
@@ -1151,7 +1208,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                 const int e = (int)(most >> 7) - 126;  // below 2^e
                 mine = min(max(e, kLeast), kMost);
                 far = ((ok >> lane) & 1u) && (spread > kSpread || mine != e);
-                grow = (far && !every) || mine > bound;
+                grow = (far && !every) || mine > bound || huge;
             }
             float top[NT][2];
 #pragma unroll
@@ -1163,31 +1220,21 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                     for (int kt = 1; kt < KT; ++kt)
                         top[n][i] = fmaxf(top[n][i], fmaxf(x[kt][n][i], x[kt][n][i + 2]));
                     // (4 bits: no row of the stage is above this)
-                    grow |= Q4 ? fmaf(top[n][i], sc[n][i], (float)bound) > m[n][i] + kSlack
-                               : top[n][i] > m[n][i] + p.slack;
+                    if constexpr (Q4)
+                        grow |= fmaf(top[n][i], sc[n][i], (float)bound) > kAbove + kSlack - up[n][i];
+                    else
+                        grow |= top[n][i] > m[n][i] + p.slack;
                 }
             if (__any_sync(0xffffffffu, grow)) {
+                [[maybe_unused]] float ve[KT][2];  // 4 bits: the exponents of rows g and g + 8
                 if constexpr (Q4) {
                     bound = max(bound, __reduce_max_sync(0xffffffffu, mine));
-                    float ve[KT][2];  // the exponents of rows g and g + 8
 #pragma unroll
                     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
                             ve[kt][k] = (float)__shfl_sync(0xffffffffu, mine,
                                                            kt * 16 + phys<Q4>(g) + 8 * k);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            top[n][i] = -INFINITY;
-#pragma unroll
-                            for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                                for (int k = 0; k < 2; ++k)
-                                    top[n][i] = fmaxf(top[n][i], fmaf(x[kt][n][i + 2 * k], sc[n][i],
-                                                                      ve[kt][k]));
-                        }
                     const uint32_t rows = __ballot_sync(0xffffffffu, far);
                     if (rows) {  // the queries that see one of them
                         const int first = row0 + __ffs(rows) - 1;
@@ -1200,21 +1247,32 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                         every = __all_sync(0xffffffffu, wide == kMine);
                     }
                 }
+                if constexpr (Q4) huge = take_m<KT, NT>(x, top, sc, m, up, huge);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float mx = fmaxf(m[n][i], top[n][i]);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float base =
-                            mx == -INFINITY ? 0.f : (Q4 ? mx - kAbove : mx * sc[n][i]);
-                        const float f = m[n][i] == -INFINITY ? 0.f : ex2(ref[n][i] - base);
-                        // 4 bits: a query's numbers are the same whatever the others see
-                        if (Q4 && !(mx > m[n][i] + kSlack)) continue;
-                        m[n][i] = mx;
-                        ref[n][i] = base;
+                        float mx = Q4 ? -INFINITY : fmaxf(m[n][i], top[n][i]);
+                        if constexpr (Q4)
+#pragma unroll
+                            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k)
+                                    mx = fmaxf(mx, fmaf(x[kt][n][i + 2 * k], sc[n][i], ve[kt][k]));
+#pragma unroll
+                        for (int sh = 4; sh <= 16; sh <<= 1)
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+                        float f;
+                        if constexpr (Q4) {
+                            // a query's numbers are the same whatever the others see
+                            const float old = kAbove - up[n][i];
+                            if (!(mx > old + kSlack)) continue;
+                            f = up[n][i] == kUnset ? 0.f : ex2(old - mx);
+                            up[n][i] = kAbove - mx;
+                        } else {
+                            f = m[n][i] == kNone ? 0.f : ex2((m[n][i] - mx) * sc[n][i]);
+                            m[n][i] = mx;
+                        }
                         l[n][i] *= f;
 #pragma unroll
                         for (int e = 0; e < D / 16; ++e) {
@@ -1230,8 +1288,11 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int kt = 0; kt < KT; ++kt) {
-                        x[kt][n][i] = ex2(fmaf(x[kt][n][i], sc[n][i], -ref[n][i]));
-                        x[kt][n][i + 2] = ex2(fmaf(x[kt][n][i + 2], sc[n][i], -ref[n][i]));
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float& z = x[kt][n][i + 2 * k];
+                            z = ex2(Q4 ? fmaf(z, sc[n][i], up[n][i]) : (z - m[n][i]) * sc[n][i]);
+                        }
                         l[n][i] += x[kt][n][i] + x[kt][n][i + 2];
                     }
             // rows that only some of the tokens see: an infinity or a NaN there must not reach
@@ -1317,7 +1378,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
         cp_wait<0>();
         if (place.u0 >= place.u1) let_next_begin();
 
-        // sums over the lanes that share a query
+        // sums over the lanes that share a query; from here on m is the base-2 logit that they are
+        // relative to, fix what its rounding left
+        float fix[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1325,7 +1388,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
 #pragma unroll
                 for (int sh = 4; sh <= 16; sh <<= 1)
                     l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], sh);
-                m[n][i] = m[n][i] == -INFINITY ? m[n][i] : ref[n][i];  // from here on: base-2 logits
+                m[n][i] = base_of(m[n][i], sc[n][i], Q4 ? up[n][i] : 0.f, fix[n][i]);
+                l[n][i] *= fix[n][i];
                 if (g == 0) {
                     sh_m[warp][8 * n + 2 * t + i] = m[n][i];
                     sh_l[warp][8 * n + 2 * t + i] = l[n][i];
@@ -1338,7 +1402,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = 8 * n + 2 * t + i;
-                const float f = weight(m[n][i], l[n][i], row_max(sh_m, r));
+                const float f = weight(m[n][i], l[n][i], row_max(sh_m, r)) * fix[n][i];
                 float* dst = acc + ((size_t)warp * ROWS + r) * D;
                 [[maybe_unused]] float add[W];
                 if constexpr (Q4)
@@ -1412,12 +1476,12 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
         }
         __syncthreads();
         int last[ROWS];
-        float m[ROWS], ref[ROWS], l[ROWS], o[ROWS][4];
+        float m[ROWS], l[ROWS], o[ROWS][4];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             last[r] = row_first + r < p.R ? c.len - p.T + (row_first + r) / p.G : c.len - 1;
-            m[r] = -INFINITY;
-            ref[r] = l[r] = 0.f;
+            m[r] = kNone;
+            l[r] = 0.f;
             o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
         }
         const int all_see = c.len - p.T + row_first / p.G;
@@ -1490,9 +1554,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
 #pragma unroll
                 for (int r = 0; r < ROWS; ++r) {
                     const float mx = fmaxf(m[r], warp_max(x[r]));
-                    const float f = m[r] == -INFINITY ? 0.f : ex2((m[r] - mx) * p.scale);
+                    const float f = m[r] == kNone ? 0.f : ex2((m[r] - mx) * p.scale);
                     m[r] = mx;
-                    ref[r] = mx == -INFINITY ? 0.f : mx * p.scale;
                     l[r] *= f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[r][i] *= f;
@@ -1500,7 +1563,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
             }
 #pragma unroll
             for (int r = 0; r < ROWS; ++r) {
-                x[r] = ex2(fmaf(x[r], p.scale, -ref[r]));
+                x[r] = ex2((x[r] - m[r]) * p.scale);
                 if (side == 0) l[r] += x[r];
             }
             if (side == 0) {
@@ -1527,10 +1590,11 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
             }
         }
         cp_wait<0>();
+        float fix[ROWS];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            l[r] = warp_sum(l[r]);
-            m[r] = m[r] == -INFINITY ? m[r] : ref[r];  // from here on: base-2 logits
+            m[r] = base_of(m[r], p.scale, 0.f, fix[r]);  // from here on: base-2 logits
+            l[r] = warp_sum(l[r]) * fix[r];
             if (lane == 0) {
                 sh_m[warp][r] = m[r];
                 sh_l[warp][r] = l[r];
@@ -1543,7 +1607,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
         float* acc = reinterpret_cast<float*>(smem);
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            const float f = weight(m[r], l[r], row_max(sh_m, r));
+            const float f = weight(m[r], l[r], row_max(sh_m, r)) * fix[r];
             if (lane < UPR)
                 *reinterpret_cast<float4*>(acc + ((size_t)warp * ROWS + r) * D + 4 * lane) =
                     make_float4(o[r][0] * f, o[r][1] * f, o[r][2] * f, o[r][3] * f);

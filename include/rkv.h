@@ -464,7 +464,9 @@ int rkv_q4_read(const rkv_paged_desc* desc, const rkv_q4_cache* cache,
  * query gives no weight, or does not see, may hold numbers of any size.  V's
  * scales and lows count in full from 2^-100 to 2^100.  A 4-bit cache takes a
  * query's elements relative to its row's largest (exact down to 2^-27 of it, the
- * others to 2^-35 of it; magnitudes below 2^115).
+ * others to 2^-35 of it; magnitudes below 2^115).  Logits (to base 2) may have any
+ * size that fp32 holds: past 2^24 they are as coarse as fp32 is there.  The sums of
+ * probabilities times V, before they are divided, are up to 2^8 sum |V| (fp32).
  * q, out: rkv_rows by sequence and token (bf16 for 4-bit caches). */
 #define RKV_MAX_NEW_TOKENS 64
 /* Bytes for the current device (the work is cut for its SMs) and either cache;
