@@ -809,8 +809,9 @@ RKV_DEV float base_of(float m, float scale, float up, float& fix) {
     return base;
 }
 // 4 bits: logits q . k less their queries' m, after a step of m to the stage's maximum
-// where that is past kHuge from it (up with it, so that the sums keep their
-// reference).  Whether some query has an m.
+// where that is past kHuge from 0, or past an m there is (up with it, so that the sums
+// keep their reference; up stays as small as the exponents of V).  Whether some query
+// has an m.
 template <int KT, int NT>
 RKV_DEV bool take_m(float (&x)[KT][NT][4], const float (&top)[NT][2], const float (&sc)[NT][2],
                     float (&m)[NT][2], float (&up)[NT][2], bool huge) {
@@ -828,14 +829,17 @@ RKV_DEV bool take_m(float (&x)[KT][NT][4], const float (&top)[NT][2], const floa
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float mx = top[n][i] - m[n][i];
+            float mx = top[n][i];
 #pragma unroll
             for (int sh = 4; sh <= 16; sh <<= 1)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-            const float z = mx * sc[n][i], old = m[n][i];
-            const bool step = fabsf(z) <= FLT_MAX && (up[n][i] == kUnset ? fabsf(z) : z) > kHuge;
-            if (step) m[n][i] = old + mx;
-            if (step && up[n][i] != kUnset) up[n][i] += (m[n][i] - old) * sc[n][i];
+            const float z = (mx - m[n][i]) * sc[n][i];
+            const bool step = fabsf(z) <= FLT_MAX &&
+                              (up[n][i] == kUnset ? fabsf(z) : z) > (m[n][i] == 0.f ? kHuge : 0.f);
+            if (step) {
+                if (up[n][i] != kUnset) up[n][i] += z;
+                m[n][i] = mx;
+            }
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll

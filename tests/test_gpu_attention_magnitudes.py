@@ -102,3 +102,34 @@ def test_an_ordinary_query_beside_a_large_one(kind):
         else:  # (a shared rescaling may move a sum's last bits)
             assert ((a[:, :, keep] - b[:, :, keep]).abs() <= 2.0 ** (-7 if kind == "bf16" else -18) * (a[:, :, keep].abs() + 0.1)).all()
         assert torch.isfinite(b).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q4", "fp32"])
+@pytest.mark.parametrize("lens", [[1345], [357] * 20, [9001, 60]], ids=lambda n: f"S{len(n)}n{max(n)}")
+def test_any_keys_and_large_queries(lens, kind):
+    """Ordinary keys: one row has the weight where its logit is ahead of the others by
+    more than fp32 may be off; everything is finite."""
+    T, G, d, bs = 3, 2, 128, 16
+    cache, table, rows = make_cache(len(lens), 1, d, bs, lens, kind, 5, junk=False)
+    q0 = rnd((len(lens), T, G, d), FP if kind == "fp32" else BF, 7)
+    lens_d = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    scale = d ** -0.5
+    for k in (3, 8, 14, 17, 20, 27, 33, 40, 60):
+        q = q0 * 2.0 ** k
+        out, lse = attend(kind, q, cache, table, lens_d, max_rows=max(lens), lse=True)
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+        for s, n in enumerate(lens):
+            for t in range(T):
+                kk, vv = (x[s][0, :n - T + t + 1] for x in rows)
+                z = q[s, t].double().cpu() @ kk.T * scale
+                two, at = z.topk(2, -1)
+                # a logit is off by (d + 40) 2^-24 of sum |q| |k| at most (4 bits: of the groups'
+                # parts, below 16 times that)
+                off = (q[s, t].double().cpu().abs() @ kk.abs().T).amax(-1) * scale * (d + 40) * ref.U32 * 16
+                for g in range(G):
+                    if two[g, 0] - two[g, 1] > 2 * off[g] + 40:  # the others below e^-40
+                        e = vv[at[g, 0]]
+                        got = out[s, t, g].double().cpu()
+                        # p = 1: the output's rounding, 4 bits also that of one product of the code
+                        assert ((got - e).abs() <= 2.0 ** -7 * e.abs() + 2.0 ** -9 * vv.abs().amax()).all()
+                assert ((lse[s, t].double().cpu() - torch.logsumexp(z, -1)).abs() <= off + 1e-4 + 2.0 ** -20 * z.abs().amax(-1)).all()
