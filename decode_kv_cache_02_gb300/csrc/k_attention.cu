@@ -39,11 +39,11 @@
 // p stays below 2^8 and the rescaling almost never runs.  (4 bits: by more than 4.)
 //
 // Measured (one GB300, KV heads 8): 64 ragged sequences to 4224 rows, G = 5,
-// head_dim 128: 91.4 us, 6.3 TB/s; 256 of 1152, G = 4: 184 us, 6.6 TB/s; 16 ragged
-// to 16389 with 8 new tokens, head_dim 64: 59.6 us, 5.2 TB/s (copies alone, before
-// its launch overlapped what was there: 55); one of 1152: 6.0 us.  4 bits: one
-// of 131071, G = 5: 46.6 us, 3.6 TB/s.  In steady state a warp spends 378 instructions
-// and an SM quarter 591 cycles on 16 rows, where HBM's rate would allow 435: no pipe is
+// head_dim 128: 91.8 us, 6.2 TB/s; 256 of 1152, G = 4: 183 us, 6.6 TB/s; 16 ragged
+// to 16389 with 8 new tokens, head_dim 64: 61.0 us, 5.1 TB/s (copies alone, before
+// its launch overlapped what was there: 55); one of 1152: 6.1 us.  4 bits: one
+// of 131071, G = 5: 47.0 us, 3.6 TB/s.  In steady state a warp spends 379 instructions
+// and an SM quarter 592 cycles on 16 rows, where HBM's rate would allow 435: no pipe is
 // above 55 in a hundred of them (logic; issue slots 64), the twelve warps of an SM
 // wait for their own last instructions.
 #include <cuda_fp16.h>
