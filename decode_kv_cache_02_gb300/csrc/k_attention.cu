@@ -22,7 +22,7 @@
 // free as long as both sides share it), and P^T turns from an accumulator into
 // an operand with one movmatrix per 8 x 8.  (tcgen05 would need 64 or 128
 // keys a step and the probabilities through tensor memory, between warps; at 8
-// to 32 queries a row the tensor pipe is under a tenth busy as it is.)
+// to 32 queries a row the tensor pipe is a seventh to a third busy as it is.)
 //
 // 4 bits: codes become fp16 numbers exactly: K as they lie, c * 2^-24 or c *
 // 2^-20 (half a shift and a logic op for two), against queries brought to fp16 by
