@@ -22,7 +22,7 @@ import struct
 import torch
 
 from . import rkv as _rkv
-from .rkv import RKV_DTYPE_BF16, RKV_DTYPE_FP32, _Q4Cache, _RopeConfig, _RopePlan, _check
+from .rkv import RKV_DTYPE_BF16, RKV_DTYPE_FP32, _Q4Cache, _Q8Cache, _RopeConfig, _RopePlan, _check
 
 RKV_MAX_NEW_TOKENS = 64
 _MAX_ROWS = 1 << 30  # of a sequence in an attention (past 31 bits an int would wrap on its way to C)
@@ -383,6 +383,12 @@ def rkv_q4_read(cache: Q4Cache, block_table, lens, n_rows: int, first=None, out_
     if _away(at, stream):
         return _elsewhere(rkv_q4_read, at, stream, cache, block_table, lens, n_rows, first, out_K,
                           out_V, dtype, workspace)
+    return _read(load().rkv_q4_read, "rkv_q4_read", cache, block_table, lens, n_rows, first, out_K,
+                 out_V, dtype, workspace)
+
+
+def _read(call, where, cache, block_table, lens, n_rows, first, out_K, out_V, dtype, workspace):
+    at = cache.K_codes
     dev = at.get_device()
     nb, H, bs, d = cache.shape
     if block_table.dim() != 2:
@@ -399,21 +405,80 @@ def rkv_q4_read(cache: Q4Cache, block_table, lens, n_rows: int, first=None, out_
         if t.shape != shape or t.dtype != dt or not t.is_contiguous() or t.get_device() != dev:
             raise ValueError(f"{n} must be contiguous {list(shape)}, K and V of one dtype, on the "
                              "cache's device")
-    rc = load().rkv_q4_read(_pack_desc(S, H, 1, d, bs, nb, mb, code), cache._packed,
-                            _ints(block_table, "block_table", dev, S, mb),
-                            _ints(lens, "lens", dev, S),
-                            None if first is None else _ints(first, "first", dev, S), n_rows,
-                            out_K.data_ptr(), out_V.data_ptr(), _workspace(workspace, dev)[0],
-                            _raw_stream(dev))
+    rc = call(_pack_desc(S, H, 1, d, bs, nb, mb, code), cache._packed,
+              _ints(block_table, "block_table", dev, S, mb), _ints(lens, "lens", dev, S),
+              None if first is None else _ints(first, "first", dev, S), n_rows, out_K.data_ptr(),
+              out_V.data_ptr(), _workspace(workspace, dev)[0], _raw_stream(dev))
     if rc:
-        _check(rc, "rkv_q4_read")
+        _check(rc, where)
     return out_K, out_V
+
+
+# ------------------------------------------------------------------ 8 bits --
+
+class Q8Cache:
+    """A paged cache held in 8 bits (rkv_q8_cache in include/rkv.h): codes int8
+    [num_blocks, H, block_size, d], scales fp32 [num_blocks, H, block_size],
+    for K and for V."""
+
+    def __init__(self, K_codes, K_scales, V_codes, V_scales):
+        for t, n in ((K_codes, "K_codes"), (V_codes, "V_codes")):
+            if t.dtype != torch.int8 or t.dim() != 4 or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"{n} must be contiguous CUDA int8 [num_blocks, H, block_size, d]")
+        if V_codes.shape != K_codes.shape:
+            raise ValueError("K_codes and V_codes must have one shape")
+        for t, n in ((K_scales, "K_scales"), (V_scales, "V_scales")):
+            if t.dtype != _F32 or not t.is_contiguous() or t.shape != K_codes.shape[:3]:
+                raise ValueError(f"{n} must be contiguous fp32 [num_blocks, H, block_size]")
+        if any(t.device != K_codes.device for t in (K_scales, V_codes, V_scales)):
+            raise ValueError("the arrays must be on one device")
+        self.K_codes, self.K_scales, self.V_codes, self.V_scales = (K_codes, K_scales, V_codes,
+                                                                    V_scales)
+        self.shape = tuple(K_codes.shape)
+        self._c = _Q8Cache(K_codes.data_ptr(), K_scales.data_ptr(), V_codes.data_ptr(),
+                           V_scales.data_ptr())
+        self._packed = bytes(self._c)
+
+
+def alloc_q8_cache(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int,
+                   device="cuda") -> Q8Cache:
+    """A zeroed 8-bit cache (8 bits a value, 32 more a row)."""
+    t = []
+    for _ in range(2):
+        t.append(torch.zeros((num_blocks, num_kv_heads, block_size, head_dim), dtype=torch.int8,
+                             device=device))
+        t.append(torch.zeros((num_blocks, num_kv_heads, block_size), dtype=_F32, device=device))
+    return Q8Cache(*t)
+
+
+def rkv_q8_append(cache: Q8Cache, k, v, block_table, lens, cu_tokens=None,
+                  rope: RopePlan | None = None, positions=None, q=None, out_q=None,
+                  workspace=None, stream=None):
+    """rkv_paged_append into an 8-bit cache (k, v, q bf16 or fp32)."""
+    at = cache.K_codes
+    if _away(at, stream):
+        return _elsewhere(rkv_q8_append, at, stream, cache, k, v, block_table, lens, cu_tokens,
+                          rope, positions, q, out_q, workspace)
+    return _append(load().rkv_q8_append, "rkv_q8_append", (cache._packed,), at.get_device(),
+                   cache.shape, k, v, block_table, lens, cu_tokens, rope, positions, q, out_q,
+                   workspace)
+
+
+def rkv_q8_read(cache: Q8Cache, block_table, lens, n_rows: int, first=None, out_K=None,
+                out_V=None, dtype=torch.bfloat16, workspace=None, stream=None):
+    """rkv_q4_read of an 8-bit cache."""
+    at = cache.K_codes
+    if _away(at, stream):
+        return _elsewhere(rkv_q8_read, at, stream, cache, block_table, lens, n_rows, first, out_K,
+                          out_V, dtype, workspace)
+    return _read(load().rkv_q8_read, "rkv_q8_read", cache, block_table, lens, n_rows, first, out_K,
+                 out_V, dtype, workspace)
 
 
 # --------------------------------------------------------------- attention --
 
 def rkv_attention_workspace_size(q, num_kv_heads: int, max_rows: int) -> int:
-    """Workspace bytes of rkv_paged_attention and rkv_q4_attention for q [S,
+    """Workspace bytes of rkv_paged_attention, rkv_q4_attention and rkv_q8_attention for q [S,
     n_new, heads, d] over at most max_rows rows a sequence, on q's device."""
     if q.is_cuda and q.get_device() != _current_device():
         with torch.cuda.device(q.device):
@@ -512,5 +577,17 @@ def rkv_q4_attention(q, cache: Q4Cache, block_table, lens, max_rows: int | None 
         return _elsewhere(rkv_q4_attention, at, stream, q, cache, block_table, lens, max_rows,
                           scale, out, lse, workspace)
     return _attention(load().rkv_q4_attention, "rkv_q4_attention", (cache._packed,),
+                      at.get_device(), cache.shape, q, block_table, lens, max_rows, scale, out,
+                      lse, workspace)
+
+
+def rkv_q8_attention(q, cache: Q8Cache, block_table, lens, max_rows: int | None = None,
+                     scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
+    """rkv_paged_attention over an 8-bit cache (q bf16)."""
+    at = cache.K_codes
+    if _away(at, stream):
+        return _elsewhere(rkv_q8_attention, at, stream, q, cache, block_table, lens, max_rows,
+                          scale, out, lse, workspace)
+    return _attention(load().rkv_q8_attention, "rkv_q8_attention", (cache._packed,),
                       at.get_device(), cache.shape, q, block_table, lens, max_rows, scale, out,
                       lse, workspace)

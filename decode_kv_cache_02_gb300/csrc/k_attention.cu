@@ -64,16 +64,17 @@ constexpr float kNone = -FLT_MAX, kUnset = 1e30f;  // no maximum yet
 constexpr float kHuge = 0x1p20f;
 
 // Bytes and rows of one stage of a warp's ring.
-template <int D, bool Q4>
+template <int D, int BITS>
 struct Stage {
+    static constexpr bool Q4 = BITS == 4, Q8 = BITS == 8;
     static constexpr int W = D / 32;
-    static constexpr int KEYS = Q4 ? 32 : (D == 128 ? 16 : 32);
+    static constexpr int KEYS = BITS ? 32 : (D == 128 ? 16 : 32);
     // one stage in flight is enough where a stage is 5 KB of long arithmetic (4
     // bits, head_dim 128: 48.5 us against 49.7 with two, one of 131071; 84.8
     // against 86.5, 64 of 4224), not for bf16 (256 of 1152: 184 us with two, 189)
-    static constexpr int DEPTH = Q4 ? 2 : 3;
-    static constexpr int ROW = Q4 ? D / 2 : D * 2;
-    static constexpr int SROW = Q4 ? W * 4 : 0;
+    static constexpr int DEPTH = BITS ? 2 : 3;
+    static constexpr int ROW = Q4 ? D / 2 : (Q8 ? D : D * 2);
+    static constexpr int SROW = Q4 ? W * 4 : (Q8 ? 4 : 0);
     static constexpr int V = KEYS * ROW;
     static constexpr int ks() { return 2 * KEYS * ROW; }
     static constexpr int vs() { return ks() + KEYS * SROW; }
@@ -142,6 +143,11 @@ RKV_DEV void cp16(uint32_t dst, const void* src) {
 RKV_DEV void cp16(uint32_t dst, const void* src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(ok ? 16 : 0)
+                 : "memory");
+}
+RKV_DEV void cp4(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(ok ? 4 : 0)
                  : "memory");
 }
 RKV_DEV void cp8(uint32_t dst, const void* src, bool ok) {
@@ -287,14 +293,16 @@ RKV_DEV uint32_t pack_rest(float lo, float hi, uint32_t h) {
 // Physical row (within 16) of row r of a key fragment.  Quarter-warp reads of
 // K (two rows) and half-warp reads of V (four rows) then meet no bank twice,
 // with the 16-byte units of a row permuted by unit_xor.
-template <bool Q4>
+template <int BITS>
 RKV_DEV int phys(int r) {
-    if constexpr (Q4) return r ^ ((r >> 1) & 1);
+    if constexpr (BITS != 0) return r ^ ((r >> 1) & 1);
     return (r & 8) | ((r & 7) >> 1) | ((r & 1) << 2);
 }
-template <int D, bool Q4>
+template <int D, int BITS>
 RKV_DEV int unit_xor(int row) {
-    if constexpr (Q4) return D == 128 ? ((row >> 2) & 1) << 1 : 0;
+    if constexpr (BITS == 4) return D == 128 ? ((row >> 2) & 1) << 1 : 0;
+    if constexpr (BITS == 8)
+        return D == 128 ? (row & 6) ^ ((row & 1) << 2) : ((row >> 2) & 1) << 1;
     return ((row & 3) << 1) ^ (((row >> 2) & 1) << 2);
 }
 
@@ -302,9 +310,9 @@ constexpr uint32_t kNoRow = 0xffffffffu;
 
 // Copies the rows of a stage; lane i holds the pool row of row i (kNoRow:
 // zeros; full: there are none).
-template <int D, bool Q4>
+template <int D, int BITS>
 RKV_DEV void copy_stage(const Params& p, uint32_t dst, uint32_t mine, bool full) {
-    using S = Stage<D, Q4>;
+    using S = Stage<D, BITS>;
     const int lane = threadIdx.x & 31;
     constexpr int UPR = S::ROW / 16;  // units per row
     const int u = lane % UPR;
@@ -315,7 +323,7 @@ RKV_DEV void copy_stage(const Params& p, uint32_t dst, uint32_t mine, bool full)
         for (int i = 0; i < S::KEYS * UPR / 32; ++i) {
             const int r = i * (32 / UPR) + lane / UPR;
             const uint64_t at = (uint64_t)__shfl_sync(0xffffffffu, mine, r) * S::ROW;
-            const uint32_t to = dst + r * S::ROW + ((u ^ unit_xor<D, Q4>(r)) << 4);
+            const uint32_t to = dst + r * S::ROW + ((u ^ unit_xor<D, BITS>(r)) << 4);
             cp16(to, k + at);
             cp16(to + S::V, v + at);
         }
@@ -326,12 +334,12 @@ RKV_DEV void copy_stage(const Params& p, uint32_t dst, uint32_t mine, bool full)
             const uint32_t row = __shfl_sync(0xffffffffu, mine, r);
             const bool ok = row != kNoRow;
             const uint64_t at = (uint64_t)(ok ? row : 0u) * S::ROW;
-            const uint32_t to = dst + r * S::ROW + ((u ^ unit_xor<D, Q4>(r)) << 4);
+            const uint32_t to = dst + r * S::ROW + ((u ^ unit_xor<D, BITS>(r)) << 4);
             cp16(to, k + at, ok);
             cp16(to + S::V, v + at, ok);
         }
     }
-    if constexpr (Q4) {
+    if constexpr (BITS != 0) {
         static_assert(S::KEYS == 32, "one lane per row");
         const bool ok = mine != kNoRow;
         const uint64_t at = (uint64_t)(ok ? mine : 0u) * S::SROW;
@@ -339,6 +347,9 @@ RKV_DEV void copy_stage(const Params& p, uint32_t dst, uint32_t mine, bool full)
         if constexpr (S::SROW == 16) {
             cp16(to + S::ks(), p.ks + at, ok);
             cp16(to + S::vs(), p.vs + at, ok);
+        } else if constexpr (S::SROW == 4) {
+            cp4(to + S::ks(), p.ks + at, ok);
+            cp4(to + S::vs(), p.vs + at, ok);
         } else {
             cp8(to + S::ks(), p.ks + at, ok);
             cp8(to + S::vs(), p.vs + at, ok);
@@ -350,9 +361,9 @@ RKV_DEV void copy_stage(const Params& p, uint32_t dst, uint32_t mine, bool full)
 template <int D, int NT>
 RKV_DEV void logits_bf16(uint32_t st, int base, const uint32_t (&qf)[NT][D / 8],
                          float (&c)[NT][4]) {
-    using S = Stage<D, false>;
+    using S = Stage<D, 0>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int pr = base + phys<false>(g), f = unit_xor<D, false>(pr);
+    const int pr = base + phys<0>(g), f = unit_xor<D, 0>(pr);
     const uint32_t row = st + pr * S::ROW;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -371,11 +382,105 @@ RKV_DEV void logits_bf16(uint32_t st, int base, const uint32_t (&qf)[NT][D / 8],
     }
 }
 
+// An 8-bit cache's codes as bf16 numbers, exactly: bytes 0 and 2 of a word.  128 + c's
+// low seven bits lie in the mantissa as they are, and the sign (-128) is in the 128
+// or 256 that is taken away: two logic operations and a subtraction for two codes,
+// where a conversion through integers takes six.  Constants in registers, as below.
+struct Bytes {
+    uint32_t low, sign, base;
+};
+RKV_DEV Bytes byte_constants() {
+    Bytes k;
+    asm volatile("mov.b32 %0, 0x007f007f;" : "=r"(k.low));
+    asm volatile("mov.b32 %0, 0x00800080;" : "=r"(k.sign));
+    asm volatile("mov.b32 %0, 0x43004300;" : "=r"(k.base));  // bf16 128, 128
+    return k;
+}
+RKV_DEV uint32_t bytes_as_bf16(const Bytes& k, uint32_t w) {
+    const uint32_t a = and_or(w, k.low, k.base), b = and_or(w, k.sign, k.base);
+    const __nv_bfloat162 c = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&c);
+}
+
+// q . k of 16 keys of an 8-bit stage; lane (g, t) holds values 64 ch + 16 t .. of its
+// keys, byte pairs (0, 2) and (1, 3) of a word as neighbours.
+template <int D, int NT>
+RKV_DEV void logits_q8(const Bytes& bk, uint32_t st, int base, const uint32_t (&qf)[NT][D / 8],
+                       float (&c)[NT][4]) {
+    using S = Stage<D, 8>;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int pr = base + phys<8>(g), f = unit_xor<D, 8>(pr);
+    const uint32_t row = st + pr * S::ROW;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[n][i] = 0.f;
+#pragma unroll
+    for (int ch = 0; ch < D / 64; ++ch) {
+        const int at = ((4 * ch + t) ^ f) << 4;
+        const uint4 a = lds16(row + at);
+        const uint4 b = lds16(row + 8 * S::ROW + at);
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint32_t a0 = bytes_as_bf16(bk, x[w]), a2 = bytes_as_bf16(bk, x[w] >> 8);
+            const uint32_t a1 = bytes_as_bf16(bk, y[w]), a3 = bytes_as_bf16(bk, y[w] >> 8);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                mma(c[n], a0, a1, a2, a3, qf[n][8 * ch + 2 * w], qf[n][8 * ch + 2 * w + 1]);
+        }
+    }
+    const float s0 = __uint_as_float(lds4(st + S::ks() + pr * 4));
+    const float s1 = __uint_as_float(lds4(st + S::ks() + (pr + 8) * 4));
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[n][i] *= i < 2 ? s0 : s1;
+}
+
+// O^T += V^T P^T for 16 keys of an 8-bit stage (the scales are in P).  Lane (g, t)
+// holds values D / 8 * g .. of its keys; accumulator e stands for values 2 e and
+// 2 e + 1 of them.
+template <int D, int NT, bool TWO>
+RKV_DEV void values_q8(const Bytes& bk, uint32_t st, int base, const uint32_t (&pb)[NT][2],
+                       const uint32_t (&pr)[NT][2], float (&o)[D / 16][NT][4]) {
+    using S = Stage<D, 8>;
+    constexpr int WORDS = D / 32;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint32_t x[4][WORDS];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = base + phys<8>(2 * t + (k & 1) + 8 * (k >> 1));
+        const uint32_t row = st + S::V + r * S::ROW;
+        if constexpr (D == 128) {
+            const uint4 y = lds16(row + ((g ^ unit_xor<D, 8>(r)) << 4));
+            x[k][0] = y.x; x[k][1] = y.y; x[k][2] = y.z; x[k][3] = y.w;
+        } else {
+            const uint2 y = lds8(row + (((g >> 1) ^ unit_xor<D, 8>(r)) << 4) + ((g & 1) << 3));
+            x[k][0] = y.x; x[k][1] = y.y;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) {
+        const uint32_t sel = (e & 1) ? 0x7632 : 0x5410;
+        const uint32_t u = __byte_perm(x[0][e >> 1], x[1][e >> 1], sel);
+        const uint32_t v = __byte_perm(x[2][e >> 1], x[3][e >> 1], sel);
+        const uint32_t a0 = bytes_as_bf16(bk, u), a1 = bytes_as_bf16(bk, u >> 8);
+        const uint32_t a2 = bytes_as_bf16(bk, v), a3 = bytes_as_bf16(bk, v >> 8);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            mma(o[e][n], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            if constexpr (TWO) mma(o[e][n], a0, a1, a2, a3, pr[n][0], pr[n][1]);
+        }
+    }
+}
+
 // Where the scales of row lane % 16 of the 16 keys from base on lie (head_dim
 // 128: 16 bytes a row).
 RKV_DEV int scale_row(int base) {
     const int lane = threadIdx.x & 31;
-    return (base + phys<true>(lane & 7) + (lane & 8)) * 16;
+    return (base + phys<4>(lane & 7) + (lane & 8)) * 16;
 }
 
 // The same for a 4-bit stage: sum over groups of scale * (q . c), and (scale,
@@ -383,10 +488,10 @@ RKV_DEV int scale_row(int base) {
 template <int D, int NT>
 RKV_DEV void logits_q4(const Unpack& uk, uint32_t st, int base, const uint32_t (&qf)[NT][D / 8],
                        const uint32_t (&qb)[NT][3], float (&c)[NT][4]) {
-    using S = Stage<D, true>;
+    using S = Stage<D, 4>;
     constexpr int W = S::W;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int pr = base + phys<true>(g), f = unit_xor<D, true>(pr);
+    const int pr = base + phys<4>(g), f = unit_xor<D, 4>(pr);
     uint32_t word[2][W], sc[2][W], own[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -442,7 +547,7 @@ template <int D, int NT, bool TWO, bool ONE>
 RKV_DEV void values_bf16(uint32_t st, int base, const uint32_t (&pb)[NT][2],
                          const uint32_t (&pr)[NT][2], uint32_t keep0, uint32_t keep1,
                          uint32_t cols, float (&o)[D / 16][NT][4]) {
-    using S = Stage<D, false>;
+    using S = Stage<D, 0>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t v = st + S::V;
 #pragma unroll
@@ -450,8 +555,8 @@ RKV_DEV void values_bf16(uint32_t st, int base, const uint32_t (&pb)[NT][2],
         uint4 x[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int pr = base + phys<false>(2 * t + (k & 1) + 8 * (k >> 1));
-            x[k] = lds16(v + pr * S::ROW + (((8 * j + g) ^ unit_xor<D, false>(pr)) << 4));
+            const int pr = base + phys<0>(2 * t + (k & 1) + 8 * (k >> 1));
+            x[k] = lds16(v + pr * S::ROW + (((8 * j + g) ^ unit_xor<D, 0>(pr)) << 4));
         }
         const uint32_t w[4][4] = {{x[0].x, x[0].y, x[0].z, x[0].w}, {x[1].x, x[1].y, x[1].z, x[1].w},
                                   {x[2].x, x[2].y, x[2].z, x[2].w}, {x[3].x, x[3].y, x[3].z, x[3].w}};
@@ -488,7 +593,7 @@ RKV_DEV void values_bf16(uint32_t st, int base, const uint32_t (&pb)[NT][2],
 // and |low|: the bits of the largest (as bf16) and how far the smallest lies below.
 template <int D>
 RKV_DEV void row_sizes(uint32_t st, int r, uint32_t& top, uint32_t& spread) {
-    using S = Stage<D, true>;
+    using S = Stage<D, 4>;
     const uint32_t row = st + S::vs() + r * S::SROW;
     uint32_t most, least;  // of the groups with even and with odd numbers
     if constexpr (S::W == 4) {
@@ -510,9 +615,10 @@ RKV_DEV void row_sizes(uint32_t st, int r, uint32_t& top, uint32_t& spread) {
 
 // Whether row r of a stage holds an infinity or a NaN in V (4 bits: in its
 // scales).
-template <int D, bool Q4>
+template <int D, int BITS>
 RKV_DEV bool unfinite(uint32_t st, int r) {
-    using S = Stage<D, Q4>;
+    constexpr bool Q4 = BITS == 4;
+    using S = Stage<D, BITS>;
     const uint32_t row = Q4 ? st + S::vs() + r * S::SROW : st + S::V + r * S::ROW;
     bool bad = false;
 #pragma unroll 4
@@ -532,12 +638,12 @@ RKV_DEV bool unfinite(uint32_t st, int r) {
 template <int D, int NT, bool MIXED>
 RKV_DEV void values_q4(const Unpack& uk, uint32_t st, int base, const float (&p)[NT][4],
                        uint32_t wide, bool every, float (&o)[D / 16][NT][4]) {
-    using S = Stage<D, true>;
+    using S = Stage<D, 4>;
     constexpr int W = S::W;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint32_t sc[2][W];
     {
-        const int pr = base + phys<true>(g);
+        const int pr = base + phys<4>(g);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const uint32_t srow = st + S::vs() + (pr + 8 * k) * S::SROW;
@@ -553,10 +659,10 @@ RKV_DEV void values_q4(const Unpack& uk, uint32_t st, int base, const float (&p)
     uint32_t x[4][W / 2];  // a key's codes of its lane: two groups a word
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const int pr = base + phys<true>(2 * t + (k & 1) + 8 * (k >> 1));
+        const int pr = base + phys<4>(2 * t + (k & 1) + 8 * (k >> 1));
         const uint32_t row = st + S::V + pr * S::ROW;
         if constexpr (W == 4) {
-            const uint2 y = lds8(row + (((g >> 1) ^ unit_xor<D, true>(pr)) << 4) + ((g & 1) << 3));
+            const uint2 y = lds8(row + (((g >> 1) ^ unit_xor<D, 4>(pr)) << 4) + ((g & 1) << 3));
             x[k][0] = y.x; x[k][1] = y.y;
         } else {
             x[k][0] = lds4(row + g * 4);
@@ -616,7 +722,7 @@ RKV_DEV void values_q4(const Unpack& uk, uint32_t st, int base, const float (&p)
 // (scale, low) of the 16 keys as operand rows: row 2 w scale, row 2 w + 1 low.
 template <int D>
 RKV_DEV void low_rows(uint32_t st, int base, uint32_t (&a)[2]) {
-    using S = Stage<D, true>;
+    using S = Stage<D, 4>;
     if constexpr (S::W == 4) {
         ldm2t(a, st + S::vs() + scale_row(base));
     } else {
@@ -624,7 +730,7 @@ RKV_DEV void low_rows(uint32_t st, int base, uint32_t (&a)[2]) {
         uint32_t x[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int pr = base + phys<true>(2 * t + (k & 1) + 8 * (k >> 1));
+            const int pr = base + phys<4>(2 * t + (k & 1) + 8 * (k >> 1));
             x[k] = lds2(st + S::vs() + pr * S::SROW + 2 * (g & 3));
         }
         a[0] = g < 4 ? __byte_perm(x[0], x[1], 0x5410) : 0u;  // (rows past 2 W stand for nothing)
@@ -993,9 +1099,10 @@ RKV_DEV void finish_cluster(const Params& p, float* acc, const float (&sh_m)[kWa
 }
 
 // NT * 8 queries of a KV head's group against a run of rows.
-template <int D, int NT, bool Q4, bool TWO>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kernel(const __grid_constant__ Params p) {
-    using S = Stage<D, Q4>;
+template <int D, int NT, int BITS, bool TWO>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 && BITS ? 3 : 2) attn_kernel(const __grid_constant__ Params p) {
+    constexpr bool Q4 = BITS == 4, Q8 = BITS == 8;
+    using S = Stage<D, BITS>;
     constexpr int ROWS = 8 * NT, W = D / 32, KT = S::KEYS / 16, UNIT = kWarps * S::KEYS;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float sh_m[kWarps][ROWS], sh_l[kWarps][ROWS];
@@ -1014,6 +1121,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
 
     [[maybe_unused]] Unpack uk;
     if constexpr (Q4) uk = unpack_constants();
+    [[maybe_unused]] Bytes bk;
+    if constexpr (Q8) bk = byte_constants();
     wait_for_last();
 
     Place place{};
@@ -1046,7 +1155,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
             if (!good && r < end) set_error(p.status, kDevErrIndex, (unsigned)r);
             const uint32_t row =
                 good ? (((uint32_t)b * p.H + h) << p.log2bs) | (uint32_t)(r & mask) : kNoRow;
-            if (fetch < c1) copy_stage<D, Q4>(p, to, row, ok == kAll);
+            if (fetch < c1) copy_stage<D, BITS>(p, to, row, ok == kAll);
             cp_commit();
             fetch += UNIT;
             to = to == ring + (S::DEPTH - 1) * S::BYTES ? ring : to + S::BYTES;
@@ -1079,7 +1188,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
 #pragma unroll
             for (int w = 0; w < W; ++w) {
                 uint4 x = make_uint4(0, 0, 0, 0);
-                if (ok) x = *reinterpret_cast<const uint4*>(q + 32 * w + 8 * t);
+                // (8 bits: lane t holds values 64 w' + 16 t .. in two steps)
+                if (ok) x = *reinterpret_cast<const uint4*>(Q8 ? q + 64 * (w >> 1) + 16 * t + 8 * (w & 1) : q + 32 * w + 8 * t);
                 x.x ^= p.flip; x.y ^= p.flip; x.z ^= p.flip; x.w ^= p.flip;
                 if constexpr (Q4) {
                     const uint32_t y[4] = {x.x, x.y, x.z, x.w};
@@ -1093,6 +1203,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                     x = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
                                    __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
                 }
+                if constexpr (Q8)
+                    x = make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.x, x.y, 0x7632),
+                                   __byte_perm(x.z, x.w, 0x5410), __byte_perm(x.z, x.w, 0x7632));
                 qf[n][4 * w] = x.x;
                 qf[n][4 * w + 1] = x.y;
                 qf[n][4 * w + 2] = x.z;
@@ -1188,6 +1301,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
             for (int kt = 0; kt < KT; ++kt) {
                 if constexpr (Q4)
                     logits_q4<D, NT>(uk, st, kt * 16, qf, qb, x[kt]);
+                else if constexpr (Q8)
+                    logits_q8<D, NT>(bk, st, kt * 16, qf, x[kt]);
                 else
                     logits_bf16<D, NT>(st, kt * 16, qf, x[kt]);
             }
@@ -1198,7 +1313,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int r = kt * 16 + phys<Q4>(g + 8 * (i >> 1));
+                            const int r = kt * 16 + phys<BITS>(g + 8 * (i >> 1));
                             if (row0 + r > last[n][i & 1] || !((ok >> r) & 1u))
                                 x[kt][n][i] = -INFINITY;
                         }
@@ -1238,7 +1353,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
                             ve[kt][k] = (float)__shfl_sync(0xffffffffu, mine,
-                                                           kt * 16 + phys<Q4>(g) + 8 * k);
+                                                           kt * 16 + phys<BITS>(g) + 8 * k);
                     const uint32_t rows = __ballot_sync(0xffffffffu, far);
                     if (rows) {  // the queries that see one of them
                         const int first = row0 + __ffs(rows) - 1;
@@ -1302,16 +1417,32 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
             // rows that only some of the tokens see: an infinity or a NaN there must not reach
             // the others as 0 * inf, so such a stage is taken one token at a time (rows nobody
             // sees are zeros here: rows past len and rows without a block)
+            // (8 bits: codes are finite, and a hidden row's scale is left out below)
             bool apart = false;
-            if (masked && p.T > 1) {
+            if (!Q8 && masked && p.T > 1) {
                 const int r = row0 + lane;
                 const bool part = lane < S::KEYS && r < c1 && r > all_see;
-                apart = __any_sync(0xffffffffu, part && unfinite<D, Q4>(st, lane));
+                apart = __any_sync(0xffffffffu, part && unfinite<D, BITS>(st, lane));
             }
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
                 uint32_t pb[NT][2];
                 [[maybe_unused]] uint32_t pr[NT][2];
+                if constexpr (Q8) {
+                    // V's scales meet the probabilities, but for rows that a query does not see
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int r = kt * 16 + phys<8>(g) + 8 * k;
+                        const float vs = __uint_as_float(lds4(st + S::vs() + r * 4));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                float& y = x[kt][n][i + 2 * k];
+                                y = masked && row0 + r > last[n][i] ? 0.f : y * vs;
+                            }
+                    }
+                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -1337,6 +1468,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                             if constexpr (TWO)
                                 mma(low[n], la[0], 0u, la[1], 0u, pr[n][0], pr[n][1]);
                         }
+                    } else if constexpr (Q8) {
+                        values_q8<D, NT, TWO>(bk, st, kt * 16, pb, pr, o);
                     } else {
                         values_bf16<D, NT, TWO, false>(st, kt * 16, pb, pr, ~0u, ~0u, ~0u, o);
                     }
@@ -1350,8 +1483,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                     uint32_t keep[2], cols = 0u;
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int ra = row0 + kt * 16 + phys<Q4>(2 * t + 8 * k);
-                        const int rb = row0 + kt * 16 + phys<Q4>(2 * t + 1 + 8 * k);
+                        const int ra = row0 + kt * 16 + phys<BITS>(2 * t + 8 * k);
+                        const int rb = row0 + kt * 16 + phys<BITS>(2 * t + 1 + 8 * k);
                         keep[k] = (ra <= see ? 0xffffu : 0u) | (rb <= see ? 0xffff0000u : 0u);
                     }
 #pragma unroll
@@ -1372,7 +1505,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                             for (int i = 0; i < 2; ++i)
                                 if ((cols >> (2 * n + i)) & 1u) low[n][i] += y[i];
                         }
-                    } else {
+                    } else if constexpr (!Q8) {
                         values_bf16<D, NT, TWO, true>(st, kt * 16, pb, pr, keep[0], keep[1], cols, o);
                     }
                 }
@@ -1418,7 +1551,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && Q4 ? 3 : 2) attn_kerne
                 for (int e = 0; e < D / 16; ++e) {
                     // the pair of dimensions this accumulator's rows g and g + 8 stand for
                     const int d = Q4 ? 32 * (e / 2) + 4 * g + 2 * (e % 2)
-                                     : 64 * (e / 4) + 8 * g + 2 * (e % 4);
+                                     : (Q8 ? D / 8 * g + 2 * e : 64 * (e / 4) + 8 * g + 2 * (e % 4));
                     float a = o[e][n][i], b = o[e][n][i + 2];
                     if constexpr (Q4) {
                         a += add[e / 2];
@@ -1712,10 +1845,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
 
 Params params(const AttnArgs& a, const AttnPlan& pl) {
     Params p{};
-    p.k = static_cast<const uint8_t*>(a.q4 ? a.q4p.k_codes : a.k);
-    p.v = static_cast<const uint8_t*>(a.q4 ? a.q4p.v_codes : a.v);
-    p.ks = reinterpret_cast<const uint8_t*>(a.q4p.k_scales);
-    p.vs = reinterpret_cast<const uint8_t*>(a.q4p.v_scales);
+    p.k = static_cast<const uint8_t*>(a.bits == 4 ? a.q4p.k_codes : (a.bits == 8 ? a.q8p.k_codes : a.k));
+    p.v = static_cast<const uint8_t*>(a.bits == 4 ? a.q4p.v_codes : (a.bits == 8 ? a.q8p.v_codes : a.v));
+    p.ks = a.bits == 8 ? reinterpret_cast<const uint8_t*>(a.q8p.k_scales)
+                       : reinterpret_cast<const uint8_t*>(a.q4p.k_scales);
+    p.vs = a.bits == 8 ? reinterpret_cast<const uint8_t*>(a.q8p.v_scales)
+                       : reinterpret_cast<const uint8_t*>(a.q4p.v_scales);
     p.table = a.pg.table;
     p.lens = a.lens;
     p.q = static_cast<const __nv_bfloat16*>(a.q.data);
@@ -1756,12 +1891,12 @@ cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
     return e;
 }
 
-template <int D, int NT, bool Q4, bool TWO>
+template <int D, int NT, int BITS, bool TWO>
 cudaError_t go(const Params& p, unsigned ctas, cudaStream_t s) {
-    using S = Stage<D, Q4>;
+    using S = Stage<D, BITS>;
     constexpr int ring = kWarps * S::DEPTH * S::BYTES, join = kWarps * 8 * NT * D * 4;
     constexpr int bytes = ring > join ? ring : join;
-    auto kern = attn_kernel<D, NT, Q4, TWO>;
+    auto kern = attn_kernel<D, NT, BITS, TWO>;
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kern, bytes, done);
     if (e != cudaSuccess) return e;
@@ -1781,14 +1916,14 @@ cudaError_t go(const Params& p, unsigned ctas, cudaStream_t s) {
     cfg.numAttrs = p.cluster ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
-template <bool Q4>
+template <int BITS>
 cudaError_t go(const Params& p, int d, int rows, unsigned ctas, cudaStream_t s) {
-    if (d == 128 && p.R > kTwoQueries) return go<128, 2, Q4, false>(p, ctas, s);
+    if (d == 128 && p.R > kTwoQueries) return go<128, 2, BITS, false>(p, ctas, s);
     if (d == 128)
-        return rows == 8 ? go<128, 1, Q4, true>(p, ctas, s) : go<128, 2, Q4, true>(p, ctas, s);
-    return rows == 8 ? go<64, 1, Q4, true>(p, ctas, s)
-                     : (rows == 16 ? go<64, 2, Q4, true>(p, ctas, s)
-                                   : go<64, 4, Q4, false>(p, ctas, s));
+        return rows == 8 ? go<128, 1, BITS, true>(p, ctas, s) : go<128, 2, BITS, true>(p, ctas, s);
+    return rows == 8 ? go<64, 1, BITS, true>(p, ctas, s)
+                     : (rows == 16 ? go<64, 2, BITS, true>(p, ctas, s)
+                                   : go<64, 4, BITS, false>(p, ctas, s));
 }
 template <int D>
 cudaError_t go32(const Params& p, unsigned ctas, cudaStream_t s) {
@@ -1801,7 +1936,7 @@ cudaError_t go32(const Params& p, unsigned ctas, cudaStream_t s) {
     return launch_early(kern, ctas, kWarps * 32, bytes, s, p);
 }
 
-bool is_f32(const AttnArgs& a) { return !a.q4 && a.dtype == RKV_DTYPE_FP32; }
+bool is_f32(const AttnArgs& a) { return !a.bits && a.dtype == RKV_DTYPE_FP32; }
 
 }  // namespace
 
@@ -1820,13 +1955,13 @@ AttnPlan attn_plan(const AttnArgs& a) {
     pl.rows = R <= 8 ? 8 : (R <= 16 ? 16 : 32);
     if (pl.rows > most) pl.rows = most;
     pl.groups = (R + pl.rows - 1) / pl.rows;
-    pl.unit = kWarps * (is_f32(a) ? 16 : (a.q4 ? Stage<128, true>::KEYS
-                                               : (a.d == 128 ? Stage<128, false>::KEYS
-                                                             : Stage<64, false>::KEYS)));
+    pl.unit = kWarps * (is_f32(a) ? 16 : (a.bits ? Stage<128, 4>::KEYS
+                                               : (a.d == 128 ? Stage<128, 0>::KEYS
+                                                             : Stage<64, 0>::KEYS)));
     // as many blocks as the device's SMs hold at once: shared memory for two (one with
     // fp32 rows of 128), with 4-bit rows registers for three
     const int sms = tc::sm_count();
-    const int blocks = sms * (is_f32(a) && a.d == 128 ? 1 : (a.q4 && pl.rows == 8 ? 3 : 2));
+    const int blocks = sms * (is_f32(a) && a.d == 128 ? 1 : (a.bits && pl.rows == 8 ? 3 : 2));
     const int64_t per = ((int64_t)a.max_rows + pl.unit - 1) / pl.unit, problems = a.num_seqs * a.pg.H;
     // a few short sequences: a cluster for each problem, one launch
     if (!is_f32(a) && per > 1 && per <= kClusterUnits && problems * pl.groups * kCluster <= 2 * sms) {
@@ -1839,7 +1974,7 @@ AttnPlan attn_plan(const AttnArgs& a) {
     // ragged sequences of 131 .. 4224 rows, us at 0, 1, 2, 4, 8: bf16 103, 102,
     // 95, 95, 96; 4 bits 64, 60, 56, 58, 62; 8 new tokens, head_dim 64: 72, 70,
     // 66, 61, 61)
-    pl.lead = a.q4 ? 2 : 4;
+    pl.lead = a.bits ? 2 : 4;
     int64_t runs = (blocks + pl.groups - 1) / pl.groups;
     if (runs > units) runs = units;
     pl.runs = (int)runs;
@@ -1855,7 +1990,8 @@ cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& pl, cudaStream_t
     if (ctas == 0) return cudaSuccess;
     const Params p = params(a, pl);
     if (is_f32(a)) return a.d == 128 ? go32<128>(p, ctas, s) : go32<64>(p, ctas, s);
-    return a.q4 ? go<true>(p, a.d, pl.rows, ctas, s) : go<false>(p, a.d, pl.rows, ctas, s);
+    if (a.bits == 8) return go<8>(p, a.d, pl.rows, ctas, s);
+    return a.bits == 4 ? go<4>(p, a.d, pl.rows, ctas, s) : go<0>(p, a.d, pl.rows, ctas, s);
 }
 
 template <typename T, int D>

@@ -1,6 +1,6 @@
 // k_tokens.cu -- new tokens on their way to the cache: rotary positions, the
-// append to a paged pool, and the append to a 4-bit pool, in one kernel; and
-// reading 4-bit rows back.
+// append to a paged pool, and the append to a 4-bit or an 8-bit pool, in one
+// kernel; and reading 4-bit and 8-bit rows back.
 //
 // Rotation: pair i of a head is turned by pos * f_i.  The plan holds f_i /
 // (2 pi) as a 64-bit fixed-point part of a turn, so the low 64 bits of
@@ -26,6 +26,10 @@
 // mantissa bits.  16.8
 // thousand tokens with their queries, written and read back, 473 MB: 80 us,
 // 5.9 TB/s (the blocks wait for their rows' places).
+//
+// 8 bits: the same four lanes own a row and find its largest magnitude with two
+// shuffles; codes are rounded as above, and a lane's eight of a group are one
+// store of 8 bytes, the row's four lanes together a sector.
 #include <float.h>
 
 #include "rkv_common.cuh"
@@ -244,6 +248,49 @@ RKV_DEV float fifteenth(float x) {
     return fmaf(fmaf(-15.f, q, x), c, q);
 }
 
+// x / 127 rounded to nearest, in the same way (compared with the division for every
+// x of a binade and for the binades at both ends).
+RKV_DEV float part_of_127(float x) {
+    constexpr float c = 1.f / 127.f;
+    const float q = x * c;
+    return fmaf(fmaf(-127.f, q, x), c, q);
+}
+
+// One 8-bit row's share of a lane: values 32 w + 8 t .. + 7.  The four lanes of the
+// row take part.  Scale: the fp32 nearest to the largest magnitude / 127 (NaN where
+// the row holds a NaN or an infinity; its codes are then 0), code: x * r rounded to
+// the nearest whole number (halves to even), r the fp32 nearest to 1 / scale.
+template <int W>
+RKV_DEV void quantise8_store(const float (&v)[W][8], int t, bool write, uint8_t* codes,
+                             float* scale) {
+    const uint32_t quad = 0xfu << (threadIdx.x & 28);
+    float mx = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) mx = max_of(mx, fabsf(v[w][i]), fabsf(v[w][i + 1]));
+#pragma unroll
+    for (int o = 1; o <= 2; o <<= 1) mx = max_of(mx, mx, __shfl_xor_sync(quad, mx, o));
+    const bool good = mx <= FLT_MAX;
+    const float s = good ? part_of_127(mx) : __int_as_float(0x7fffffff);
+    const float r = good && s >= FLT_MIN ? __frcp_rn(s) : 0.f;
+    if (!write) return;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        uint32_t b[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                c[i] = __float_as_uint(fmaf(good ? v[w][4 * k + i] : 0.f, r, 12582912.f));
+            b[k] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        }
+        *reinterpret_cast<uint2*>(codes + 32 * w + 8 * t) = make_uint2(b[0], b[1]);
+    }
+    if (t == 0) *scale = s;
+}
+
 // One 4-bit row's share of a lane: values of W groups.  The four lanes of the
 // row take part.
 template <int W>
@@ -368,18 +415,20 @@ template <typename T> constexpr int kHeads = sizeof(T) == 2 ? 4 : 2;
 
 // VEC: the rotated part splits into whole steps of eight.  A unit is one item
 // (the eight pairs, or eight elements, that a thread holds; without VEC one
-// pair or element) of kHeads heads, or a lane of a 4-bit row.
+// pair or element) of kHeads heads, or a lane of a row of BITS bits (0: the pools
+// hold T).
 // 64 registers, eight blocks an SM, where the compiler would take more (28.9
 // thousand tokens appended at 80: 127 us against 122; 16384 at 4 bits 72 against
 // 64.5; at 56 and less these spill: 81 and 78); the others are left to it (the
 // interleaved rotation of 16384 x 48 heads 67.5 us, 69.6 bounded).
-template <typename T, bool INTER, bool Q4>
-constexpr int kBlocks = Q4 || (sizeof(T) == 2 && !INTER) ? 8 : 0;
-template <typename T, bool VEC, bool INTER, bool Q4, int W>
-__global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel(const __grid_constant__ Params p) {
+template <typename T, bool INTER, bool PACKED>
+constexpr int kBlocks = PACKED || (sizeof(T) == 2 && !INTER) ? 8 : 0;
+template <typename T, bool VEC, bool INTER, int BITS, int W>
+__global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, BITS != 0>) tokens_kernel(const __grid_constant__ Params p) {
+    constexpr bool PACKED = BITS != 0;
     extern __shared__ __align__(16) uint8_t smem[];
     Token* tok = reinterpret_cast<Token*>(smem);                          // [tokens]
-    float* sines = reinterpret_cast<float*>(smem + sizeof(Token) * p.tokens);  // 4 bits: [tokens][2][half]
+    float* sines = reinterpret_cast<float*>(smem + sizeof(Token) * p.tokens);  // packed: [tokens][2][half]
     __shared__ uint64_t turns[kTurns];
     constexpr int HG = kHeads<T>, PAIRS = VEC ? (INTER ? 4 : 8) : 1;
     const TokenArgs& a = p.a;
@@ -410,17 +459,17 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
 
     // sources: tokens by sequence, or numbered through
     const int64_t seq = a.cu ? 0 : div_by((uint32_t)j, p.div_seq), within = j - seq * a.per_seq;
-    const bool is_k = !Q4 && !is_q && unit < (uint32_t)p.uk;
+    const bool is_k = !PACKED && !is_q && unit < (uint32_t)p.uk;
     const RowsView& src = is_q ? a.q : (is_k ? a.k : a.v);
     uint32_t item = 0, head = 0;
     bool turning = false;  // the item is turned (else copied)
     int at = 0;            // its first element
     Eight<T> x[HG], y[HG];
-    [[maybe_unused]] Eight<T> row4[W];
+    [[maybe_unused]] Eight<T> packed[W];
     T one_x[HG], one_y[HG];
-    [[maybe_unused]] bool is_v4 = false;
+    [[maybe_unused]] bool is_pv = false;
     const T* from = nullptr;
-    if (!Q4 || is_q) {
+    if (!PACKED || is_q) {
         const uint32_t u = is_q || is_k ? unit : unit - p.uk;
         const bool rotated = is_q || is_k;
         const uint32_t g = div_by(u, rotated ? p.div_iph : p.div_ipv);
@@ -449,16 +498,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
                 if (turning) one_y[k] = f[INTER ? 1 : p.half];
             }
         }
-    } else if constexpr (Q4) {
+    } else if constexpr (PACKED) {
         // K of all heads, then V: a warp rarely holds both
         const uint32_t r = unit >> 2;
-        is_v4 = r >= (uint32_t)a.k.heads;
-        head = r - (is_v4 ? a.k.heads : 0);
-        const RowsView& v = is_v4 ? a.v : a.k;
+        is_pv = r >= (uint32_t)a.k.heads;
+        head = r - (is_pv ? a.k.heads : 0);
+        const RowsView& v = is_pv ? a.v : a.k;
         from = static_cast<const T*>(v.data) + seq * v.seq + within * v.tok + head * v.head;
         if (on)
 #pragma unroll
-            for (int w = 0; w < W; ++w) row4[w].load(from + 32 * w + 8 * (unit & 3));
+            for (int w = 0; w < W; ++w) packed[w].load(from + 32 * w + 8 * (unit & 3));
     }
 
     if (tid < p.half) turns[turn_slot<PAIRS>(tid)] = a.turns[tid];
@@ -476,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
             if ((tid & 31) == 0) tok[i] = x;
         }
         __syncthreads();
-        if constexpr (Q4) {
+        if constexpr (PACKED) {
             if (!is_q) {
 #pragma unroll 1  // (unrolled, the append takes 78 us instead of 64.5)
                 for (int q = tid; q < n * p.half; q += kThreads) {
@@ -495,10 +544,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
         if (on && a.cu) t.live = j < a.cu[a.num_seqs] && j >= a.cu[0];
         if (p.half > 0) __syncthreads();  // the turns
     }
-    if (!on || !t.live) return;  // (a 4-bit row's four lanes leave together)
+    if (!on || !t.live) return;  // (a packed row's four lanes leave together)
 
     const int64_t hs = (int64_t)1 << a.pg.log2bs;  // rows between heads of a block
-    if (!Q4 || is_q) {
+    if (!PACKED || is_q) {
         if (!is_q && append && t.row < 0) return;
         T* to;
         int64_t step;
@@ -562,27 +611,34 @@ __global__ void __launch_bounds__(kThreads, kBlocks<T, INTER, Q4>) tokens_kernel
                 q[INTER ? 1 : p.half] = one_of<T>(v * c + u * s);
             }
         }
-    } else if constexpr (Q4) {
+    } else if constexpr (PACKED) {
         const int l = unit & 3;
         float v[W][8];
 #pragma unroll
-        for (int w = 0; w < W; ++w) row4[w].get(v[w]);
-        if (!is_v4 && p.half > 0) {
+        for (int w = 0; w < W; ++w) packed[w].get(v[w]);
+        if (!is_pv && p.half > 0) {
             const float* cs = sines + tl * 2 * p.half;
             turn_row<T, VEC, INTER, W>(v, from, l, p, cs, cs + p.half);
         }
         const int64_t row = t.row + head * hs;
-        quantise_store<W>(v, l, t.row >= 0, (is_v4 ? a.q4p.v_codes : a.q4p.k_codes) + row * (a.d / 2),
-                          (is_v4 ? a.q4p.v_scales : a.q4p.k_scales) + row * W);
+        if constexpr (BITS == 4)
+            quantise_store<W>(v, l, t.row >= 0, (is_pv ? a.q4p.v_codes : a.q4p.k_codes) + row * (a.d / 2),
+                              (is_pv ? a.q4p.v_scales : a.q4p.k_scales) + row * W);
+        else
+            quantise8_store<W>(v, l, t.row >= 0, (is_pv ? a.q8p.v_codes : a.q8p.k_codes) + row * a.d,
+                               (is_pv ? a.q8p.v_scales : a.q8p.k_scales) + row);
     }
 }
 
 template <typename T, bool VEC, bool INTER>
 cudaError_t go(const Params& p, unsigned grid, size_t smem, cudaStream_t s) {
-    if (!p.a.q4)
-        return launch_early(tokens_kernel<T, VEC, INTER, false, 2>, grid, kThreads, smem, s, p);
-    return p.a.d == 128 ? launch_early(tokens_kernel<T, VEC, INTER, true, 4>, grid, kThreads, smem, s, p)
-                        : launch_early(tokens_kernel<T, VEC, INTER, true, 2>, grid, kThreads, smem, s, p);
+    if (p.a.bits == 0)
+        return launch_early(tokens_kernel<T, VEC, INTER, 0, 2>, grid, kThreads, smem, s, p);
+    if (p.a.bits == 8)
+        return p.a.d == 128 ? launch_early(tokens_kernel<T, VEC, INTER, 8, 4>, grid, kThreads, smem, s, p)
+                            : launch_early(tokens_kernel<T, VEC, INTER, 8, 2>, grid, kThreads, smem, s, p);
+    return p.a.d == 128 ? launch_early(tokens_kernel<T, VEC, INTER, 4, 4>, grid, kThreads, smem, s, p)
+                        : launch_early(tokens_kernel<T, VEC, INTER, 4, 2>, grid, kThreads, smem, s, p);
 }
 template <typename T>
 cudaError_t go(Params& p, cudaStream_t s) {
@@ -595,8 +651,8 @@ cudaError_t go(Params& p, cudaStream_t s) {
     constexpr int HG = kHeads<T>;
     const auto groups = [&](int heads) { return (heads + HG - 1) / HG; };
     p.uq = a.q.data ? groups(a.q.heads) * p.iph : 0;
-    p.uk = a.k.data && !a.q4 ? groups(a.k.heads) * p.iph : 0;
-    p.ukv = a.q4 ? a.k.heads * 2 * 4 : p.uk + (a.v.data ? groups(a.v.heads) * p.ipv : 0);
+    p.uk = a.k.data && !a.bits ? groups(a.k.heads) * p.iph : 0;
+    p.ukv = a.bits ? a.k.heads * 2 * 4 : p.uk + (a.v.data ? groups(a.v.heads) * p.ipv : 0);
     p.total_q = a.num_tokens * p.uq;
     p.total_kv = a.num_tokens * p.ukv;
     const int least = p.uq > 0 && (p.ukv == 0 || p.uq < p.ukv) ? p.uq : p.ukv;
@@ -615,7 +671,7 @@ cudaError_t go(Params& p, cudaStream_t s) {
     p.minor = (uint32_t)(p.minor_q ? qb : kb);
     p.period = make_div(p.minor ? (uint32_t)((p.minor_q ? kb : qb) / p.minor) + 1 : 1);
     const size_t smem = a.pg.table ? sizeof(Token) * p.tokens +
-                                         (a.q4 ? sizeof(float) * 2 * p.half * p.tokens : 0)
+                                         (a.bits ? sizeof(float) * 2 * p.half * p.tokens : 0)
                                    : 0;
     const unsigned g = (unsigned)blocks;
     if (a.interleaved)
@@ -682,6 +738,55 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const __grid_constant
     }
 }
 
+// ------------------------------------------------------------- q8 read --
+
+// Sixteen values of a row a thread.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) q8_read_kernel(const __grid_constant__ Q8ReadArgs a,
+                                                           int64_t total, int both, Div by_rows,
+                                                           Div by_heads) {
+    let_next_begin();
+    wait_for_last();
+    constexpr int N = D / 16;
+    const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (e >= total) return;
+    const int t = (int)(e % N);
+    uint32_t r = div_by((uint32_t)(e / N), by_rows);  // problem (and tensor)
+    const int i = (int)((uint32_t)(e / N) - r * (uint32_t)a.n_rows);
+    bool is_v = a.out_k == nullptr;
+    if (both) {
+        is_v = r & 1;
+        r >>= 1;
+    }
+    const uint32_t s = div_by(r, by_heads), h = r - s * (uint32_t)a.pg.H;
+    const int64_t row = (a.first ? a.first[s] : 0) + (int64_t)i;
+    if (row >= a.lens[s]) return;
+    int64_t phys = -1;
+    if (row >= 0 && row < ((int64_t)a.pg.max_blocks << a.pg.log2bs)) {
+        const int blk = a.pg.table[(int64_t)s * a.pg.max_blocks + (row >> a.pg.log2bs)];
+        if ((unsigned)blk < (unsigned)a.pg.num_blocks)
+            phys = (((int64_t)blk * a.pg.H + h) << a.pg.log2bs) | (row & ((1 << a.pg.log2bs) - 1));
+    }
+    if (phys < 0) {
+        set_error(a.status, kDevErrIndex, (unsigned)s);
+        return;
+    }
+    const uint4 c = reinterpret_cast<const uint4*>((is_v ? a.p.v_codes : a.p.k_codes) + phys * D)[t];
+    const float sc = (is_v ? a.p.v_scales : a.p.k_scales)[phys];
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    T* dst = static_cast<T*>(is_v ? a.out_v : a.out_k) + ((int64_t)r * a.n_rows + i) * D + 16 * t;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            v[x] = sc * (float)(int8_t)(uint8_t)(w[2 * k + (x >> 2)] >> (8 * (x & 3)));
+        Eight<T> o;
+        o.set(v);
+        o.store(dst + 8 * k);
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_tokens(const TokenArgs& a, cudaStream_t s) {
@@ -704,6 +809,20 @@ cudaError_t launch_q4_read(const Q4ReadArgs& a, cudaStream_t s) {
                             g, kThreads, 0, s, a, total, both, rows, heads);
     }
     return launch_early(a.d == 128 ? q4_read_kernel<float, 4> : q4_read_kernel<float, 2>, g, kThreads,
+                        0, s, a, total, both, rows, heads);
+}
+
+cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
+    const int both = a.out_k && a.out_v;
+    const int64_t total = a.num_seqs * a.pg.H * (int64_t)a.n_rows * (a.d / 16) * (both ? 2 : 1);
+    if (total == 0) return cudaSuccess;
+    const unsigned g = (unsigned)((total + kThreads - 1) / kThreads);
+    const Div rows = make_div((uint32_t)a.n_rows), heads = make_div((uint32_t)a.pg.H);
+    if (a.dtype == RKV_DTYPE_BF16) {
+        return launch_early(a.d == 128 ? q8_read_kernel<__nv_bfloat16, 128> : q8_read_kernel<__nv_bfloat16, 64>,
+                            g, kThreads, 0, s, a, total, both, rows, heads);
+    }
+    return launch_early(a.d == 128 ? q8_read_kernel<float, 128> : q8_read_kernel<float, 64>, g, kThreads,
                         0, s, a, total, both, rows, heads);
 }
 

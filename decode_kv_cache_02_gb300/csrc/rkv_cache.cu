@@ -1,5 +1,5 @@
 // rkv_cache.cu -- the C ABI of the cache in use (declared in include/rkv.h):
-// rotary plans, appends to paged and 4-bit caches, and attention over them.
+// rotary plans, appends to paged and packed caches, and attention over them.
 // Argument checks and the launch of k_tokens.cu and k_attention.cu; nothing
 // here allocates or synchronises, and no state is kept between calls but on
 // which devices an attention kernel's shared memory has been asked for (the
@@ -195,6 +195,23 @@ bool meets_any(const Span& pool, const Span& out, const Span (&in)[3]) {
     return overlap(pool, out) || overlap(pool, in[0]) || overlap(pool, in[1]) || overlap(pool, in[2]);
 }
 
+int check_q8(const rkv_paged_desc* d, const rkv_q8_cache* c, rkv::Q8Pools* p, Span (&spans)[4]) {
+    if (!c) return RKV_ERR_INVALID_ARG;
+    void* const at[4] = {c->k_codes, c->k_scales, c->v_codes, c->v_scales};
+    const int64_t rows = pool_rows(d);
+    for (int i = 0; i < 4; ++i) {
+        if (!at[i] || !aligned16(at[i])) return RKV_ERR_INVALID_ARG;
+        spans[i] = span_of(at[i], rows * (i % 2 ? 4 : d->head_dim));
+        for (int j = 0; j < i; ++j)
+            if (overlap(spans[i], spans[j])) return RKV_ERR_ALIAS;
+    }
+    p->k_codes = static_cast<uint8_t*>(at[0]);
+    p->k_scales = static_cast<float*>(at[1]);
+    p->v_codes = static_cast<uint8_t*>(at[2]);
+    p->v_scales = static_cast<float*>(at[3]);
+    return RKV_OK;
+}
+
 int check_q4(const rkv_paged_desc* d, const rkv_q4_cache* c, rkv::Q4Pools* p, Span (&spans)[4]) {
     if (!c) return RKV_ERR_INVALID_ARG;
     void* const at[4] = {c->k_codes, c->k_scales, c->v_codes, c->v_scales};
@@ -214,19 +231,19 @@ int check_q4(const rkv_paged_desc* d, const rkv_q4_cache* c, rkv::Q4Pools* p, Sp
 
 // The sizes of an attention call; the plan follows from them alone.
 int check_attention(const rkv_paged_desc* desc, const int32_t* table, int n_new, int max_rows,
-                    bool q4, AttnArgs* a) {
+                    int bits, AttnArgs* a) {
     const int rc = rkv::check_paged_call(desc, table, &a->pg);
     if (rc) return rc;
     if (n_new < 1 || max_rows < 1 ||
         (int64_t)max_rows > (int64_t)desc->max_blocks_per_seq * desc->block_size)
         return RKV_ERR_INVALID_ARG;
     if (n_new > RKV_MAX_NEW_TOKENS || max_rows > (1 << 30) || (int64_t)desc->num_kv_heads * desc->gqa_group > kMaxHeads ||
-        (q4 && desc->dtype != RKV_DTYPE_BF16))
+        (bits && desc->dtype != RKV_DTYPE_BF16))
         return RKV_ERR_UNSUPPORTED;
     a->dtype = desc->dtype;
     a->d = desc->head_dim;
     a->G = desc->gqa_group;
-    a->q4 = q4;
+    a->bits = bits;
     a->n_new = n_new;
     a->max_rows = max_rows;
     a->num_seqs = desc->num_seqs;
@@ -251,12 +268,12 @@ size_t attention_bytes(const AttnPlan& p) {
 }
 
 int attend(const rkv_paged_desc* desc, int n_new, const rkv_rows* q, const void* K_pool,
-           const void* V_pool, const rkv_q4_cache* cache, const int32_t* table,
+           const void* V_pool, const rkv_q4_cache* four, const rkv_q8_cache* eight, const int32_t* table,
            const int32_t* lens, int max_rows, float scale, const rkv_rows* out, float* lse,
-           void* workspace, size_t workspace_bytes, void* stream, bool q4) {
+           void* workspace, size_t workspace_bytes, void* stream, int bits) {
     AttnCall call;
     AttnArgs& a = call.args;
-    int rc = check_attention(desc, table, n_new, max_rows, q4, &a);
+    int rc = check_attention(desc, table, n_new, max_rows, bits, &a);
     if (rc) return rc;
     if (!isfinite(scale)) return RKV_ERR_INVALID_ARG;
     call.plan = rkv::attn_plan(a);
@@ -276,9 +293,10 @@ int attend(const rkv_paged_desc* desc, int n_new, const rkv_rows* q, const void*
     if ((rc = check_rows(out, a.dtype, a.d, Hq, desc->num_seqs, n_new, true, &a.out, &os)))
         return rc;
     if (overlap(qs, os)) return RKV_ERR_ALIAS;
-    if (q4) {
+    if (bits) {
         Span spans[4];
-        if ((rc = check_q4(desc, cache, &a.q4p, spans))) return rc;
+        if ((rc = bits == 4 ? check_q4(desc, four, &a.q4p, spans) : check_q8(desc, eight, &a.q8p, spans)))
+            return rc;
         for (const Span& sp : spans)
             if (overlap(sp, os)) return RKV_ERR_ALIAS;
     } else {
@@ -296,10 +314,45 @@ int attend(const rkv_paged_desc* desc, int n_new, const rkv_rows* q, const void*
     a.status = static_cast<DeviceStatus*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = rkv::timed_cache(q4 ? rkv::kCacheAttnQ4 : rkv::kCacheAttn, s, run_attention, &call);
+    cudaError_t e = rkv::timed_cache(bits == 8 ? rkv::kCacheAttnQ8 : (bits == 4 ? rkv::kCacheAttnQ4 : rkv::kCacheAttn),
+                                    s, run_attention, &call);
     if (e == cudaSuccess && pl.join)
         e = rkv::timed_cache(rkv::kCacheAttnCombine, s, run_combine, &call);
     return rc_of(e);
+}
+
+// Rows of a packed cache as values: the checks and the launch of both formats.
+template <typename Args, typename Cache, typename Check>
+int read_rows(const rkv_paged_desc* desc, const Cache* cache, const int32_t* block_table,
+              const int32_t* lens, const int32_t* first, int n_rows, void* out_K, void* out_V,
+              void* workspace, void* stream, Check check, rkv::CacheKernel kernel,
+              cudaError_t (*launch)(const void*, cudaStream_t), Args* a) {
+    int rc = rkv::check_paged_call(desc, block_table, &a->pg);
+    if (rc) return rc;
+    if (n_rows < 0) return RKV_ERR_INVALID_ARG;
+    if (workspace && !aligned_ws(workspace)) return RKV_ERR_WORKSPACE;
+    if (desc->num_seqs == 0 || n_rows == 0) return RKV_OK;
+    if (!block_table || !lens || (!out_K && !out_V) || !aligned16(out_K) || !aligned16(out_V))
+        return RKV_ERR_INVALID_ARG;
+    Span pools[4];
+    if ((rc = check(desc, cache, &a->p, pools))) return rc;
+    a->dtype = desc->dtype;
+    a->d = desc->head_dim;
+    const int64_t rows = desc->num_seqs * (int64_t)desc->num_kv_heads * n_rows;
+    if (rows >= ((int64_t)1 << 30)) return RKV_ERR_UNSUPPORTED;
+    const int64_t bytes = rows * a->d * elem(a->dtype);
+    const Span ks = span_of(out_K, out_K ? bytes : 0), vs = span_of(out_V, out_V ? bytes : 0);
+    if (overlap(ks, vs)) return RKV_ERR_ALIAS;
+    for (const Span& p : pools)
+        if (overlap(p, ks) || overlap(p, vs)) return RKV_ERR_ALIAS;
+    a->num_seqs = desc->num_seqs;
+    a->lens = lens;
+    a->first = first;
+    a->n_rows = n_rows;
+    a->out_k = out_K;
+    a->out_v = out_V;
+    a->status = static_cast<DeviceStatus*>(workspace);
+    return rc_of(rkv::timed_cache(kernel, static_cast<cudaStream_t>(stream), launch, a));
 }
 
 }  // namespace
@@ -441,59 +494,64 @@ int rkv_q4_append(const rkv_paged_desc* desc, const rkv_rope_plan* rope,
     if ((rc = check_q4(desc, cache, &a.q4p, pools))) return rc;
     for (const Span& p : pools)
         if (meets_any(p, out, in)) return RKV_ERR_ALIAS;
-    a.q4 = true;
+    a.bits = 4;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return rc_of(rkv::timed_cache(rkv::kCacheQ4Append, s, run_tokens, &a));
+}
+
+int rkv_q8_append(const rkv_paged_desc* desc, const rkv_rope_plan* rope,
+                  const rkv_q8_cache* cache, const int32_t* block_table, const int32_t* lens,
+                  int64_t num_tokens, int new_per_seq, const int32_t* cu_tokens,
+                  const int32_t* positions, const rkv_rows* k, const rkv_rows* v,
+                  const rkv_rows* q, const rkv_rows* out_q, void* workspace, void* stream) {
+    TokenArgs a;
+    Span out, in[3], pools[4];
+    int rc = check_append(desc, rope, block_table, lens, num_tokens, new_per_seq, cu_tokens,
+                          positions, k, v, q, out_q, workspace, &a, &out, in);
+    if (rc || a.num_tokens == 0) return rc;
+    if ((rc = check_q8(desc, cache, &a.q8p, pools))) return rc;
+    for (const Span& p : pools)
+        if (meets_any(p, out, in)) return RKV_ERR_ALIAS;
+    a.bits = 8;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return rc_of(rkv::timed_cache(rkv::kCacheQ8Append, s, run_tokens, &a));
 }
 
 int rkv_q4_read(const rkv_paged_desc* desc, const rkv_q4_cache* cache,
                 const int32_t* block_table, const int32_t* lens, const int32_t* first,
                 int n_rows, void* out_K, void* out_V, void* workspace, void* stream) {
     rkv::Q4ReadArgs a;
-    int rc = rkv::check_paged_call(desc, block_table, &a.pg);
-    if (rc) return rc;
-    if (n_rows < 0) return RKV_ERR_INVALID_ARG;
-    if (workspace && !aligned_ws(workspace)) return RKV_ERR_WORKSPACE;
-    if (desc->num_seqs == 0 || n_rows == 0) return RKV_OK;
-    if (!block_table || !lens || (!out_K && !out_V) || !aligned16(out_K) || !aligned16(out_V))
-        return RKV_ERR_INVALID_ARG;
-    Span pools[4];
-    if ((rc = check_q4(desc, cache, &a.p, pools))) return rc;
-    a.dtype = desc->dtype;
-    a.d = desc->head_dim;
-    const int64_t rows = desc->num_seqs * (int64_t)desc->num_kv_heads * n_rows;
-    if (rows >= ((int64_t)1 << 30)) return RKV_ERR_UNSUPPORTED;
-    const int64_t bytes = rows * a.d * elem(a.dtype);
-    const Span ks = span_of(out_K, out_K ? bytes : 0), vs = span_of(out_V, out_V ? bytes : 0);
-    if (overlap(ks, vs)) return RKV_ERR_ALIAS;
-    for (const Span& p : pools)
-        if (overlap(p, ks) || overlap(p, vs)) return RKV_ERR_ALIAS;
-    a.num_seqs = desc->num_seqs;
-    a.lens = lens;
-    a.first = first;
-    a.n_rows = n_rows;
-    a.out_k = out_K;
-    a.out_v = out_V;
-    a.status = static_cast<DeviceStatus*>(workspace);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return rc_of(rkv::timed_cache(
-        rkv::kCacheQ4Read, s,
-        [](const void* x, cudaStream_t st) {
-            return rkv::launch_q4_read(*static_cast<const rkv::Q4ReadArgs*>(x), st);
-        },
-        &a));
+    return read_rows(desc, cache, block_table, lens, first, n_rows, out_K, out_V, workspace, stream,
+                     check_q4, rkv::kCacheQ4Read,
+                     [](const void* x, cudaStream_t st) {
+                         return rkv::launch_q4_read(*static_cast<const rkv::Q4ReadArgs*>(x), st);
+                     },
+                     &a);
+}
+
+int rkv_q8_read(const rkv_paged_desc* desc, const rkv_q8_cache* cache,
+                const int32_t* block_table, const int32_t* lens, const int32_t* first,
+                int n_rows, void* out_K, void* out_V, void* workspace, void* stream) {
+    rkv::Q8ReadArgs a;
+    return read_rows(desc, cache, block_table, lens, first, n_rows, out_K, out_V, workspace, stream,
+                     check_q8, rkv::kCacheQ8Read,
+                     [](const void* x, cudaStream_t st) {
+                         return rkv::launch_q8_read(*static_cast<const rkv::Q8ReadArgs*>(x), st);
+                     },
+                     &a);
 }
 
 size_t rkv_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int max_rows) {
-    // one size serves the pool and the 4-bit cache
+    // one size serves the pool and the packed caches
     AttnArgs a;
-    if (check_attention(desc, nullptr, n_new, max_rows, false, &a)) return 0;
+    if (check_attention(desc, nullptr, n_new, max_rows, 0, &a)) return 0;
     size_t n = attention_bytes(rkv::attn_plan(a));
-    if (desc->dtype == RKV_DTYPE_BF16) {
-        a.q4 = true;
-        const size_t m = attention_bytes(rkv::attn_plan(a));
-        if (m > n) n = m;
-    }
+    if (desc->dtype == RKV_DTYPE_BF16)
+        for (const int bits : {4, 8}) {
+            a.bits = bits;
+            const size_t m = attention_bytes(rkv::attn_plan(a));
+            if (m > n) n = m;
+        }
     return n;
 }
 
@@ -501,16 +559,24 @@ int rkv_paged_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q
                         const void* K_pool, const void* V_pool, const int32_t* block_table,
                         const int32_t* lens, int max_rows, float scale, const rkv_rows* out,
                         float* lse, void* workspace, size_t workspace_bytes, void* stream) {
-    return attend(desc, n_new, q, K_pool, V_pool, nullptr, block_table, lens, max_rows, scale, out,
-                  lse, workspace, workspace_bytes, stream, false);
+    return attend(desc, n_new, q, K_pool, V_pool, nullptr, nullptr, block_table, lens, max_rows, scale,
+                  out, lse, workspace, workspace_bytes, stream, 0);
 }
 
 int rkv_q4_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
                      const rkv_q4_cache* cache, const int32_t* block_table, const int32_t* lens,
                      int max_rows, float scale, const rkv_rows* out, float* lse, void* workspace,
                      size_t workspace_bytes, void* stream) {
-    return attend(desc, n_new, q, nullptr, nullptr, cache, block_table, lens, max_rows, scale, out,
-                  lse, workspace, workspace_bytes, stream, true);
+    return attend(desc, n_new, q, nullptr, nullptr, cache, nullptr, block_table, lens, max_rows, scale,
+                  out, lse, workspace, workspace_bytes, stream, 4);
+}
+
+int rkv_q8_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
+                     const rkv_q8_cache* cache, const int32_t* block_table, const int32_t* lens,
+                     int max_rows, float scale, const rkv_rows* out, float* lse, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    return attend(desc, n_new, q, nullptr, nullptr, nullptr, cache, block_table, lens, max_rows, scale,
+                  out, lse, workspace, workspace_bytes, stream, 8);
 }
 
 }  // extern "C"

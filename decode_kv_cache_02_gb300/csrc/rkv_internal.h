@@ -216,8 +216,16 @@ struct Q4Pools {
     uint32_t* v_scales = nullptr;
 };
 
+// The four arrays of an 8-bit cache: codes (head_dim bytes a row) and scales.
+struct Q8Pools {
+    uint8_t* k_codes = nullptr;
+    float* k_scales = nullptr;
+    uint8_t* v_codes = nullptr;
+    float* v_scales = nullptr;
+};
+
 // New tokens on their way to a cache, or through the rotation alone (table ==
-// nullptr): see rkv_rope_apply, rkv_paged_append, rkv_q4_append.
+// nullptr): see rkv_rope_apply, rkv_paged_append, rkv_q4_append, rkv_q8_append.
 struct TokenArgs {
     int dtype = 0, d = 0;
     int rot = 0;  // 0: no rotation
@@ -234,8 +242,9 @@ struct TokenArgs {
     const int32_t* cu = nullptr;
     void* k_pool = nullptr;
     void* v_pool = nullptr;
-    bool q4 = false;
+    int bits = 0;  // 0: pools of dtype, 4: q4p, 8: q8p
     Q4Pools q4p;
+    Q8Pools q8p;
     DeviceStatus* status = nullptr;
 };
 cudaError_t launch_tokens(const TokenArgs& a, cudaStream_t s);
@@ -254,16 +263,31 @@ struct Q4ReadArgs {
 };
 cudaError_t launch_q4_read(const Q4ReadArgs& a, cudaStream_t s);
 
-// One attention call over a paged cache (bf16, fp32 or 4-bit).
+struct Q8ReadArgs {
+    int dtype = 0, d = 0;
+    PagedIn pg;
+    int64_t num_seqs = 0;
+    const int32_t* lens = nullptr;
+    const int32_t* first = nullptr;
+    int n_rows = 0;
+    Q8Pools p;
+    void* out_k = nullptr;
+    void* out_v = nullptr;
+    DeviceStatus* status = nullptr;
+};
+cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
+
+// One attention call over a paged cache (bf16, fp32, 4-bit or 8-bit).
 struct AttnArgs {
     int dtype = 0, d = 0, G = 1;
-    bool q4 = false;
+    int bits = 0;  // 0: pools of dtype, 4: q4p, 8: q8p
     int n_new = 1, max_rows = 0;
     int64_t num_seqs = 0;
     PagedIn pg;
-    const void* k = nullptr;  // pools (unused with q4)
+    const void* k = nullptr;  // pools (bits 0)
     const void* v = nullptr;
     Q4Pools q4p;
+    Q8Pools q8p;
     RowsView q, out;
     const int32_t* lens = nullptr;
     float scale = 1.f;
@@ -293,7 +317,10 @@ enum CacheKernel {
     kCacheQ4Read,
     kCacheAttn,
     kCacheAttnQ4,
-    kCacheAttnCombine
+    kCacheAttnCombine,
+    kCacheQ8Append,
+    kCacheQ8Read,
+    kCacheAttnQ8
 };
 cudaError_t timed_cache(CacheKernel kernel, cudaStream_t s,
                         cudaError_t (*launch)(const void*, cudaStream_t), const void* arg);

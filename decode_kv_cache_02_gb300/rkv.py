@@ -31,7 +31,8 @@ EXPORTED = [
     "rkv_noalloc_device_status", "rkv_noalloc_selftest_wait_timeout", "rkv_set_overlap",
     "rkv_trace_enable", "rkv_trace_read", "rkv_rope_init", "rkv_rope_init_freqs",
     "rkv_rope_apply", "rkv_paged_append", "rkv_q4_append", "rkv_q4_read",
-    "rkv_attention_workspace_size", "rkv_paged_attention", "rkv_q4_attention",
+    "rkv_attention_workspace_size", "rkv_paged_attention", "rkv_q4_attention", "rkv_q8_append",
+    "rkv_q8_read", "rkv_q8_attention",
 ]
 RKV_MAX_POOL_WINDOW = 255
 RKV_ERR_DEVICE = 6
@@ -162,6 +163,11 @@ class _Q4Cache(ctypes.Structure):
                 ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
 
 
+class _Q8Cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -262,6 +268,12 @@ def load(path: str | None = None):
         lib.rkv_paged_attention.restype = i32
         lib.rkv_q4_attention.argtypes = [vp, i32, vp, vp, vp, vp, i32, f32, vp, vp, vp, sz, vp]
         lib.rkv_q4_attention.restype = i32
+        lib.rkv_q8_append.argtypes = lib.rkv_q4_append.argtypes
+        lib.rkv_q8_append.restype = i32
+        lib.rkv_q8_read.argtypes = lib.rkv_q4_read.argtypes
+        lib.rkv_q8_read.restype = i32
+        lib.rkv_q8_attention.argtypes = lib.rkv_q4_attention.argtypes
+        lib.rkv_q8_attention.restype = i32
         lib.rkv_kernel_name.argtypes = [i32]
         lib.rkv_kernel_name.restype = ctypes.c_char_p
         _lib = lib

@@ -303,7 +303,7 @@ int rkv_paged_compress(const rkv_paged_desc* desc, void* K_pool, void* V_pool,
 /* ------------------------------------------------------ the cache in use --
  * What a decode loop does with a paged cache between two compressions:
  * rotate the new tokens' queries and keys by their positions, write the new
- * rows through the block table (as they are, or at 4 bits), and attend over
+ * rows through the block table (as they are, or at 4 or 8 bits), and attend over
  * the rows.  After a compression a row of the cache is no longer its token's
  * position, so the calls take the positions (int32 [tokens]) apart from the
  * rows (lens).
@@ -444,6 +444,33 @@ int rkv_q4_read(const rkv_paged_desc* desc, const rkv_q4_cache* cache,
                 const int32_t* block_table, const int32_t* lens, const int32_t* first,
                 int n_rows, void* out_K, void* out_V, void* workspace, void* stream);
 
+/* A paged cache held in 8 bits: each row of head_dim values as x ~ scale * code,
+ *   scale the fp32 nearest to the row's largest magnitude / 127,
+ *   code  the whole number nearest to x * r, r the fp32 nearest to 1 / scale (0
+ *         where the scale is below 2^-126); halves go to even; -127 .. 127.
+ * A row that holds a NaN or an infinity reads as NaN.  codes [num_blocks,
+ * num_kv_heads, block_size, head_dim] int8, in the values' order; scales
+ * [num_blocks, num_kv_heads, block_size] fp32.  All four arrays are 16-byte
+ * aligned. */
+typedef struct {
+    void* k_codes;
+    void* k_scales;
+    void* v_codes;
+    void* v_scales;
+} rkv_q8_cache;
+
+/* rkv_paged_append into an 8-bit cache (desc->dtype: that of k, v and q). */
+int rkv_q8_append(const rkv_paged_desc* desc, const rkv_rope_plan* rope,
+                  const rkv_q8_cache* cache, const int32_t* block_table, const int32_t* lens,
+                  int64_t num_tokens, int new_per_seq, const int32_t* cu_tokens,
+                  const int32_t* positions, const rkv_rows* k, const rkv_rows* v,
+                  const rkv_rows* q, const rkv_rows* out_q, void* workspace, void* stream);
+
+/* rkv_q4_read of an 8-bit cache: scale * code, rounded to desc->dtype. */
+int rkv_q8_read(const rkv_paged_desc* desc, const rkv_q8_cache* cache,
+                const int32_t* block_table, const int32_t* lens, const int32_t* first,
+                int n_rows, void* out_K, void* out_V, void* workspace, void* stream);
+
 /* Attention of the newest n_new (1 .. RKV_MAX_NEW_TOKENS) tokens of every
  * sequence over its cache: token t sees rows j <= lens[s] - n_new + t,
  *   out[s, t, head] = sum_j p_j V_j,  p = softmax_j(scale * q . K_j)
@@ -469,7 +496,7 @@ int rkv_q4_read(const rkv_paged_desc* desc, const rkv_q4_cache* cache,
  * probabilities times V, before they are divided, are up to 2^8 sum |V| (fp32).
  * q, out: rkv_rows by sequence and token (bf16 for 4-bit caches). */
 #define RKV_MAX_NEW_TOKENS 64
-/* Bytes for the current device (the work is cut for its SMs) and either cache;
+/* Bytes for the current device (the work is cut for its SMs) and any of the caches;
  * 0: invalid sizes. */
 size_t rkv_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int max_rows);
 int rkv_paged_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
@@ -478,6 +505,15 @@ int rkv_paged_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q
                         float* lse, void* workspace, size_t workspace_bytes, void* stream);
 int rkv_q4_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
                      const rkv_q4_cache* cache, const int32_t* block_table,
+                     const int32_t* lens, int max_rows, float scale, const rkv_rows* out,
+                     float* lse, void* workspace, size_t workspace_bytes, void* stream);
+/* The same over an 8-bit cache (q and out bf16).  Codes enter the products as
+ * bf16 numbers, exactly; K's scale meets the logit and V's the probability in
+ * fp32, and the probability times the scale goes on as a bf16 cache's
+ * probabilities do (two bf16 parts, one where n_new * gqa_group is above 16).
+ * What a hidden row holds, codes or scale, reaches no query. */
+int rkv_q8_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
+                     const rkv_q8_cache* cache, const int32_t* block_table,
                      const int32_t* lens, int max_rows, float scale, const rkv_rows* out,
                      float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
