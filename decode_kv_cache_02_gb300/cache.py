@@ -32,6 +32,7 @@ _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 _pack_rows = struct.Struct("@Pqqq").pack      # rkv_rows
 _pack_desc = struct.Struct("@q7i4x").pack     # rkv_paged_desc
 _pack_q4 = struct.Struct("@4P").pack          # rkv_q4_cache
+_pack_prefixes = struct.Struct("@3P3i4x").pack  # rkv_prefixes
 _current_device = torch.cuda.current_device
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -503,7 +504,7 @@ def alloc_attention_workspace(q, num_kv_heads: int, max_rows: int) -> torch.Tens
 
 
 def _attention(call, where, cache_args, dev, shape, q, block_table, lens, max_rows, scale, out,
-               lse, workspace):
+               lse, workspace, prefixes=None):
     nb, H, bs, d = shape
     sh = q.shape
     if len(sh) != 4:
@@ -534,7 +535,10 @@ def _attention(call, where, cache_args, dev, shape, q, block_table, lens, max_ro
         at = lse.data_ptr()
     desc = _pack_desc(S, H, G, d, bs, nb, mb, _dtype(q))
     if workspace is None:
-        n = load().rkv_attention_workspace_size(desc, T, max_rows)
+        if prefixes is None:
+            n = load().rkv_attention_workspace_size(desc, T, max_rows)
+        else:
+            n = load().rkv_prefix_attention_workspace_size(desc, T, max_rows, prefixes)
         workspace = torch.empty(max(n, 256), dtype=_U8, device=q.device)
     wp, wn = _workspace(workspace, dev)
     tokens = S * T
@@ -591,3 +595,84 @@ def rkv_q8_attention(q, cache: Q8Cache, block_table, lens, max_rows: int | None 
     return _attention(load().rkv_q8_attention, "rkv_q8_attention", (cache._packed,),
                       at.get_device(), cache.shape, q, block_table, lens, max_rows, scale, out,
                       lse, workspace)
+
+
+# --------------------------------------------------------- shared prefixes --
+
+def _prefix_sizes(q, H, max_rows, num_prefixes, max_prefix_rows):
+    if q.dim() != 4 or H < 1 or q.shape[2] == 0 or q.shape[2] % H:
+        raise ValueError("q must be [num_seqs, n_new, H * gqa_group, d]")
+    if not 0 < max_rows <= _MAX_ROWS or (num_prefixes and not 0 < max_prefix_rows <= _MAX_ROWS):
+        raise ValueError("max_rows and max_prefix_rows must be 1 .. 2^30")
+
+
+def rkv_prefix_attention_workspace_size(q, num_kv_heads: int, max_rows: int, num_prefixes: int,
+                                        max_prefix_rows: int) -> int:
+    """Workspace bytes of rkv_prefix_attention for q [S, n_new, heads, d] over at
+    most max_rows own rows a sequence and num_prefixes prefixes of at most
+    max_prefix_rows rows, however the sequences are shared out, on q's device."""
+    if q.is_cuda and q.get_device() != _current_device():
+        with torch.cuda.device(q.device):
+            return rkv_prefix_attention_workspace_size(q, num_kv_heads, max_rows, num_prefixes,
+                                                       max_prefix_rows)
+    H, P = int(num_kv_heads), int(num_prefixes)
+    max_rows, max_prefix_rows = int(max_rows), int(max_prefix_rows)
+    _prefix_sizes(q, H, max_rows, P, max_prefix_rows)
+    S, T, hq, d = q.shape
+    # (blocks of one row are the least that any pool has; the size does not depend on them, and with some cu_seqs the
+    # sequences need not divide)
+    desc = _pack_desc(S, H, hq // H, d, 1, 1, max_rows, _dtype(q))
+    rows = max(max_prefix_rows, 1)
+    n = int(load().rkv_prefix_attention_workspace_size(desc, T, max_rows,
+                                                       _pack_prefixes(0, 0, 256, P, rows, rows)))
+    if n == 0:
+        raise ValueError("invalid workspace request")
+    return n
+
+
+def alloc_prefix_attention_workspace(q, num_kv_heads: int, max_rows: int, num_prefixes: int,
+                                     max_prefix_rows: int) -> torch.Tensor:
+    """A zero-filled uint8 tensor of rkv_prefix_attention_workspace_size() bytes."""
+    return torch.zeros(rkv_prefix_attention_workspace_size(q, num_kv_heads, max_rows, num_prefixes,
+                                                           max_prefix_rows), dtype=_U8, device=q.device)
+
+
+def rkv_prefix_attention(q, K_pool, V_pool, prefix_table, prefix_lens, block_table, lens,
+                         cu_seqs=None, max_prefix_rows: int | None = None,
+                         max_rows: int | None = None, scale: float | None = None, out=None,
+                         lse=None, workspace=None, stream=None):
+    """rkv_paged_attention of sequences that share prefixes: rows of the pools
+    held once, named by prefix_table [P, blocks] with prefix_lens [P] rows (int32).
+    Sequences cu_seqs[p] .. cu_seqs[p + 1] - 1 (int32 [P + 1] on the device) share
+    prefix p, those behind the last have none; without cu_seqs every prefix has S /
+    P of them.  Every token sees its whole prefix, then its sequence's own rows as
+    in rkv_paged_attention (block_table and lens name those alone).
+    max_prefix_rows and max_rows bound the lengths (default: the tables' rows)."""
+    if _away(K_pool, stream):
+        return _elsewhere(rkv_prefix_attention, K_pool, stream, q, K_pool, V_pool, prefix_table,
+                          prefix_lens, block_table, lens, cu_seqs, max_prefix_rows, max_rows,
+                          scale, out, lse, workspace)
+    dev = K_pool.get_device()
+    nb, H, bs, d = _pools(K_pool, V_pool, dev)
+    if q.dtype != K_pool.dtype:
+        raise ValueError("q and the pools must share a dtype")
+    if prefix_table.dim() != 2:
+        raise ValueError("prefix_table must be int32 [num_prefixes, max_blocks]")
+    P, pb = prefix_table.shape
+    rows = pb * bs if max_prefix_rows is None else int(max_prefix_rows)
+    if P and not 0 < rows <= _MAX_ROWS:
+        raise ValueError("max_prefix_rows (by default the table's rows) must be 1 .. 2^30")
+    S = q.shape[0] if q.dim() == 4 else 0
+    if cu_seqs is None and P and S % P:
+        raise ValueError("without cu_seqs every prefix has the same number of sequences")
+    prefixes = _pack_prefixes(_ints(prefix_table, "prefix_table", dev, P, pb),
+                              _ints(prefix_lens, "prefix_lens", dev, P),
+                              0 if cu_seqs is None else _ints(cu_seqs, "cu_seqs", dev, P + 1),
+                              P, pb, rows)
+    call = load().rkv_prefix_attention
+
+    def with_prefixes(desc, n_new, rq, K, V, *rest):
+        return call(desc, n_new, rq, K, V, prefixes, *rest)
+    return _attention(with_prefixes, "rkv_prefix_attention", (K_pool.data_ptr(), V_pool.data_ptr()),
+                      dev, (nb, H, bs, d), q, block_table, lens, max_rows, scale, out, lse,
+                      workspace, prefixes)

@@ -49,8 +49,6 @@
 #include <cuda_fp16.h>
 #include <float.h>
 
-#include <atomic>
-
 #include "rkv_common.cuh"
 #include "rkv_internal.h"
 
@@ -122,6 +120,8 @@ struct Params {
     int num_seqs;
     int64_t q_seq, q_tok, q_head, o_seq, o_tok, o_head;
     float* lse;
+    float* raw;         // (see AttnArgs)
+    float* raw_ml;
     float* partial;     // [slot][rows][D]
     float* partial_ml;  // [slot][rows][2]
     int4* joins;        // [run][group]: (sequence, head, parts) of the problem to join, if parts
@@ -967,13 +967,28 @@ RKV_DEV void store4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack(v.x, v.y), pack(v.z, v.w));
 }
 
+// Four values of a query's output from its sums v relative to 2^mx, and the log of its
+// sum (or, where they are to be joined with others', v and mx and the sum as they are).
+template <typename T, int D>
+RKV_DEV void emit(const Params& p, int64_t s, int tk, int hd, int d, float4 v, float mx, float sum) {
+    const int64_t at = (s * p.T + tk) * (int64_t)p.H * p.G + hd;
+    if (p.raw) {
+        store4(p.raw + at * D + d, v);
+        if (d == 0) *reinterpret_cast<float2*>(p.raw_ml + 2 * at) = make_float2(mx, sum);
+        return;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    store4(reinterpret_cast<T*>(p.out) + s * p.o_seq + tk * p.o_tok + hd * p.o_head + d,
+           make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    if (d == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+}
+
 // Joins the warps' weighted sums in acc [kWarps][ROWS][D] and writes the rows:
 // the output where the chunk is the whole sequence, else its part.
 template <typename T, int D, int ROWS>
 RKV_DEV void finish(const Params& p, const float* acc, const float (&sh_m)[kWarps][ROWS],
                     const float (&sh_l)[kWarps][ROWS], int64_t s, int h, int row_first,
                     int64_t slot, bool whole) {
-    T* out = reinterpret_cast<T*>(p.out);
     for (int e = threadIdx.x; e < ROWS * D / 4; e += kWarps * 32) {
         const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
         const int row = row_first + r;
@@ -988,13 +1003,8 @@ RKV_DEV void finish(const Params& p, const float* acc, const float (&sh_m)[kWarp
             v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
         }
         if (whole) {
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
             const int tk = row / p.G, hd = h * p.G + row - tk * p.G;
-            store4(out + s * p.o_seq + tk * p.o_tok + hd * p.o_head + d,
-                   make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-            if (d == 0 && p.lse)
-                p.lse[(s * p.T + tk) * (int64_t)p.H * p.G + hd] =
-                    sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+            emit<T, D>(p, s, tk, hd, d, v, mx, sum);
         } else {
             *reinterpret_cast<float4*>(p.partial + (slot * ROWS + r) * D + d) = v;
             if (d == 0) {
@@ -1061,7 +1071,6 @@ RKV_DEV void finish_cluster(const Params& p, float* acc, const float (&sh_m)[kWa
         }
     }
     cluster_sync();
-    T* out = reinterpret_cast<T*>(p.out);
     for (int e = rank * (kWarps * 32) + tid; e < ROWS * D / 4; e += p.cluster * (kWarps * 32)) {
         const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
         const int row = row_first + r;
@@ -1087,13 +1096,8 @@ RKV_DEV void finish_cluster(const Params& p, float* acc, const float (&sh_m)[kWa
             sum += ml[i].y * f;
             v.x += x[i].x * f; v.y += x[i].y * f; v.z += x[i].z * f; v.w += x[i].w * f;
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int tk = row / p.G, hd = h * p.G + row - tk * p.G;
-        store4(out + s * p.o_seq + tk * p.o_tok + hd * p.o_head + d,
-               make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-        if (d == 0 && p.lse)
-            p.lse[((int64_t)s * p.T + tk) * p.H * p.G + hd] =
-                sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+        emit<T, D>(p, s, tk, hd, d, v, mx, sum);
     }
     cluster_sync();  // nobody leaves while its shared memory is read
 }
@@ -1799,14 +1803,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
     };
     auto write = [&](int r, float m, float l, float4 v) {
         const int row = group * rows + r;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
         const int tk = row / p.G, hd = h * p.G + row - tk * p.G;
-        if (lane < LANES)
-            store4(reinterpret_cast<T*>(p.out) + s * p.o_seq + tk * p.o_tok + hd * p.o_head + lane * 4,
-                   make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-        if (lane == 0 && p.lse)
-            p.lse[((int64_t)s * p.T + tk) * p.H * p.G + hd] =
-                l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (lane < LANES) emit<T, D>(p, s, tk, hd, lane * 4, v, m, l);
     };
     float m, l;
     float4 v;
@@ -1859,6 +1857,8 @@ Params params(const AttnArgs& a, const AttnPlan& pl) {
     p.q_seq = a.q.seq; p.q_tok = a.q.tok; p.q_head = a.q.head;
     p.o_seq = a.out.seq; p.o_tok = a.out.tok; p.o_head = a.out.head;
     p.lse = a.lse;
+    p.raw = a.raw;
+    p.raw_ml = a.raw_ml;
     p.partial = a.partial;
     const int64_t slots = 2 * (int64_t)pl.runs * pl.groups;
     p.partial_ml = a.partial + slots * pl.rows * a.d;
@@ -1875,20 +1875,6 @@ Params params(const AttnArgs& a, const AttnPlan& pl) {
     p.flip = x < 0.f ? 0x80008000u : 0u;
     p.status = a.status;
     return p;
-}
-
-// Dynamic shared memory past 48 KB has to be asked for once per kernel and
-// device (half a microsecond, so not at every call).
-template <typename K>
-cudaError_t allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
-    return e;
 }
 
 template <int D, int NT, int BITS, bool TWO>

@@ -1,0 +1,377 @@
+// k_prefix.cu -- attention of a batch whose sequences share long prefixes: the pass
+// over the prefixes on the CUDA cores (fp32 pools, and bf16 pools in blocks too small
+// for the tensor-core pass, k_prefix_tc.cu), and the join of its pieces.
+//
+// out = sum_j p_j V_j over the rows of the prefix, then the sequence's own: the softmax
+// over both is that of the sums over each, brought to a common maximum.  The own rows'
+// sums come from the attention over the cache (k_attention.cu), which goes first; here
+// the queries of all sequences of a prefix are the rows of one product, so the prefix
+// is read once for all of them.
+//
+// CUDA cores: a block takes 64 queries and 64 rows at a time through shared memory; a
+// thread holds 8 queries x 4 rows of the logits (rows tx, tx + 16, ..: reads of 8
+// neighbouring rows of 528 bytes meet no bank twice) and 8 queries x D / 16 of the
+// output, so four FMAs stand against each word that is read.
+#include <atomic>
+
+#include "rkv_prefix.cuh"
+
+namespace rkv {
+namespace prefix {
+namespace {
+
+constexpr int kTile = 64, kUnit = 64, kThreads = 128;
+
+RKV_DEV uint32_t smem_at(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+// Four values into shared memory as fp32 (ok: there are any, else zeros).
+RKV_DEV void fetch4(float* dst, const float* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_at(dst)), "l"(src),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+}
+RKV_DEV void fetch4(float* dst, const __nv_bfloat16* src, bool ok) {
+    uint2 x = make_uint2(0u, 0u);
+    if (ok) x = *reinterpret_cast<const uint2*>(src);
+    *reinterpret_cast<float4*>(dst) =
+        make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
+                    __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
+}
+RKV_DEV void fetched() {
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+}
+
+template <int D>
+struct Smem {
+    static constexpr int LD = D + 4, LP = kUnit + 4;
+    float q[kTile][LD], k[kUnit][LD], v[kUnit][D];  // (probabilities [kTile][LP] lie over k)
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2) prefix_kernel(const __grid_constant__ Params p) {
+    using M = Smem<D>;
+    static_assert(M::LP <= M::LD, "the probabilities fit over the keys");
+    extern __shared__ __align__(16) uint8_t raw[];
+    M& sm = *reinterpret_cast<M*>(raw);
+    float (*prob)[M::LP] = reinterpret_cast<float (*)[M::LP]>(&sm.k[0][0]);
+    __shared__ int64_t at_row[kUnit];  // pool row of each row of the unit (-1: none)
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const uint32_t run = blockIdx.x;
+    constexpr int NV = D / 64;  // float4 of the output a thread holds a query
+    const float sign = p.flip ? -1.f : 1.f;
+    wait_for_last();
+
+    Place place = find_place<kUnit>(p, run);
+    Piece c{};
+    while (next_piece<kUnit>(p, run, place, c)) {
+        if (tid == 0 && bad_length(p, c)) set_error(p.status, kDevErrIndex, (unsigned)c.i);
+        __syncthreads();  // the piece before has been read
+        for (int e = tid; e < kTile * (D / 4); e += kThreads) {
+            const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+            const bool ok = r < c.rows;
+            int s = 0, tk = 0, hd = 0;
+            if (ok) place_of_row(p, c.seq0, c.h, c.row0 + r, s, tk, hd);
+            fetch4(&sm.q[r][d], static_cast<const T*>(p.q) + s * p.q_seq + tk * p.q_tok + hd * p.q_head + d, ok);
+        }
+        float m[8], l[8], o[8][NV * 4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            m[i] = kNone;
+            l[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < NV * 4; ++j) o[i][j] = 0.f;
+        }
+        for (int r0 = c.c0; r0 < c.c1; r0 += kUnit) {
+            __syncthreads();  // k and v have been read
+            if (tid < kUnit) {
+                const int r = r0 + tid;
+                int64_t x = -1;
+                if (r < c.c1) {
+                    const int b = p.table[(int64_t)c.i * p.max_blocks + (r >> p.log2bs)];
+                    if ((unsigned)b < (unsigned)p.num_blocks)
+                        x = (((int64_t)b * p.H + c.h) << p.log2bs) | (r & ((1 << p.log2bs) - 1));
+                    else
+                        set_error(p.status, kDevErrIndex, (unsigned)r);
+                }
+                at_row[tid] = x;
+            }
+            __syncthreads();
+#pragma unroll 4
+            for (int e = tid; e < kUnit * (D / 4); e += kThreads) {
+                const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
+                const int64_t x = at_row[r];
+                const int64_t at = (x < 0 ? 0 : x) * D + d;
+                fetch4(&sm.k[r][d], static_cast<const T*>(p.k) + at, x >= 0);
+                fetch4(&sm.v[r][d], static_cast<const T*>(p.v) + at, x >= 0);
+            }
+            fetched();
+            __syncthreads();
+            float x[8][4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[i][j] = 0.f;
+#pragma unroll 2
+            for (int d = 0; d < D; d += 4) {
+                float4 b[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][d]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 a = *reinterpret_cast<const float4*>(&sm.q[ty * 8 + i][d]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[i][j] = fmaf(a.x, b[j].x, fmaf(a.y, b[j].y, fmaf(a.z, b[j].z, fmaf(a.w, b[j].w, x[i][j]))));
+                }
+            }
+            bool there[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) there[j] = at_row[tx + 16 * j] >= 0;
+            __syncthreads();  // the keys have been read: probabilities take their place
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[i][j] = there[j] ? x[i][j] * sign : -INFINITY;
+                    top = fmaxf(top, x[i][j]);
+                }
+#pragma unroll
+                for (int sh = 1; sh <= 8; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
+                if (top > m[i] + p.slack) {
+                    const float f = m[i] == kNone ? 0.f : ex2((m[i] - top) * p.scale);
+                    m[i] = top;
+                    l[i] *= f;
+#pragma unroll
+                    for (int j = 0; j < NV * 4; ++j) o[i][j] *= f;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float y = ex2((x[i][j] - m[i]) * p.scale);
+                    l[i] += y;
+                    prob[ty * 8 + i][tx + 16 * j] = y;
+                }
+            }
+            __syncwarp();  // a warp reads its own queries' probabilities
+#pragma unroll 2
+            for (int k = 0; k < kUnit; k += 4) {
+                float4 w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const float4*>(&prob[ty * 8 + i][k]);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                    for (int n = 0; n < NV; ++n) {
+                        const float4 y = *reinterpret_cast<const float4*>(&sm.v[k + kk][n * 64 + tx * 4]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float f = kk == 0 ? w[i].x : (kk == 1 ? w[i].y : (kk == 2 ? w[i].z : w[i].w));
+                            o[i][4 * n] = fmaf(f, y.x, o[i][4 * n]);
+                            o[i][4 * n + 1] = fmaf(f, y.y, o[i][4 * n + 1]);
+                            o[i][4 * n + 2] = fmaf(f, y.z, o[i][4 * n + 2]);
+                            o[i][4 * n + 3] = fmaf(f, y.w, o[i][4 * n + 3]);
+                        }
+                    }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int sh = 1; sh <= 8; sh <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], sh);
+            float fix;
+            const float base = base_of(m[i], p.scale, fix);
+            const int r = ty * 8 + i;
+            if (r >= c.rows) continue;
+            if (c.whole) {
+                int s, tk, hd;
+                place_of_row(p, c.seq0, c.h, c.row0 + r, s, tk, hd);
+                const int64_t at = ((int64_t)s * p.T + tk) * p.H * p.G + hd;
+                const Joined j = join_own(base, l[i] * fix, p.own_ml[at]);
+                T* out = static_cast<T*>(p.out) + s * p.o_seq + tk * p.o_tok + hd * p.o_head;
+#pragma unroll
+                for (int n = 0; n < NV; ++n) {
+                    const int d = n * 64 + tx * 4;
+                    const float4 v = make_float4(o[i][4 * n] * fix, o[i][4 * n + 1] * fix,
+                                                 o[i][4 * n + 2] * fix, o[i][4 * n + 3] * fix);
+                    store4(out + d, join4(j, v, *reinterpret_cast<const float4*>(p.own + at * D + d)));
+                }
+                if (tx == 0 && p.lse) p.lse[at] = j.lse;
+            } else {
+#pragma unroll
+                for (int n = 0; n < NV; ++n)
+                    p.partial[((int64_t)c.slot * (D / 4) + n * 16 + tx) * kTile + r] =
+                        make_float4(o[i][4 * n] * fix, o[i][4 * n + 1] * fix, o[i][4 * n + 2] * fix,
+                                    o[i][4 * n + 3] * fix);
+                if (tx == 0) p.partial_ml[(int64_t)c.slot * kTile + r] = make_float2(base, l[i] * fix);
+            }
+        }
+    }
+    if (tid == 0) {
+        p.joins[2 * run] = make_int4(c.seq0, c.rows, c.h, c.row0);
+        p.joins[2 * run + 1] = make_int4((int)c.parts, 0, 0, 0);
+    }
+}
+
+// Joins the pieces of the tile that begins in a run and ends in a later one, and the
+// own rows' sums.  A block takes 32 queries (lanes) and the dimensions 32 at a time; its
+// warps share the pieces.
+constexpr int kJoinWarps = 8;
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const __grid_constant__ Params p) {
+    __shared__ float4 sh_v[kJoinWarps][8][32];
+    __shared__ float sh_m[kJoinWarps][32], sh_l[kJoinWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int run = blockIdx.x, groups = p.tile / 32;
+    const int r = (blockIdx.y % groups) * 32 + lane;
+    wait_for_last();  // the pieces are written
+    const int4 job = p.joins[2 * run];
+    const int parts = p.joins[2 * run + 1].x;
+    if (parts == 0 || r - lane >= job.y) return;
+    int s = 0, tk = 0, hd = 0;
+    if (r < job.y) place_of_row(p, job.x, job.z, job.w + r, s, tk, hd);
+    const int64_t at = ((int64_t)s * p.T + tk) * p.H * p.G + hd;
+    for (int dg = blockIdx.y / groups; dg < D / 32; dg += gridDim.y / groups) {
+        float m = -INFINITY, l = 0.f;
+        float4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = warp; i < parts; i += kJoinWarps) {
+            const int64_t slot = i == 0 ? 2 * run + 1 : 2 * (run + i);
+            const float2 ml = p.partial_ml[slot * p.tile + r];
+            float4 x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = p.partial[(slot * (D / 4) + dg * 8 + k) * p.tile + r];
+            const float mx = fmaxf(m, ml.x);
+            const float f = weight(m, l, mx), g = weight(ml.x, ml.y, mx);
+            m = mx;
+            l = l * f + ml.y * g;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = make_float4(v[k].x * f + x[k].x * g, v[k].y * f + x[k].y * g,
+                                   v[k].z * f + x[k].z * g, v[k].w * f + x[k].w * g);
+        }
+        sh_m[warp][lane] = m;
+        sh_l[warp][lane] = l;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sh_v[warp][k][lane] = v[k];
+        __syncthreads();
+        float mx = sh_m[0][lane], sum = 0.f;
+#pragma unroll
+        for (int w = 1; w < kJoinWarps; ++w) mx = fmaxf(mx, sh_m[w][lane]);
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float f = weight(sh_m[w][lane], sh_l[w][lane], mx);
+            const float4 x = sh_v[w][warp][lane];
+            sum += sh_l[w][lane] * f;
+            y.x += x.x * f; y.y += x.y * f; y.z += x.z * f; y.w += x.w * f;
+        }
+        if (r < job.y) {
+            const int d = (dg * 8 + warp) * 4;
+            const Joined j = join_own(mx, sum, p.own_ml[at]);
+            store4(static_cast<T*>(p.out) + s * p.o_seq + tk * p.o_tok + hd * p.o_head + d,
+                   join4(j, y, *reinterpret_cast<const float4*>(p.own + at * D + d)));
+            if (d == 0 && p.lse) p.lse[at] = j.lse;
+        }
+        __syncthreads();
+    }
+}
+
+Params params(const PrefixArgs& a, const PrefixPlan& pl) {
+    Params p{};
+    const AttnArgs& w = a.own;
+    p.k = w.k;
+    p.v = w.v;
+    p.table = a.table;
+    p.lens = a.lens;
+    p.cu = a.cu;
+    p.P = a.num_prefixes;
+    p.per = a.num_prefixes > 0 ? (int)(w.num_seqs / a.num_prefixes) : 0;
+    p.max_blocks = a.max_blocks;
+    p.log2bs = w.pg.log2bs;
+    p.num_blocks = w.pg.num_blocks;
+    p.max_rows = a.max_rows;
+    p.S = (int)w.num_seqs; p.H = w.pg.H; p.G = w.G; p.T = w.n_new; p.R = w.G * w.n_new;
+    p.q = w.q.data;
+    p.out = w.out.data;
+    p.q_seq = w.q.seq; p.q_tok = w.q.tok; p.q_head = w.q.head;
+    p.o_seq = w.out.seq; p.o_tok = w.out.tok; p.o_head = w.out.head;
+    p.lse = w.lse;
+    p.own = w.raw;
+    p.own_ml = reinterpret_cast<const float2*>(w.raw_ml);
+    const int64_t slots = 2 * (int64_t)pl.runs;
+    p.partial = reinterpret_cast<float4*>(a.partial);
+    p.partial_ml = reinterpret_cast<float2*>(a.partial + slots * pl.tile * w.d);
+    p.joins = reinterpret_cast<int4*>(a.partial + slots * pl.tile * (w.d + 2));
+    p.tile = pl.tile;
+    p.runs = pl.runs;
+    p.lead = pl.lead;
+    // (as for the own rows: a scale of almost nothing still orders the logits)
+    const float x = w.scale * kLog2e, y = x < 0.f ? -x : x;
+    p.scale = y < 1e-30f ? 1e-30f : y;
+    p.slack = 8.f / p.scale;
+    p.flip = x < 0.f ? 0x80008000u : 0u;
+    p.status = w.status;
+    return p;
+}
+
+template <typename T, int D>
+cudaError_t go(const Params& p, cudaStream_t s) {
+    constexpr int bytes = sizeof(Smem<D>);
+    auto kern = prefix_kernel<T, D>;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kern, bytes, done);
+    if (e != cudaSuccess) return e;
+    return launch_early(kern, (unsigned)p.runs, kThreads, bytes, s, p);
+}
+template <typename T, int D>
+cudaError_t go_join(const Params& p, int heads_tiles, cudaStream_t s) {
+    // few tiles: many pieces each, and a block for every 32 dimensions as well
+    const int groups = p.tile / 32, y = groups * (4 * heads_tiles < p.runs ? D / 32 : 1);
+    return launch_early(prefix_join_kernel<T, D>, dim3((unsigned)p.runs, (unsigned)y), kJoinWarps * 32, 0, s, p);
+}
+
+}  // namespace
+}  // namespace prefix
+
+PrefixPlan prefix_plan(const PrefixArgs& a) {
+    using namespace prefix;
+    PrefixPlan pl;
+    const AttnArgs& w = a.own;
+    const int64_t R = (int64_t)w.G * w.n_new;
+    const int sms = tc::sm_count();
+    pl.tile = kTile;
+    pl.unit = kUnit;
+    pl.lead = 1;
+    // every group may leave one tile that is not full
+    pl.tiles = (w.num_seqs * R / pl.tile + a.num_prefixes + 1) * w.pg.H;
+    const int64_t most = ((int64_t)a.max_rows + pl.unit - 1) / pl.unit;
+    const int64_t units = pl.tiles * most;
+    int64_t runs = 2 * sms;
+    if (runs > units) runs = units;
+    pl.runs = (int)runs;
+    pl.raw_floats = (size_t)w.num_seqs * R * w.pg.H * (w.d + 2);
+    pl.partial_floats = (size_t)pl.runs * (2 * pl.tile * (w.d + 2) + 8);
+    return pl;
+}
+
+cudaError_t launch_prefix(const PrefixArgs& a, const PrefixPlan& pl, cudaStream_t s) {
+    const prefix::Params p = prefix::params(a, pl);
+    const bool wide = a.own.d == 128;
+    if (a.own.dtype == RKV_DTYPE_FP32)
+        return wide ? prefix::go<float, 128>(p, s) : prefix::go<float, 64>(p, s);
+    return wide ? prefix::go<__nv_bfloat16, 128>(p, s) : prefix::go<__nv_bfloat16, 64>(p, s);
+}
+
+cudaError_t launch_prefix_join(const PrefixArgs& a, const PrefixPlan& pl, cudaStream_t s) {
+    const prefix::Params p = prefix::params(a, pl);
+    const bool wide = a.own.d == 128;
+    const int tiles = (int)(pl.tiles < (1 << 20) ? pl.tiles : 1 << 20);
+    if (a.own.dtype == RKV_DTYPE_FP32)
+        return wide ? prefix::go_join<float, 128>(p, tiles, s) : prefix::go_join<float, 64>(p, tiles, s);
+    return wide ? prefix::go_join<__nv_bfloat16, 128>(p, tiles, s)
+                : prefix::go_join<__nv_bfloat16, 64>(p, tiles, s);
+}
+
+}  // namespace rkv

@@ -55,13 +55,16 @@ enum KernelId {
     kTokensQ8Append,
     kQ8Read,
     kAttentionQ8,
+    kPrefixAttention,
+    kPrefixJoin,
     kNumKernels
 };
 const char* const kKernelNames[kNumKernels] = {
     "key_stats", "importance", "importance_tc", "gram_tc", "gram_simt", "select", "gather",
     "identity_idx", "compact", "variant", "key_stats_paged", "compact_paged", "paged_release",
     "sentence_penalty", "sentence_reps", "rope", "paged_append", "q4_append", "q4_read",
-    "attention", "attention_q4", "attention_combine", "q8_append", "q8_read", "attention_q8"};
+    "attention", "attention_q4", "attention_combine", "q8_append", "q8_read", "attention_q8",
+    "attention_prefix", "attention_prefix_join"};
 
 // ---------------------------------------------------------------- timing --
 // Events belong to the context they were created in, and a stream records

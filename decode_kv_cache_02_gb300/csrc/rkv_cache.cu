@@ -267,6 +267,57 @@ size_t attention_bytes(const AttnPlan& p) {
     return kAlign + (p.partial_floats * sizeof(float) + kAlign - 1) / kAlign * kAlign;
 }
 
+// The parts of an attention call that do not depend on its workspace: pools, tables and
+// rows.
+int check_attend(const rkv_paged_desc* desc, int n_new, const rkv_rows* q, const void* K_pool,
+                 const void* V_pool, const rkv_q4_cache* four, const rkv_q8_cache* eight,
+                 const int32_t* table, const int32_t* lens, float scale, const rkv_rows* out,
+                 float* lse, int bits, AttnArgs* a) {
+    int rc;
+    if (!table || !lens) return RKV_ERR_INVALID_ARG;
+    const int64_t Hq = (int64_t)desc->num_kv_heads * desc->gqa_group;
+    Span qs, os;
+    if ((rc = check_rows(q, a->dtype, a->d, Hq, desc->num_seqs, n_new, false, &a->q, &qs))) return rc;
+    if ((rc = check_rows(out, a->dtype, a->d, Hq, desc->num_seqs, n_new, true, &a->out, &os)))
+        return rc;
+    if (overlap(qs, os)) return RKV_ERR_ALIAS;
+    if (bits) {
+        Span spans[4];
+        if ((rc = bits == 4 ? check_q4(desc, four, &a->q4p, spans) : check_q8(desc, eight, &a->q8p, spans)))
+            return rc;
+        for (const Span& sp : spans)
+            if (overlap(sp, os)) return RKV_ERR_ALIAS;
+    } else {
+        if (!K_pool || !V_pool || !aligned16(K_pool) || !aligned16(V_pool))
+            return RKV_ERR_INVALID_ARG;
+        const int64_t bytes = pool_rows(desc) * a->d * elem(a->dtype);
+        if (overlap(span_of(K_pool, bytes), os) || overlap(span_of(V_pool, bytes), os))
+            return RKV_ERR_ALIAS;
+        a->k = K_pool;
+        a->v = V_pool;
+    }
+    a->lens = lens;
+    a->scale = scale;
+    a->lse = lse;
+    return RKV_OK;
+}
+
+// Whether the kernels' 32-bit counts hold the units and pool rows of a call.
+bool countable(const rkv_paged_desc* desc, const AttnArgs& a, const AttnPlan& pl) {
+    return a.num_seqs * a.pg.H * ((int64_t)(a.max_rows - 1) / pl.unit + 1 + pl.lead) <
+               ((int64_t)1 << 31) &&
+           pool_rows(desc) < ((int64_t)1 << 32) - 1;
+}
+
+cudaError_t enqueue_attention(const AttnCall& call, cudaStream_t s) {
+    const int bits = call.args.bits;
+    cudaError_t e = rkv::timed_cache(bits == 8 ? rkv::kCacheAttnQ8 : (bits == 4 ? rkv::kCacheAttnQ4 : rkv::kCacheAttn),
+                                     s, run_attention, &call);
+    if (e == cudaSuccess && call.plan.join)
+        e = rkv::timed_cache(rkv::kCacheAttnCombine, s, run_combine, &call);
+    return e;
+}
+
 int attend(const rkv_paged_desc* desc, int n_new, const rkv_rows* q, const void* K_pool,
            const void* V_pool, const rkv_q4_cache* four, const rkv_q8_cache* eight, const int32_t* table,
            const int32_t* lens, int max_rows, float scale, const rkv_rows* out, float* lse,
@@ -277,48 +328,70 @@ int attend(const rkv_paged_desc* desc, int n_new, const rkv_rows* q, const void*
     if (rc) return rc;
     if (!isfinite(scale)) return RKV_ERR_INVALID_ARG;
     call.plan = rkv::attn_plan(a);
-    const AttnPlan& pl = call.plan;
-    // the kernel counts units and pool rows in 32 bits
-    if (a.num_seqs * a.pg.H * ((int64_t)(max_rows - 1) / pl.unit + 1 + pl.lead) >=
-            ((int64_t)1 << 31) ||
-        pool_rows(desc) >= ((int64_t)1 << 32) - 1)
-        return RKV_ERR_UNSUPPORTED;
-    if (!workspace || !aligned_ws(workspace) || workspace_bytes < attention_bytes(pl))
+    if (!countable(desc, a, call.plan)) return RKV_ERR_UNSUPPORTED;
+    if (!workspace || !aligned_ws(workspace) || workspace_bytes < attention_bytes(call.plan))
         return RKV_ERR_WORKSPACE;
     if (desc->num_seqs == 0) return RKV_OK;
-    if (!table || !lens) return RKV_ERR_INVALID_ARG;
-    const int64_t Hq = (int64_t)desc->num_kv_heads * desc->gqa_group;
-    Span qs, os;
-    if ((rc = check_rows(q, a.dtype, a.d, Hq, desc->num_seqs, n_new, false, &a.q, &qs))) return rc;
-    if ((rc = check_rows(out, a.dtype, a.d, Hq, desc->num_seqs, n_new, true, &a.out, &os)))
+    if ((rc = check_attend(desc, n_new, q, K_pool, V_pool, four, eight, table, lens, scale, out, lse, bits, &a)))
         return rc;
-    if (overlap(qs, os)) return RKV_ERR_ALIAS;
-    if (bits) {
-        Span spans[4];
-        if ((rc = bits == 4 ? check_q4(desc, four, &a.q4p, spans) : check_q8(desc, eight, &a.q8p, spans)))
-            return rc;
-        for (const Span& sp : spans)
-            if (overlap(sp, os)) return RKV_ERR_ALIAS;
-    } else {
-        if (!K_pool || !V_pool || !aligned16(K_pool) || !aligned16(V_pool))
-            return RKV_ERR_INVALID_ARG;
-        const int64_t bytes = pool_rows(desc) * a.d * elem(a.dtype);
-        if (overlap(span_of(K_pool, bytes), os) || overlap(span_of(V_pool, bytes), os))
-            return RKV_ERR_ALIAS;
-        a.k = K_pool;
-        a.v = V_pool;
-    }
-    a.lens = lens;
-    a.scale = scale;
-    a.lse = lse;
     a.status = static_cast<DeviceStatus*>(workspace);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = rkv::timed_cache(bits == 8 ? rkv::kCacheAttnQ8 : (bits == 4 ? rkv::kCacheAttnQ4 : rkv::kCacheAttn),
-                                    s, run_attention, &call);
-    if (e == cudaSuccess && pl.join)
-        e = rkv::timed_cache(rkv::kCacheAttnCombine, s, run_combine, &call);
-    return rc_of(e);
+    return rc_of(enqueue_attention(call, static_cast<cudaStream_t>(stream)));
+}
+
+// --------------------------------------------------------------- prefixes --
+
+size_t aligned_floats(size_t n) { return (n * sizeof(float) + kAlign - 1) / kAlign * kAlign; }
+
+struct PrefixCall {
+    rkv::PrefixArgs args;
+    AttnPlan own;
+    rkv::PrefixPlan plan;
+    size_t own_bytes() const { return attention_bytes(own); }
+    size_t bytes() const {
+        return own_bytes() + aligned_floats(plan.raw_floats) + aligned_floats(plan.partial_floats);
+    }
+};
+
+// The sizes of a call over prefixes, its plans, and whether it can be counted.
+int check_prefix(const rkv_paged_desc* desc, const int32_t* table, int n_new, int max_rows,
+                 const rkv_prefixes* p, PrefixCall* c) {
+    rkv::PrefixArgs& a = c->args;
+    const int rc = check_attention(desc, table, n_new, max_rows, 0, &a.own);
+    if (rc) return rc;
+    if (!p || p->num_prefixes < 0) return RKV_ERR_INVALID_ARG;
+    if (p->num_prefixes > 0 &&
+        (p->max_blocks < 1 || p->max_rows < 1 ||
+         (int64_t)p->max_rows > (int64_t)p->max_blocks * desc->block_size))
+        return RKV_ERR_INVALID_ARG;
+    if (p->num_prefixes > 0 && p->max_rows > (1 << 30)) return RKV_ERR_UNSUPPORTED;
+    if (p->num_prefixes > 0 && !p->cu_seqs && desc->num_seqs % p->num_prefixes != 0)
+        return RKV_ERR_INVALID_ARG;
+    a.table = p->table;
+    a.lens = p->lens;
+    a.cu = p->num_prefixes > 0 ? p->cu_seqs : nullptr;
+    a.num_prefixes = p->num_prefixes;
+    a.max_blocks = p->num_prefixes > 0 ? p->max_blocks : 1;
+    a.max_rows = p->num_prefixes > 0 ? p->max_rows : 1;
+    // before the plans: every query in 32 bits
+    if (desc->num_seqs * (int64_t)desc->num_kv_heads * desc->gqa_group * n_new >= ((int64_t)1 << 31) ||
+        p->num_prefixes >= (1 << 24))
+        return RKV_ERR_UNSUPPORTED;
+    c->own = rkv::attn_plan(a.own);
+    c->plan = rkv::prefix_plan(a);
+    const int64_t most = ((int64_t)a.max_rows - 1) / c->plan.unit + 1 + c->plan.lead;
+    if (!countable(desc, a.own, c->own) || c->plan.tiles * most >= ((int64_t)1 << 31))
+        return RKV_ERR_UNSUPPORTED;
+    return RKV_OK;
+}
+
+cudaError_t run_prefix(const void* x, cudaStream_t s) {
+    const PrefixCall& c = *static_cast<const PrefixCall*>(x);
+    return rkv::launch_prefix(c.args, c.plan, s);
+}
+cudaError_t run_prefix_join(const void* x, cudaStream_t s) {
+    const PrefixCall& c = *static_cast<const PrefixCall*>(x);
+    return rkv::launch_prefix_join(c.args, c.plan, s);
 }
 
 // Rows of a packed cache as values: the checks and the launch of both formats.
@@ -577,6 +650,44 @@ int rkv_q8_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
                      size_t workspace_bytes, void* stream) {
     return attend(desc, n_new, q, nullptr, nullptr, nullptr, cache, block_table, lens, max_rows, scale,
                   out, lse, workspace, workspace_bytes, stream, 8);
+}
+
+size_t rkv_prefix_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int max_rows,
+                                           const rkv_prefixes* prefixes) {
+    PrefixCall c;
+    return check_prefix(desc, nullptr, n_new, max_rows, prefixes, &c) ? 0 : c.bytes();
+}
+
+int rkv_prefix_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
+                         const void* K_pool, const void* V_pool, const rkv_prefixes* prefixes,
+                         const int32_t* block_table, const int32_t* lens, int max_rows, float scale,
+                         const rkv_rows* out, float* lse, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+    PrefixCall c;
+    int rc = check_prefix(desc, block_table, n_new, max_rows, prefixes, &c);
+    if (rc) return rc;
+    if (!isfinite(scale)) return RKV_ERR_INVALID_ARG;
+    if (!workspace || !aligned_ws(workspace) || workspace_bytes < c.bytes()) return RKV_ERR_WORKSPACE;
+    if (desc->num_seqs == 0) return RKV_OK;
+    if (prefixes->num_prefixes > 0 && (!prefixes->table || !prefixes->lens)) return RKV_ERR_INVALID_ARG;
+    AttnArgs& a = c.args.own;
+    if ((rc = check_attend(desc, n_new, q, K_pool, V_pool, nullptr, nullptr, block_table, lens, scale, out,
+                           lse, 0, &a)))
+        return rc;
+    char* const ws = static_cast<char*>(workspace);
+    a.status = reinterpret_cast<DeviceStatus*>(ws);
+    a.partial = reinterpret_cast<float*>(ws + kAlign);
+    a.raw = reinterpret_cast<float*>(ws + c.own_bytes());
+    a.raw_ml = a.raw + c.plan.raw_floats / (a.d + 2) * a.d;
+    c.args.partial = reinterpret_cast<float*>(ws + c.own_bytes() + aligned_floats(c.plan.raw_floats));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    AttnCall own;
+    own.args = a;
+    own.plan = c.own;
+    cudaError_t e = enqueue_attention(own, s);
+    if (e == cudaSuccess) e = rkv::timed_cache(rkv::kCachePrefix, s, run_prefix, &c);
+    if (e == cudaSuccess) e = rkv::timed_cache(rkv::kCachePrefixJoin, s, run_prefix_join, &c);
+    return rc_of(e);
 }
 
 }  // extern "C"

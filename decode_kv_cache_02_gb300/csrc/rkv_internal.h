@@ -293,6 +293,10 @@ struct AttnArgs {
     float scale = 1.f;
     float* lse = nullptr;
     float* partial = nullptr;  // attn_plan().partial_floats of scratch
+    // not null: instead of out and lse, the sums that they come from: [S, n_new,
+    // heads][d] relative to 2^maximum, and (maximum, sum) [S, n_new, heads]
+    float* raw = nullptr;
+    float* raw_ml = nullptr;
     DeviceStatus* status = nullptr;
 };
 // How a call is cut: groups of `rows` queries per KV head; the units (`unit`
@@ -308,6 +312,27 @@ AttnPlan attn_plan(const AttnArgs& a);
 cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
 cudaError_t launch_attention_combine(const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
 
+// Attention over shared prefixes: the own rows as an attention call that leaves its
+// sums (own.raw), then the prefixes' rows.
+struct PrefixArgs {
+    AttnArgs own;
+    const int32_t* table = nullptr;  // [num_prefixes, max_blocks]
+    const int32_t* lens = nullptr;
+    const int32_t* cu = nullptr;
+    int num_prefixes = 0, max_blocks = 0, max_rows = 0;
+    float* partial = nullptr;
+};
+// Tiles of `tile` queries, units of `unit` rows, `runs` equal runs of the line; tiles:
+// no call with these sizes has more.
+struct PrefixPlan {
+    int tile = 64, unit = 64, runs = 0, lead = 1;
+    int64_t tiles = 0;
+    size_t raw_floats = 0, partial_floats = 0;
+};
+PrefixPlan prefix_plan(const PrefixArgs& a);
+cudaError_t launch_prefix(const PrefixArgs& a, const PrefixPlan& p, cudaStream_t s);
+cudaError_t launch_prefix_join(const PrefixArgs& a, const PrefixPlan& p, cudaStream_t s);
+
 // Runs `launch` with the library's timing and tracing around it (kernel: an
 // index of rkv_kernel_name).
 enum CacheKernel {
@@ -320,7 +345,9 @@ enum CacheKernel {
     kCacheAttnCombine,
     kCacheQ8Append,
     kCacheQ8Read,
-    kCacheAttnQ8
+    kCacheAttnQ8,
+    kCachePrefix,
+    kCachePrefixJoin
 };
 cudaError_t timed_cache(CacheKernel kernel, cudaStream_t s,
                         cudaError_t (*launch)(const void*, cudaStream_t), const void* arg);

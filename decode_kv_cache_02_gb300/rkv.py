@@ -32,7 +32,8 @@ EXPORTED = [
     "rkv_trace_enable", "rkv_trace_read", "rkv_rope_init", "rkv_rope_init_freqs",
     "rkv_rope_apply", "rkv_paged_append", "rkv_q4_append", "rkv_q4_read",
     "rkv_attention_workspace_size", "rkv_paged_attention", "rkv_q4_attention", "rkv_q8_append",
-    "rkv_q8_read", "rkv_q8_attention",
+    "rkv_q8_read", "rkv_q8_attention", "rkv_prefix_attention_workspace_size",
+    "rkv_prefix_attention",
 ]
 RKV_MAX_POOL_WINDOW = 255
 RKV_ERR_DEVICE = 6
@@ -168,6 +169,12 @@ class _Q8Cache(ctypes.Structure):
                 ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
 
 
+class _Prefixes(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("cu_seqs", ctypes.c_void_p), ("num_prefixes", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("max_rows", ctypes.c_int32)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -274,6 +281,11 @@ def load(path: str | None = None):
         lib.rkv_q8_read.restype = i32
         lib.rkv_q8_attention.argtypes = lib.rkv_q4_attention.argtypes
         lib.rkv_q8_attention.restype = i32
+        lib.rkv_prefix_attention_workspace_size.argtypes = [vp, i32, i32, vp]
+        lib.rkv_prefix_attention_workspace_size.restype = sz
+        lib.rkv_prefix_attention.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, i32, f32, vp, vp, vp,
+                                             sz, vp]
+        lib.rkv_prefix_attention.restype = i32
         lib.rkv_kernel_name.argtypes = [i32]
         lib.rkv_kernel_name.restype = ctypes.c_char_p
         _lib = lib

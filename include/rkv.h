@@ -517,6 +517,46 @@ int rkv_q8_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
                      const int32_t* lens, int max_rows, float scale, const rkv_rows* out,
                      float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Attention of a batch whose sequences share long prefixes (samples of one prompt,
+ * requests over one document): rows of the pools that are held once, named by a
+ * table of their own, and read once for all of their sequences.  rkv_paged_compress
+ * wants a sequence's blocks for itself; a prefix is not compacted, so its blocks
+ * stay as they are while the sequences' own rows, in block_table and lens, are
+ * appended to and compressed as ever.
+ *   table     [num_prefixes, max_blocks] int32 block ids
+ *   lens      [num_prefixes] int32 rows of each prefix, 0 .. max_rows
+ *   cu_seqs   [num_prefixes + 1] int32, ascending from 0: sequences cu_seqs[p] ..
+ *             cu_seqs[p + 1] - 1 share prefix p, those from cu_seqs[num_prefixes]
+ *             on have none.  NULL: every prefix has num_seqs / num_prefixes
+ *             (a whole number) sequences, in order.
+ * All on the device; num_prefixes 0 leaves the own rows. */
+typedef struct {
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* cu_seqs;
+    int32_t num_prefixes;
+    int32_t max_blocks; /* row stride of table (>= 1) */
+    int32_t max_rows;   /* bounds lens (>= 1), at most 2^30 and the table's rows */
+} rkv_prefixes;
+
+/* Bytes for the current device; 0: invalid sizes. */
+size_t rkv_prefix_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int max_rows,
+                                           const rkv_prefixes* prefixes);
+
+/* rkv_paged_attention where token t of sequence s sees all rows of its prefix and
+ * then its own rows j <= lens[s] - n_new + t (max_rows bounds lens; a sequence may
+ * have no rows of its own): one softmax over both; lse likewise.  What is said there
+ * of sums, sizes of logits, hidden rows, bad ids and lengths holds here for both
+ * tables; a cu_seqs that descends or passes the last sequence is recorded and cut.
+ * The probabilities of a prefix's rows meet a bf16 V as one bf16 part (2^-8 of
+ * them).  Prefixes are read by tensor-core kernels where the pools are bf16 with
+ * blocks of 8 rows or more, else on the CUDA cores. */
+int rkv_prefix_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
+                         const void* K_pool, const void* V_pool, const rkv_prefixes* prefixes,
+                         const int32_t* block_table, const int32_t* lens, int max_rows, float scale,
+                         const rkv_rows* out, float* lse, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
 /* The selection alone: for scores Z [P, n] (fp32), out_idx [P, budget] as
  * rkv_compress would produce it (top budget-n_obs of the candidates
  * 0..n-n_obs-1 by Z, ties to the larger index, then the n_obs observation
