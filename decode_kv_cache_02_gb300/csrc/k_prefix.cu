@@ -335,29 +335,39 @@ cudaError_t go_join(const Params& p, int heads_tiles, cudaStream_t s) {
 }  // namespace
 }  // namespace prefix
 
-PrefixPlan prefix_plan(const PrefixArgs& a) {
+PrefixPlan prefix_plan(const PrefixArgs& a, bool tensor) {
     using namespace prefix;
     PrefixPlan pl;
     const AttnArgs& w = a.own;
     const int64_t R = (int64_t)w.G * w.n_new;
     const int sms = tc::sm_count();
-    pl.tile = kTile;
-    pl.unit = kUnit;
+    pl.tensor = tensor;
+    if (tensor) {
+        // two groups of 128 queries a block, or, where a prefix has 128 or fewer (on
+        // average: how they are shared out is the device's), two shares of its rows
+        const int64_t groups = a.num_prefixes > 0 ? a.num_prefixes : 1;
+        pl.tile = w.num_seqs * R <= 128 * groups ? 128 : 256;
+        pl.unit = 128;
+    } else {
+        pl.tile = kTile;
+        pl.unit = kUnit;
+    }
     pl.lead = 1;
     // every group may leave one tile that is not full
     pl.tiles = (w.num_seqs * R / pl.tile + a.num_prefixes + 1) * w.pg.H;
-    const int64_t most = ((int64_t)a.max_rows + pl.unit - 1) / pl.unit;
-    const int64_t units = pl.tiles * most;
-    int64_t runs = 2 * sms;
+    const int64_t units = pl.tiles * (((int64_t)a.max_rows + pl.unit - 1) / pl.unit);
+    int64_t runs = tensor ? sms : 2 * sms;
     if (runs > units) runs = units;
     pl.runs = (int)runs;
     pl.raw_floats = (size_t)w.num_seqs * R * w.pg.H * (w.d + 2);
     pl.partial_floats = (size_t)pl.runs * (2 * pl.tile * (w.d + 2) + 8);
     return pl;
 }
+PrefixPlan prefix_plan(const PrefixArgs& a) { return prefix_plan(a, prefix::tc_takes(a)); }
 
 cudaError_t launch_prefix(const PrefixArgs& a, const PrefixPlan& pl, cudaStream_t s) {
     const prefix::Params p = prefix::params(a, pl);
+    if (pl.tensor) return prefix::launch_tc(p, a.own.d, s);
     const bool wide = a.own.d == 128;
     if (a.own.dtype == RKV_DTYPE_FP32)
         return wide ? prefix::go<float, 128>(p, s) : prefix::go<float, 64>(p, s);

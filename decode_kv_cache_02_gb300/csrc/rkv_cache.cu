@@ -655,7 +655,14 @@ int rkv_q8_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
 size_t rkv_prefix_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int max_rows,
                                            const rkv_prefixes* prefixes) {
     PrefixCall c;
-    return check_prefix(desc, nullptr, n_new, max_rows, prefixes, &c) ? 0 : c.bytes();
+    if (check_prefix(desc, nullptr, n_new, max_rows, prefixes, &c)) return 0;
+    // one size serves every block size
+    size_t n = 0;
+    for (int tensor = 0; tensor < (desc->dtype == RKV_DTYPE_BF16 ? 2 : 1); ++tensor) {
+        c.plan = rkv::prefix_plan(c.args, tensor != 0);
+        if (c.bytes() > n) n = c.bytes();
+    }
+    return n;
 }
 
 int rkv_prefix_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,

@@ -325,11 +325,13 @@ struct PrefixArgs {
 // Tiles of `tile` queries, units of `unit` rows, `runs` equal runs of the line; tiles:
 // no call with these sizes has more.
 struct PrefixPlan {
+    bool tensor = false;  // on the tensor cores
     int tile = 64, unit = 64, runs = 0, lead = 1;
     int64_t tiles = 0;
     size_t raw_floats = 0, partial_floats = 0;
 };
-PrefixPlan prefix_plan(const PrefixArgs& a);
+PrefixPlan prefix_plan(const PrefixArgs& a);  // what a call takes
+PrefixPlan prefix_plan(const PrefixArgs& a, bool tensor);
 cudaError_t launch_prefix(const PrefixArgs& a, const PrefixPlan& p, cudaStream_t s);
 cudaError_t launch_prefix_join(const PrefixArgs& a, const PrefixPlan& p, cudaStream_t s);
 

@@ -253,5 +253,10 @@ RKV_DEV float4 join4(const Joined& j, float4 v, float4 o) {
                        (v.z * j.fp + o.z * j.fo) * j.inv, (v.w * j.fp + o.w * j.fo) * j.inv);
 }
 
+// The pass over the prefixes on the tensor cores (k_prefix_tc.cu), and whether it takes
+// a call's pools.
+bool tc_takes(const PrefixArgs& a);
+cudaError_t launch_tc(const Params& p, int d, cudaStream_t s);
+
 }  // namespace prefix
 }  // namespace rkv
