@@ -1776,6 +1776,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = blockIdx.x % p.groups;
     const int run = blockIdx.x / p.groups;
+    if (p.raw) let_next_begin();  // (the pass over the prefixes waits where it takes these sums)
     wait_for_last();  // the pieces are written
     const int4 job = p.joins[blockIdx.x];
     const int s = job.x, h = job.y, parts = job.z;

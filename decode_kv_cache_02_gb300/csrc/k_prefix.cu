@@ -21,6 +21,7 @@ namespace prefix {
 namespace {
 
 constexpr int kTile = 64, kUnit = 64, kThreads = 128;
+constexpr int kMaxTeam = 8;
 
 RKV_DEV uint32_t smem_at(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -64,7 +65,7 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_kernel(const __grid_consta
 
     Place place = find_place<kUnit>(p, run);
     Piece c{};
-    while (next_piece<kUnit>(p, run, place, c)) {
+    while (next_piece<kUnit>(p, run, 0, place, c)) {
         if (tid == 0 && bad_length(p, c)) set_error(p.status, kDevErrIndex, (unsigned)c.i);
         __syncthreads();  // the piece before has been read
         for (int e = tid; e < kTile * (D / 4); e += kThreads) {
@@ -208,53 +209,78 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_kernel(const __grid_consta
         }
     }
     if (tid == 0) {
-        p.joins[2 * run] = make_int4(c.seq0, c.rows, c.h, c.row0);
-        p.joins[2 * run + 1] = make_int4((int)c.parts, 0, 0, 0);
+        p.joins[run] = make_int4(c.seq0, c.h, c.row0, join_of(c.rows, c.parts));
     }
 }
 
-// Joins the pieces of the tile that begins in a run and ends in a later one, and the
-// own rows' sums.  A block takes 32 queries (lanes) and the dimensions 32 at a time; its
+// Joins the pieces of the tiles that begin in one run and end in a later one, and the
+// own rows' sums.  A block takes 32 queries (lanes) of a tile and 32 dimensions; its
 // warps share the pieces.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 8, kMaxBlocks = 320, kJoinLook = kMaxBlocks / 32;
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 3) prefix_join_kernel(const __grid_constant__ Params p) {
     __shared__ float4 sh_v[kJoinWarps][8][32];
     __shared__ float sh_m[kJoinWarps][32], sh_l[kJoinWarps][32];
+    __shared__ int4 sh_job[kMaxBlocks];  // p.joins of the blocks that left something, and which they are
+    __shared__ short sh_from[kMaxBlocks];
+    __shared__ int sh_jobs;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int run = blockIdx.x, groups = p.tile / 32;
-    const int r = (blockIdx.y % groups) * 32 + lane;
+    const int groups = p.tile / 32, blocks = p.runs * p.team;
+    const int r = (blockIdx.y % groups) * 32 + lane, dg = blockIdx.y / groups, d = (dg * 8 + warp) * 4;
     wait_for_last();  // the pieces are written
-    const int4 job = p.joins[2 * run];
-    const int parts = p.joins[2 * run + 1].x;
-    if (parts == 0 || r - lane >= job.y) return;
-    int s = 0, tk = 0, hd = 0;
-    if (r < job.y) place_of_row(p, job.x, job.z, job.w + r, s, tk, hd);
-    const int64_t at = ((int64_t)s * p.T + tk) * p.H * p.G + hd;
-    for (int dg = blockIdx.y / groups; dg < D / 32; dg += gridDim.y / groups) {
+    if (warp == 0) {
+        int4 job[kJoinLook];
+#pragma unroll
+        for (int k = 0; k < kJoinLook; ++k) {
+            const int i = 32 * k + lane;
+            job[k] = i < blocks ? p.joins[i] : make_int4(0, 0, 0, 0);
+        }
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < kJoinLook; ++k) {
+            const uint32_t set = __ballot_sync(0xffffffffu, job[k].w != 0);
+            const int at = n + __popc(set & ((1u << lane) - 1u));
+            if (job[k].w != 0) {
+                sh_job[at] = job[k];
+                sh_from[at] = (short)(32 * k + lane);
+            }
+            n += __popc(set);
+        }
+        if (lane == 0) sh_jobs = n;
+    }
+    __syncthreads();
+    for (int which = blockIdx.x; which < sh_jobs; which += gridDim.x) {
+        const int4 job = sh_job[which];
+        const int from = sh_from[which], rows = rows_of(job.w), parts = parts_of(job.w);
+        if (r - lane >= rows) continue;  // (for the whole block)
+        int s = 0, tk = 0, hd = 0;
+        if (r < rows) place_of_row(p, job.x, job.y, job.z + r, s, tk, hd);
+        const int64_t at = ((int64_t)s * p.T + tk) * p.H * p.G + hd;
+        const float2 own = p.own_ml[at];
+        const float4 mine = *reinterpret_cast<const float4*>(p.own + at * D + d);
         float m = -INFINITY, l = 0.f;
         float4 v[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < 8; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int i = warp; i < parts; i += kJoinWarps) {
-            const int64_t slot = i == 0 ? 2 * run + 1 : 2 * (run + i);
+            const int64_t slot = i == 0 ? 2 * from + 1 : 2 * (from + (int64_t)i * p.team);
             const float2 ml = p.partial_ml[slot * p.tile + r];
-            float4 x[8];
+            float4 y[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = p.partial[(slot * (D / 4) + dg * 8 + k) * p.tile + r];
+            for (int x = 0; x < 8; ++x) y[x] = p.partial[(slot * (D / 4) + dg * 8 + x) * p.tile + r];
             const float mx = fmaxf(m, ml.x);
             const float f = weight(m, l, mx), g = weight(ml.x, ml.y, mx);
             m = mx;
             l = l * f + ml.y * g;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v[k] = make_float4(v[k].x * f + x[k].x * g, v[k].y * f + x[k].y * g,
-                                   v[k].z * f + x[k].z * g, v[k].w * f + x[k].w * g);
+            for (int x = 0; x < 8; ++x)
+                v[x] = make_float4(v[x].x * f + y[x].x * g, v[x].y * f + y[x].y * g,
+                                   v[x].z * f + y[x].z * g, v[x].w * f + y[x].w * g);
         }
         sh_m[warp][lane] = m;
         sh_l[warp][lane] = l;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sh_v[warp][k][lane] = v[k];
+        for (int x = 0; x < 8; ++x) sh_v[warp][x][lane] = v[x];
         __syncthreads();
         float mx = sh_m[0][lane], sum = 0.f;
 #pragma unroll
@@ -267,11 +293,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const __gr
             sum += sh_l[w][lane] * f;
             y.x += x.x * f; y.y += x.y * f; y.z += x.z * f; y.w += x.w * f;
         }
-        if (r < job.y) {
-            const int d = (dg * 8 + warp) * 4;
-            const Joined j = join_own(mx, sum, p.own_ml[at]);
-            store4(static_cast<T*>(p.out) + s * p.o_seq + tk * p.o_tok + hd * p.o_head + d,
-                   join4(j, y, *reinterpret_cast<const float4*>(p.own + at * D + d)));
+        if (r < rows) {
+            const Joined j = join_own(mx, sum, own);
+            store4(static_cast<T*>(p.out) + s * p.o_seq + tk * p.o_tok + hd * p.o_head + d, join4(j, y, mine));
             if (d == 0 && p.lse) p.lse[at] = j.lse;
         }
         __syncthreads();
@@ -300,13 +324,14 @@ Params params(const PrefixArgs& a, const PrefixPlan& pl) {
     p.lse = w.lse;
     p.own = w.raw;
     p.own_ml = reinterpret_cast<const float2*>(w.raw_ml);
-    const int64_t slots = 2 * (int64_t)pl.runs;
+    const int64_t slots = 2 * (int64_t)pl.runs * pl.team;
     p.partial = reinterpret_cast<float4*>(a.partial);
     p.partial_ml = reinterpret_cast<float2*>(a.partial + slots * pl.tile * w.d);
     p.joins = reinterpret_cast<int4*>(a.partial + slots * pl.tile * (w.d + 2));
     p.tile = pl.tile;
     p.runs = pl.runs;
     p.lead = pl.lead;
+    p.team = pl.team;
     // (as for the own rows: a scale of almost nothing still orders the logits)
     const float x = w.scale * kLog2e, y = x < 0.f ? -x : x;
     p.scale = y < 1e-30f ? 1e-30f : y;
@@ -326,10 +351,13 @@ cudaError_t go(const Params& p, cudaStream_t s) {
     return launch_early(kern, (unsigned)p.runs, kThreads, bytes, s, p);
 }
 template <typename T, int D>
-cudaError_t go_join(const Params& p, int heads_tiles, cudaStream_t s) {
-    // few tiles: many pieces each, and a block for every 32 dimensions as well
-    const int groups = p.tile / 32, y = groups * (4 * heads_tiles < p.runs ? D / 32 : 1);
-    return launch_early(prefix_join_kernel<T, D>, dim3((unsigned)p.runs, (unsigned)y), kJoinWarps * 32, 0, s, p);
+cudaError_t go_join(const Params& p, int64_t tiles, cudaStream_t s) {
+    // a block for every 32 queries and 32 dimensions of a tile, for as many tiles at a time
+    // as six such blocks an SM take
+    const int y = p.tile / 32 * (D / 32);
+    int64_t x = 6 * tc::sm_count() / y;
+    if (x > tiles) x = tiles;
+    return launch_early(prefix_join_kernel<T, D>, dim3((unsigned)(x < 1 ? 1 : x), (unsigned)y), kJoinWarps * 32, 0, s, p);
 }
 
 }  // namespace
@@ -345,22 +373,27 @@ PrefixPlan prefix_plan(const PrefixArgs& a, bool tensor) {
     if (tensor) {
         // two groups of 128 queries a block, or, where a prefix has 128 or fewer (on
         // average: how they are shared out is the device's), two shares of its rows
-        const int64_t groups = a.num_prefixes > 0 ? a.num_prefixes : 1;
-        pl.tile = w.num_seqs * R <= 128 * groups ? 128 : 256;
-        pl.unit = 128;
+        const int64_t groups = a.num_prefixes > 0 ? a.num_prefixes : 1, each = w.num_seqs * R / groups;
+        pl.tile = each <= 128 ? 128 : 256;
+        const int64_t tiles = (each + pl.tile - 1) / pl.tile;
+        pl.team = tiles < 1 ? 1 : (tiles > kMaxTeam ? kMaxTeam : (int)tiles);
+        pl.unit = 64;
     } else {
         pl.tile = kTile;
         pl.unit = kUnit;
     }
-    pl.lead = 1;
+    pl.lead = tensor ? 6 : 1;
     // every group may leave one tile that is not full
-    pl.tiles = (w.num_seqs * R / pl.tile + a.num_prefixes + 1) * w.pg.H;
-    const int64_t units = pl.tiles * (((int64_t)a.max_rows + pl.unit - 1) / pl.unit);
-    int64_t runs = tensor ? sms : 2 * sms;
+    const int64_t sets = (w.num_seqs * R / (pl.tile * pl.team) + a.num_prefixes + 1) * w.pg.H;
+    pl.tiles = sets * pl.team;
+    const int64_t units = sets * (((int64_t)a.max_rows + pl.unit - 1) / pl.unit);
+    int64_t runs = tensor ? sms / pl.team : 2 * sms;
     if (runs > units) runs = units;
+    if (runs * pl.team > kMaxBlocks) runs = kMaxBlocks / pl.team;
+    if (runs < 1) runs = 1;
     pl.runs = (int)runs;
     pl.raw_floats = (size_t)w.num_seqs * R * w.pg.H * (w.d + 2);
-    pl.partial_floats = (size_t)pl.runs * (2 * pl.tile * (w.d + 2) + 8);
+    pl.partial_floats = (size_t)pl.runs * pl.team * (2 * pl.tile * (w.d + 2) + 4);
     return pl;
 }
 PrefixPlan prefix_plan(const PrefixArgs& a) { return prefix_plan(a, prefix::tc_takes(a)); }
@@ -377,11 +410,10 @@ cudaError_t launch_prefix(const PrefixArgs& a, const PrefixPlan& pl, cudaStream_
 cudaError_t launch_prefix_join(const PrefixArgs& a, const PrefixPlan& pl, cudaStream_t s) {
     const prefix::Params p = prefix::params(a, pl);
     const bool wide = a.own.d == 128;
-    const int tiles = (int)(pl.tiles < (1 << 20) ? pl.tiles : 1 << 20);
     if (a.own.dtype == RKV_DTYPE_FP32)
-        return wide ? prefix::go_join<float, 128>(p, tiles, s) : prefix::go_join<float, 64>(p, tiles, s);
-    return wide ? prefix::go_join<__nv_bfloat16, 128>(p, tiles, s)
-                : prefix::go_join<__nv_bfloat16, 64>(p, tiles, s);
+        return wide ? prefix::go_join<float, 128>(p, pl.tiles, s) : prefix::go_join<float, 64>(p, pl.tiles, s);
+    return wide ? prefix::go_join<__nv_bfloat16, 128>(p, pl.tiles, s)
+                : prefix::go_join<__nv_bfloat16, 64>(p, pl.tiles, s);
 }
 
 }  // namespace rkv

@@ -35,18 +35,21 @@ namespace {
 
 using namespace tc;
 
-constexpr int kUnit = 128;
-constexpr int kChunk = kUnit * 128;  // 128 rows of 64 bf16
-constexpr int kThreads = 320;
+constexpr int kUnit = 64;             // rows of a step
+constexpr int kChunk = kUnit * 128;   // 64 rows of 64 bf16
+constexpr int kQChunk = 128 * 128;    // 128 queries of 64 bf16
+constexpr float kFar = 0x1p20f;       // (see the softmax)
+constexpr int kThreads = 352;
 
 template <int D>
 struct Cfg {
     static constexpr int KC = D / 64;
-    static constexpr int TILE = KC * kChunk;  // 128 rows
-    static constexpr int STAGES = D == 128 ? 5 : 8;
-    static constexpr int RING = 2 * TILE;     // behind the queries of both groups
+    static constexpr int TILE = KC * kChunk;    // 64 rows of K or V
+    static constexpr int QTILE = KC * kQChunk;  // the queries of a group
+    static constexpr int STAGES = D == 128 ? 10 : 12;
+    static constexpr int RING = 2 * QTILE;      // behind the queries of both groups
     static constexpr int BARS = RING + STAGES * TILE;
-    static constexpr int NUM_BARS = 2 * STAGES + 8 + 4;
+    static constexpr int NUM_BARS = 2 * STAGES + 2 + 4 + 4 + 4 + 5;
     static constexpr int ML = BARS + NUM_BARS * 8 + 16;
     static constexpr int BYTES = 1024 + ML + 128 * 8;
 };
@@ -104,9 +107,9 @@ RKV_DEV uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-RKV_DEV uint64_t mul2(uint64_t a, uint64_t b) {
+RKV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 RKV_DEV void unpair(uint64_t v, float& a, float& b) {
@@ -116,8 +119,114 @@ RKV_DEV uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&b);
 }
+// One lane of a converged warp.  (The issuing warp stays together around its MMAs, so
+// that what they are given is uniform: an issue by a lane of its own, each operand moved
+// to the uniform registers, takes 100 cycles where the product takes 64.)
+RKV_DEV bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+RKV_DEV void commit_to(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// A bounded wait of a whole warp.  Without a suspend hint: with one a wait costs 200
+// cycles even where the phase is over (17 without), and a step has eight in a row.
+RKV_DEV bool wait_at(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    long long since = 0;
+    for (;;) {
+        uint32_t over;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(over)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (__all_sync(0xffffffffu, over != 0)) return true;
+        const long long now = clock64();
+        if (since == 0) since = now;
+        if (__any_sync(0xffffffffu, *abort_flag != 0 || now - since > kWaitCycles)) return false;
+    }
+}
 RKV_DEV bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+    return wait_at(smem_u32(bar), parity, abort_flag);
+}
+
+// Units whose K goes into the ring before V of unit 0 (S has two buffers a group), and
+// the places of K and V of unit u among a piece's tiles.
+template <bool SPLIT> constexpr int kAhead = SPLIT ? 4 : 2;
+template <bool SPLIT> RKV_DEV uint32_t place_k(int u) { return u + max(0, u + 1 - kAhead<SPLIT>); }
+template <bool SPLIT> RKV_DEV uint32_t place_v(int u, int n) { return u + min(u + kAhead<SPLIT>, n); }
+
+// The products of a group's units of a piece of n, by its issuing warp.  (One for each
+// group: what a warp does between two MMAs, waits that are over take 100 cycles, is time
+// in which the other's fill the tensor cores; one warp for both: 2090 cycles for 64 rows
+// of 2 x 128 queries.)
+struct Issue {
+    uint32_t bars;  // full, empty, .. as in the kernel
+    uint32_t s, o;  // TMEM of the group's S and O
+    uint32_t tile;  // tiles of earlier pieces
+    uint32_t ph;    // phases of p_full and o_done, a bit a buffer
+};
+template <int D, bool SPLIT>
+RKV_DEV bool issue_piece(Issue& w, int x, int n, bool alone, uint64_t q0, uint64_t k0, uint64_t v0,
+                         volatile int* abort_flag) {
+    using C = Cfg<D>;
+    constexpr int STEP = SPLIT ? 2 : 1;
+    constexpr uint32_t kIdescS = idesc_bf16(128, kUnit);
+    constexpr uint32_t kIdescO = idesc_bf16(128, D) | (1u << 16);  // B by rows
+    constexpr uint32_t kEmpty = 8 * C::STAGES, kS = 2 * kEmpty + 16, kP = kS + 32, kO = kP + 32;
+    uint32_t st, ph;
+    const auto find = [&](uint32_t t) {
+        t += w.tile;
+        st = t % C::STAGES;
+        ph = (t / C::STAGES) & 1u;
+        return wait_at(w.bars + 8 * st, ph, abort_flag);
+    };
+    const auto release = [&] {
+        commit_to(w.bars + kEmpty + 8 * st);
+        if (!SPLIT && alone) commit_to(w.bars + kEmpty + 8 * st);  // for the other group as well
+    };
+    const auto logits = [&](uint32_t b) {  // S into buffer b
+        if (elect_one()) {
+            const uint64_t k = k0 + st * (C::TILE >> 4);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                mma_bf16(w.s + b * 64, q0 + (i >> 2) * (kQChunk >> 4) + 2 * (i & 3),
+                         k + (i >> 2) * (kChunk >> 4) + 2 * (i & 3), kIdescS, i != 0);
+            commit_to(w.bars + kS + 16 * x + 8 * b);
+            release();
+        }
+        __syncwarp();
+    };
+    for (int u = SPLIT ? x : 0, q = 0; q < 2 && u < n; u += STEP, ++q) {
+        if (!find(place_k<SPLIT>(u))) return false;
+        logits(q);
+    }
+    for (int u = SPLIT ? x : 0, q = 0; u < n; u += STEP, ++q) {
+        const uint32_t b = q & 1;
+        if (!find(place_v<SPLIT>(u, n))) return false;
+        if (!wait_at(w.bars + kP + 16 * x + 8 * b, (w.ph >> b) & 1u, abort_flag)) return false;
+        tc_fence_after();
+        if (elect_one()) {  // O += P V, P from buffer b
+            const uint64_t v = v0 + st * (C::TILE >> 4);
+#pragma unroll
+            for (int k = 0; k < kUnit / 16; ++k)
+                mma_bf16_ts(w.o, w.s + b * 64 + 8 * k, v + (2048 >> 4) * k, kIdescO, q != 0 || k != 0);
+            commit_to(w.bars + kO + 16 * x + 8 * b);
+            release();
+        }
+        __syncwarp();
+        if (u + 2 * STEP < n) {
+            // the S of two units on takes the place of this P, which the product has to be done with
+            if (!find(place_k<SPLIT>(u + 2 * STEP))) return false;
+            if (!wait_at(w.bars + kO + 16 * x + 8 * b, (w.ph >> b) & 1u, abort_flag)) return false;
+            logits(b);
+        }
+        w.ph ^= 1u << b;
+    }
+    return true;
 }
 
 // Logits of columns from `col` on that no row stands behind become -inf: those past
@@ -148,41 +257,47 @@ __global__ void __launch_bounds__(kThreads, 1)
 prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const __grid_constant__ Params p) {
     using C = Cfg<D>;
-    constexpr int LOOK = SPLIT ? 2 : 1;  // units of S ahead of P V
+    constexpr int STEP = SPLIT ? 2 : 1;  // units between two of a group
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint8_t* ring = smem + C::RING;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BARS);
     uint64_t* empty = full + C::STAGES;
-    uint64_t* q_full = empty + C::STAGES;  // [2]
-    uint64_t* s_full = q_full + 2;         // [2]
-    uint64_t* p_full = s_full + 2;         // [2]
-    uint64_t* o_done = p_full + 2;         // [2]
-    uint64_t* tail_bar = o_done + 2;
-    uint64_t* drain_bar = tail_bar + 1;
-    uint64_t* x_full = drain_bar + 1;  // SPLIT: half of the second group's output is there
+    uint64_t* q_full = empty + C::STAGES;  // [group]
+    uint64_t* s_full = q_full + 2;         // [group][buffer]
+    uint64_t* p_full = s_full + 4;         // [group][buffer]
+    // O += P V done, by the buffer of P: a phase is then never more than one ahead of who
+    // waits for it (the next product from a buffer waits for the group's next P in it)
+    uint64_t* o_done = p_full + 4;         // [group][buffer]
+    uint64_t* tail_bar = o_done + 4;
+    uint64_t* drain_bar = tail_bar + 1;  // [group]
+    uint64_t* x_full = drain_bar + 2;  // SPLIT: half of the second group's output is there
     uint64_t* x_empty = x_full + 1;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(x_empty + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     float2* sh_ml = reinterpret_cast<float2*>(smem + C::ML);
-    float* sh_x = reinterpret_cast<float*>(smem + C::TILE);  // [D / 2][128] (the second group's queries are the first's)
+    float* sh_x = reinterpret_cast<float*>(smem + C::QTILE);  // [D / 2][128] (the second group's queries are the first's)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t run = blockIdx.x;
+    const uint32_t run = blockIdx.x / p.team;
+    const int member = blockIdx.x - run * p.team;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], SPLIT ? 1 : 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 4);
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
         mbar_init(tail_bar, 1);
-        mbar_init(drain_bar, 1);
+        mbar_init(&drain_bar[0], 1);
+        mbar_init(&drain_bar[1], 1);
         mbar_init(x_full, 4);
         mbar_init(x_empty, 4);
         *s_abort = 0;
@@ -198,42 +313,44 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    wait_for_last();
+    // (Begins while the own rows' pass ends: that pass began behind everything before it, so
+    // queries, pools and tables are there; its sums are waited for where they are read.)
     Place place = find_place<kUnit>(p, run);
     Piece c{};
     bool ok = true;
 
-    if (warp == 9) {
+    if (warp == 10) {
         // ------------------------------------------------------- producer --
-        const int log2box = p.log2bs < 7 ? p.log2bs : 7, box = 1 << log2box;
-        const int copies = (kUnit >> log2box) * C::KC;  // of a tile, at most 32
-        uint32_t kt = 0, tails = 0;
-        auto load = [&](const CUtensorMap* map, int u, bool is_v) {
-            const int st = kt % C::STAGES, r0 = c.c0 + u * kUnit;
-            const int b = lane / C::KC, ch = lane - b * C::KC, r = r0 + (b << log2box);
-            // an outer coordinate past the pool reads as zeros
-            int z = p.num_blocks * p.H;
-            if (lane < copies && r < c.c1) {
-                const int blk = p.table[(int64_t)c.i * p.max_blocks + (r >> p.log2bs)];
-                if ((unsigned)blk < (unsigned)p.num_blocks)
-                    z = blk * p.H + c.h;
-                else if (!is_v && ch == 0)
-                    set_error(p.status, kDevErrIndex, (unsigned)r);
-            }
-            if (!wait_all(&empty[st], ((kt / C::STAGES) & 1) ^ 1, s_abort)) return false;
+        // lane i copies 64 columns of a block (of up to 64 rows)
+        const int log2box = p.log2bs < 6 ? p.log2bs : 6, box = 1 << log2box;
+        const int b = lane / C::KC, ch = lane - b * C::KC, own = b << log2box;
+        const bool copies = lane < (kUnit >> log2box) * C::KC;  // 16 at most
+        const uint32_t to = ch * kChunk + own * 128;
+        uint32_t st = 0, ph = 1, tiles = 0, tails = 0;
+        // the block of the lane's rows of unit u, asked for one tile ahead (-1: rows past the piece)
+        auto look_up = [&](int u) {
+            const int r = c.c0 + u * kUnit + own;
+            return copies && r < c.c1 ? p.table[(int64_t)c.i * p.max_blocks + (r >> p.log2bs)] : -1;
+        };
+        auto load = [&](const CUtensorMap* map, int u, int block, bool is_v) {
+            const int r0 = c.c0 + u * kUnit;
+            const bool there = (unsigned)block < (unsigned)p.num_blocks;
+            if (copies && !there && !is_v && ch == 0 && r0 + own < c.c1)
+                set_error(p.status, kDevErrIndex, (unsigned)(r0 + own));
+            if (!wait_all(&empty[st], ph, s_abort)) return false;
             uint8_t* dst = ring + st * C::TILE;
             const bool clear = is_v && r0 + kUnit > c.c1 && (c.c1 & (box - 1)) != 0;
             uint64_t* bar = clear ? tail_bar : &full[st];
+            // (bytes that land before they are expected leave the count below zero for a while)
             if (lane == 0) mbar_arrive_expect_tx(bar, C::TILE);
-            __syncwarp();
-            if (lane < copies)
-                tma_load_3d(dst + ch * kChunk + (b << log2box) * 128, map, bar, ch * 64,
-                            r & ((1 << p.log2bs) - 1), z);
-            ++kt;
+            // an outer coordinate past the pool reads as zeros
+            if (copies)
+                tma_load_3d(dst + to, map, bar, ch * 64, (r0 + own) & ((1 << p.log2bs) - 1),
+                            there ? block * p.H + c.h : p.num_blocks * p.H);
             if (clear) {
                 if (!wait_all(tail_bar, tails++ & 1, s_abort)) return false;
-                const int from = c.c1 - r0, to = (from + box) & ~(box - 1);
-                for (int e = lane; e < (to - from) * 8 * C::KC; e += 32) {
+                const int from = c.c1 - r0, end = (from + box) & ~(box - 1);
+                for (int e = lane; e < (end - from) * 8 * C::KC; e += 32) {
                     const int row = from + e / (8 * C::KC), x = e % (8 * C::KC);
                     *reinterpret_cast<uint4*>(dst + (x >> 3) * kChunk + row * 128 + (x & 7) * 16) =
                         make_uint4(0u, 0u, 0u, 0u);
@@ -242,14 +359,30 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[st]);
             }
+            ++tiles;
+            if (++st == C::STAGES) {
+                st = 0;
+                ph ^= 1u;
+            }
             return true;
         };
-        while (ok && next_piece<kUnit>(p, run, place, c)) {
-            const int n = units_in(c);
-            for (int u = 0; ok && u < LOOK && u < n; ++u) ok = load(&kmap, u, false);
+        while (ok && next_piece<kUnit>(p, run, member, place, c)) {
+            const int n = c.rows > 0 ? units_in(c) : 0;
+            int k = 0, next_k = look_up(0), next_v = next_k;
+            for (; ok && k < kAhead<SPLIT> && k < n; ++k) {
+                const int block = next_k;
+                next_k = look_up(k + 1);
+                ok = load(&kmap, k, block, false);
+            }
             for (int u = 0; ok && u < n; ++u) {
-                ok = load(&vmap, u, true);
-                if (ok && u + LOOK < n) ok = load(&kmap, u + LOOK, false);
+                int block = next_v;
+                next_v = look_up(u + 1);
+                ok = load(&vmap, u, block, true);
+                if (ok && k < n) {
+                    block = next_k;
+                    next_k = look_up(k + 1);
+                    ok = load(&kmap, k++, block, false);
+                }
             }
         }
         if (!ok) {
@@ -258,146 +391,125 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         }
         // every copy issued has landed before the block may end
         volatile int never = 0;
-        for (uint32_t u = kt > (uint32_t)C::STAGES ? kt - C::STAGES : 0; u < kt; ++u)
+        for (uint32_t u = tiles > (uint32_t)C::STAGES ? tiles - C::STAGES : 0; u < tiles; ++u)
             mbar_wait(&full[u % C::STAGES], (u / C::STAGES) & 1, &never);
-    } else if (warp == 8) {
-        // ----------------------------------------------------- MMA issuer --
-        constexpr uint32_t kIdescS = idesc_bf16(128, kUnit);
-        constexpr uint32_t kIdescO = idesc_bf16(128, D) | (1u << 16);  // B by rows
-        if (lane == 0) {
-            uint32_t kt = 0, pieces = 0, done[2] = {0, 0}, filled[2] = {0, 0}, second = 0;
-            auto logits = [&](int x, const uint8_t* tile) {
-                const uint8_t* q = smem + (SPLIT ? 0 : x * C::TILE);
-#pragma unroll
-                for (int ch = 0; ch < C::KC; ++ch) {
-                    const uint64_t a = sdesc_sw128(q + ch * kChunk), b = sdesc_sw128(tile + ch * kChunk);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_bf16(tmem + x * 128, a + 2 * k, b + 2 * k, kIdescS, (ch | k) != 0);
-                }
-                mma_commit(&s_full[x]);
-            };
-            auto values = [&](int x, const uint8_t* tile, bool begin) {
-                const uint64_t b = sdesc_rows(tile, kChunk);
-#pragma unroll
-                for (int k = 0; k < kUnit / 16; ++k)
-                    mma_bf16_ts(tmem + 256 + x * D, tmem + x * 128 + 8 * k, b + (2048 >> 4) * k, kIdescO,
-                                !begin || k != 0);
-                mma_commit(&o_done[x]);
-                ++done[x];
-            };
-            while (ok && next_piece<kUnit>(p, run, place, c)) {
-                const int n = units_in(c);
-                if (n == 0) continue;
-                const bool two = !SPLIT && c.rows > 128;
-                if (!(ok = mbar_wait(&q_full[0], pieces++ & 1, s_abort))) break;
-                if (two && !(ok = mbar_wait(&q_full[1], second++ & 1, s_abort))) break;
+    } else if (warp >= 8) {
+        // ---------------------------------------------------- MMA issuers --
+        const int x = warp - 8;
+        uint32_t asked = 0;
+        Issue w{smem_u32(full), tmem + x * 128, tmem + 256 + x * D, 0u, 0u};
+        const uint64_t q0 = sdesc_sw128(smem + (SPLIT ? 0 : x * C::QTILE)), k0 = sdesc_sw128(ring),
+                       v0 = sdesc_rows(ring, kChunk);
+        while (ok && next_piece<kUnit>(p, run, member, place, c)) {
+            const int n = c.rows > 0 ? units_in(c) : 0;
+            if (n > (SPLIT ? x : 0) && (SPLIT || c.rows > 128 * x)) {
+                if (!(ok = wait_all(&q_full[x], asked++ & 1, s_abort))) break;
                 tc_fence_after();
-                for (int u = 0; ok && u < LOOK && u < n; ++u, ++kt) {
-                    const int st = kt % C::STAGES;
-                    if (!(ok = mbar_wait(&full[st], (kt / C::STAGES) & 1, s_abort))) break;
-                    logits(SPLIT ? u : 0, ring + st * C::TILE);
-                    if (two) logits(1, ring + st * C::TILE);
-                    mma_commit(&empty[st]);
-                }
-                for (int u = 0; ok && u < n; ++u) {
-                    const int sv = kt % C::STAGES, sk = (kt + 1) % C::STAGES;
-                    const bool more = u + LOOK < n;
-                    if (!(ok = mbar_wait(&full[sv], (kt / C::STAGES) & 1, s_abort))) break;
-                    for (int i = 0; i < (two ? 2 : 1); ++i) {
-                        const int x = SPLIT ? u & 1 : i;
-                        if (!(ok = mbar_wait(&p_full[x], filled[x]++ & 1, s_abort))) break;
-                        tc_fence_after();
-                        values(x, ring + sv * C::TILE, SPLIT ? u < 2 : u == 0);
-                        if (i == (two ? 1 : 0)) mma_commit(&empty[sv]);
-                        if (!more) continue;
-                        if (i == 0 &&
-                            !(ok = mbar_wait(&full[sk], ((kt + 1) / C::STAGES) & 1, s_abort)))
-                            break;
-                        // S takes the place of P, which the product has to be done with
-                        if (!(ok = mbar_wait(&o_done[x], (done[x] - 1) & 1, s_abort))) break;
-                        logits(x, ring + sk * C::TILE);
-                        if (i == (two ? 1 : 0)) mma_commit(&empty[sk]);
-                    }
-                    kt += more ? 2 : 1;
-                }
+                ok = issue_piece<D, SPLIT>(w, x, n, c.rows <= 128, q0, k0, v0, s_abort);
             }
-            if (!ok) {
-                *s_abort = 1;
-                set_error(p.status, kDevErrTimeout, 2u);
-            }
-            // every MMA issued so far is done before TMEM is released
-            mma_commit(drain_bar);
-            volatile int never = 0;
-            mbar_wait(drain_bar, 0, &never);
+            w.tile += 2 * n;
         }
+        if (!ok) {
+            *s_abort = 1;
+            if (lane == 0) set_error(p.status, kDevErrTimeout, 2u);
+        }
+        // every MMA issued so far is done before TMEM is released
+        if (elect_one()) mma_commit(&drain_bar[x]);
+        __syncwarp();
+        volatile int never = 0;
+        mbar_wait(&drain_bar[x], 0, &never);
     } else {
         // -------------------------------------------------------- softmax --
         const int x = warp >> 2, row = (warp & 3) * 32 + lane;
-        const uint32_t t_s = tmem + ((uint32_t)(warp & 3) << 21) + x * 128;
+        const uint32_t t_x = tmem + ((uint32_t)(warp & 3) << 21) + x * 128;
         const uint32_t t_o = tmem + ((uint32_t)(warp & 3) << 21) + 256 + x * D;
-        const int log2box = p.log2bs < 7 ? p.log2bs : 7, boxes = kUnit >> log2box;
-        uint32_t seen = 0, done = 0, halves = 0;  // phases of s_full, o_done, x_full
-        while (ok && next_piece<kUnit>(p, run, place, c)) {
-            if (!SPLIT && x == 1 && c.rows <= 128) continue;
-            if (threadIdx.x == 0 && bad_length(p, c)) set_error(p.status, kDevErrIndex, (unsigned)c.i);
+        const int log2box = p.log2bs < 6 ? p.log2bs : 6, boxes = kUnit >> log2box;
+        bool waited = false;
+        uint32_t seen = 0, halves = 0;  // phases of s_full and o_done (a bit a buffer), x_full
+        while (ok && next_piece<kUnit>(p, run, member, place, c)) {
+            if (!SPLIT && c.rows <= 128 * x) continue;
             const int n = units_in(c);
             const int r = (SPLIT ? 0 : x * 128) + row;
             const bool valid = r < c.rows;
             int s = 0, tk = 0, hd = 0;
             if (valid) place_of_row(p, c.seq0, c.h, c.row0 + r, s, tk, hd);
             if (n > 0 && (!SPLIT || x == 0)) {
-                const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                                s * p.q_seq + tk * p.q_tok + hd * p.q_head);
-                uint8_t* dst = smem + x * C::TILE + row * 128;
+                // a row of queries by D / 8 neighbouring lanes, all rows of the warp on their way
+                // before the first is stored
+                constexpr int LANES = D / 8;
+                const int u = lane % LANES;
+                const int64_t mine = valid ? s * p.q_seq + tk * p.q_tok + hd * p.q_head : -1;
+                uint4 y[LANES];
 #pragma unroll
-                for (int u = 0; u < D / 8; ++u) {
-                    uint4 y = make_uint4(0u, 0u, 0u, 0u);
-                    if (valid) y = q[u];
-                    y.x ^= p.flip; y.y ^= p.flip; y.z ^= p.flip; y.w ^= p.flip;
-                    *reinterpret_cast<uint4*>(dst + (u >> 3) * kChunk + (((u & 7) ^ (row & 7)) << 4)) = y;
+                for (int i = 0; i < LANES; ++i) {
+                    const int64_t at = __shfl_sync(0xffffffffu, mine, i * (32 / LANES) + lane / LANES);
+                    y[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (at >= 0)
+                        y[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at + 8 * u);
+                }
+#pragma unroll
+                for (int i = 0; i < LANES; ++i) {
+                    const int to = (warp & 3) * 32 + i * (32 / LANES) + lane / LANES;
+                    y[i].x ^= p.flip; y[i].y ^= p.flip; y[i].z ^= p.flip; y[i].w ^= p.flip;
+                    *reinterpret_cast<uint4*>(smem + x * C::QTILE + (u >> 3) * kQChunk + to * 128 +
+                                              (((u & 7) ^ (to & 7)) << 4)) = y[i];
                 }
                 fence_async();
                 mbar_arrive_warp(&q_full[x]);
+                if (SPLIT && n > 1) mbar_arrive_warp(&q_full[1]);
             }
-            // m: running maximum of q . k; sums are relative to 2^(m * scale)
-            float m = kNone, l = 0.f;
+            if (threadIdx.x == 0 && bad_length(p, c)) set_error(p.status, kDevErrIndex, (unsigned)c.i);
+            // m: running maximum of q . k; sums are relative to 2^base, base the fp32 nearest
+            // to m * scale and rest what that leaves, so that z * scale - base is one FMA and
+            // exact up to its rounding.  Past kFar, where base is coarse, they are relative to
+            // 2^(m * scale) (rest 0), and differences of q . k are taken; far: some query of
+            // the warp is there.
+            float m = kNone, l = 0.f, base = -INFINITY, rest = 0.f;
+            bool far = true;
             bool begin = true;
-            for (int u = SPLIT ? x : 0; u < n; u += LOOK) {
+            int buf = 1;
+            // the block of this lane's rows of a unit, looked at one unit later, when the load has
+            // come back (0, which there is, for lanes without rows)
+            const auto look_up = [&](int u) {
+                const int rb = c.c0 + u * kUnit + (lane << log2box);
+                return lane < boxes && rb < c.c1 ? p.table[(int64_t)c.i * p.max_blocks + (rb >> p.log2bs)] : 0;
+            };
+            int block = look_up(SPLIT ? x : 0);
+            for (int u = SPLIT ? x : 0; u < n; u += STEP) {
+                buf ^= 1;
+                const uint32_t t_s = t_x + buf * 64;
                 const int r0 = c.c0 + u * kUnit, left = c.c1 - r0;
-                bool there = true;
-                if (lane < boxes && (lane << log2box) < left) {
-                    const int rb = r0 + (lane << log2box);
-                    const int blk = p.table[(int64_t)c.i * p.max_blocks + (rb >> p.log2bs)];
-                    there = (unsigned)blk < (unsigned)p.num_blocks;
-                }
-                const uint32_t have = __ballot_sync(0xffffffffu, there);
-                if (!(ok = wait_all(&s_full[x], seen++ & 1, s_abort))) break;
+                const uint32_t have = __ballot_sync(0xffffffffu, (unsigned)block < (unsigned)p.num_blocks);
+                block = look_up(u + STEP);
+                if (!(ok = wait_all(&s_full[2 * x + buf], (seen >> buf) & 1, s_abort))) break;
+                seen ^= 1u << buf;
                 tc_fence_after();
-                // the row's maximum; the values come again below, 32 at a time (all at once
-                // they would take more registers than there are)
-                const bool masked = left < kUnit || have != 0xffffffffu;
-                float mx = -INFINITY;
+                uint32_t z[2][32];
+                float top[2];
 #pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    uint32_t z0[32], z1[32];
-                    float t0, t1;
-                    tmem_ld_32cols_max(t_s + 32 * i, z0, t0);
-                    tmem_ld_32cols_max(t_s + 32 * i + 32, z1, t1);
-                    tmem_ld_wait();
-                    if (masked) {
-                        t0 = hide(z0, 32 * i, left, have, log2box);
-                        t1 = hide(z1, 32 * i + 32, left, have, log2box);
-                    }
-                    mx = fmaxf(mx, fmaxf(t0, t1));
+                for (int i = 0; i < 2; ++i) tmem_ld_32cols_max(t_s + 32 * i, z[i], top[i]);
+                tmem_ld_wait();
+                if (left < kUnit || have != 0xffffffffu) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) top[i] = hide(z[i], 32 * i, left, have, log2box);
                 }
+                const float mx = fmaxf(top[0], top[1]);
                 const bool grow = mx > m + p.slack;
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float f = grow ? (m == kNone ? 0.f : ex2((m - mx) * p.scale)) : 1.f;
-                    if (grow) m = mx;
+                    float f = 1.f;
+                    if (grow) {
+                        // from the old reference to the new one
+                        const float z = __fmul_rn(mx, p.scale);
+                        const float r = fabsf(z) < kFar ? fmaf(mx, p.scale, -z) : 0.f;
+                        f = m == kNone ? 0.f : ex2(fmaf(m - mx, p.scale, r - rest));
+                        m = mx;
+                        base = z;
+                        rest = r;
+                    }
+                    far = __any_sync(0xffffffffu, !(fabsf(base) < kFar));
                     l *= f;
                     if (!begin) {
-                        if (!(ok = wait_all(&o_done[x], (done - 1) & 1, s_abort))) break;
+                        if (!(ok = wait_all(&o_done[2 * x + (buf ^ 1)], ((seen >> (buf ^ 1)) & 1) ^ 1, s_abort))) break;
                         tc_fence_after();
 #pragma unroll 1
                         for (int i = 0; i < D / 32; ++i) {
@@ -411,23 +523,33 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                     }
                 }
                 begin = false;
-                const uint64_t less = pair(-m, -m), by = pair(p.scale, p.scale);
                 uint64_t sum[2] = {0ull, 0ull};
-                uint32_t z[2][32];
-                tmem_ld_32cols(t_s, z[0]);
+                const uint64_t by = pair(p.scale, p.scale);
+                if (far) {
+                    // (logits past kFar: differences of q . k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    tmem_ld_wait();
-                    if (i < 3) tmem_ld_32cols(t_s + 32 * i + 32, z[(i + 1) & 1]);
-                    uint32_t (&at)[32] = z[i & 1];
-                    if (masked) hide(at, 32 * i, left, have, log2box);
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            z[i][k] = __float_as_uint(fmaf(__uint_as_float(z[i][k]) - m, p.scale, rest));
+                } else {
+                    const uint64_t less = pair(-base, -base);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            float a, b;
+                            unpair(fma2(pair(__uint_as_float(z[i][k]), __uint_as_float(z[i][k + 1])), by, less), a, b);
+                            z[i][k] = __float_as_uint(a);
+                            z[i][k + 1] = __float_as_uint(b);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
                     uint32_t y[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        float a, b;
-                        unpair(mul2(add2(pair(__uint_as_float(at[2 * k]), __uint_as_float(at[2 * k + 1])), less), by), a, b);
-                        a = ex2(a);
-                        b = ex2(b);
+                        const float a = ex2(__uint_as_float(z[i][2 * k])), b = ex2(__uint_as_float(z[i][2 * k + 1]));
                         sum[k & 1] = add2(sum[k & 1], pair(a, b));
                         y[k] = pack_bf16(a, b);
                     }
@@ -438,15 +560,15 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                 l += a + b;
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive_warp(&p_full[x]);
-                ++done;
+                mbar_arrive_warp(&p_full[2 * x + buf]);
             }
             if (!ok) break;
-            float fix;
-            float base = base_of(m, p.scale, fix);
+            float fix = 1.f;
+            if (!(fabsf(base) < kFar)) base = base_of(m, p.scale, fix);
             l *= fix;
             if (!begin) {
-                if (!(ok = wait_all(&o_done[x], (done - 1) & 1, s_abort))) break;
+                if (!(ok = wait_all(&o_done[2 * x], (seen & 1) ^ 1, s_abort))) break;
+                if (!(ok = wait_all(&o_done[2 * x + 1], ((seen >> 1) & 1) ^ 1, s_abort))) break;
                 tc_fence_after();
             }
             // SPLIT: the second group's sums join the first's, half of the dimensions at a time
@@ -481,6 +603,10 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                 base = mx;
             } else if (SPLIT && x == 1) {
                 continue;
+            }
+            if (!waited) {
+                wait_for_last();
+                waited = true;
             }
             Joined j{};
             const int64_t at = ((int64_t)s * p.T + tk) * p.H * p.G + hd;
@@ -538,9 +664,9 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             *s_abort = 1;
             if (lane == 0) set_error(p.status, kDevErrTimeout, 3u);
         }
+        if (!waited) wait_for_last();
         if (threadIdx.x == 0) {
-            p.joins[2 * run] = make_int4(c.seq0, c.rows, c.h, c.row0);
-            p.joins[2 * run + 1] = make_int4(ok ? (int)c.parts : 0, 0, 0, 0);
+            p.joins[blockIdx.x] = make_int4(c.seq0, c.h, c.row0, ok && c.rows > 0 ? join_of(c.rows, c.parts) : 0);
         }
     }
 
@@ -562,7 +688,7 @@ cudaError_t go(const Params& p, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
     cudaError_t e = allow_smem(kern, Cfg<D>::BYTES, done);
     if (e != cudaSuccess) return e;
-    return launch_early(kern, (unsigned)p.runs, kThreads, Cfg<D>::BYTES, s, k, v, p);
+    return launch_early(kern, (unsigned)(p.runs * p.team), kThreads, Cfg<D>::BYTES, s, k, v, p);
 }
 
 }  // namespace

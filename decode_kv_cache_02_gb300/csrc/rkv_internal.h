@@ -327,6 +327,7 @@ struct PrefixArgs {
 struct PrefixPlan {
     bool tensor = false;  // on the tensor cores
     int tile = 64, unit = 64, runs = 0, lead = 1;
+    int team = 1;  // blocks that take neighbouring tiles over the same rows
     int64_t tiles = 0;
     size_t raw_floats = 0, partial_floats = 0;
 };

@@ -5,7 +5,9 @@
 // tiles; a tile goes over the prefix in units of rows.  All tiles of all prefixes and
 // heads lie one after another on a line of units that is cut into equal runs, one a
 // block, so ragged prefixes and groups are balanced whatever their sizes; a tile cut
-// by a run's end is joined by a second launch.
+// by a run's end is joined by a second launch.  With more queries a prefix than a tile
+// holds, blocks go in teams that take neighbouring tiles over the same rows at the same
+// time, so that those come from HBM once: the line's tiles are then a team's.
 #pragma once
 
 #include <float.h>
@@ -37,8 +39,8 @@ struct Params {
     const float2* own_ml;
     float4* partial;       // [slot][D / 4][tile]
     float2* partial_ml;    // [slot][tile]
-    int4* joins;           // [run][2]: (first sequence, sequences, head, tile) and parts
-    int tile, runs, lead;
+    int4* joins;           // [block]: first sequence, head and first row of a tile, join_of()
+    int tile, runs, lead, team;
     float scale, slack;    // of base-2 logits, positive; how far they may pass the maximum
     uint32_t flip;         // scale < 0: the queries change their signs
     DeviceStatus* status;
@@ -79,21 +81,22 @@ RKV_DEV int len_of(const Params& p, int i) {
     const int n = p.lens[i];
     return n < 0 ? 0 : (n > p.max_rows ? p.max_rows : n);
 }
-// Units of a tile; an empty prefix has one too (its queries' outputs are written by
+// Units of a (team's) tile; an empty prefix has one too (its queries' outputs are written by
 // it).  On the line a tile is p.lead places longer: what its beginning and end cost.
 template <int UNIT>
 RKV_DEV uint32_t units_of(int rows) {
     return rows <= UNIT ? 1u : (uint32_t)(rows - 1) / UNIT + 1u;
 }
 RKV_DEV uint32_t tiles_of(const Params& p, int seqs) {
-    return ((uint32_t)seqs * (uint32_t)p.R + (uint32_t)p.tile - 1u) / (uint32_t)p.tile;
+    const uint32_t rows = (uint32_t)(p.tile * p.team);
+    return ((uint32_t)seqs * (uint32_t)p.R + rows - 1u) / rows;
 }
 
 struct Place {
     uint32_t n, runs;  // units and runs in use
     uint32_t u0, u1;   // the run (empty: none for this block)
     uint32_t start;    // first unit of the current tile
-    int i, seq0, seqs, h, tile;  // group, its sequences; head, tile
+    int i, seq0, seqs, len, h, tile;  // group, its sequences and rows; head, tile
 };
 RKV_DEV uint32_t first_of(const Place& pl, uint32_t i) {
     const uint32_t per = pl.n / pl.runs, more = pl.n - per * pl.runs;
@@ -104,14 +107,16 @@ RKV_DEV uint32_t run_of(const Place& pl, uint32_t u) {
     const uint32_t big = more * (per + 1);
     return u < big ? u / (per + 1) : more + (u - big) / per;
 }
-// By a whole warp, every lane with its stretch of groups.
+// By a whole warp, every lane with its stretch of groups (the first of which it looks up
+// once: most calls have no more than 32).
 template <int UNIT>
 RKV_DEV Place find_place(const Params& p, uint32_t run) {
     const int lane = threadIdx.x & 31;
     const int groups = p.P + 1, each = (groups + 31) / 32;
     const int a = min(lane * each, groups), b = min(a + each, groups);
-    int top = 0;  // the largest end so far
-    for (int i = a; i < b; ++i) top = max(top, end_of(p, i));
+    const int end0 = a < b ? end_of(p, a) : 0, len0 = a < b ? len_of(p, a) : 0;
+    int top = end0;  // the largest end so far
+    for (int i = a + 1; i < b; ++i) top = max(top, end_of(p, i));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, top, o);
@@ -122,8 +127,9 @@ RKV_DEV Place find_place(const Params& p, uint32_t run) {
     uint32_t sum = 0;
     bool wrong = false;
     for (int i = a, at = from; i < b; ++i) {
-        const int e = max(at, end_of(p, i));
-        sum += tiles_of(p, e - at) * (uint32_t)p.H * (units_of<UNIT>(len_of(p, i)) + p.lead);
+        const int e = max(at, i == a ? end0 : end_of(p, i));
+        sum += tiles_of(p, e - at) * (uint32_t)p.H *
+               (units_of<UNIT>(i == a ? len0 : len_of(p, i)) + p.lead);
         if (run == 0 && p.cu && i < p.P) wrong |= p.cu[i + 1] != e || (i == 0 && p.cu[0] != 0);
         at = e;
     }
@@ -146,13 +152,14 @@ RKV_DEV Place find_place(const Params& p, uint32_t run) {
     pl.i = a;
     pl.seq0 = from;
     pl.seqs = 0;
+    pl.len = 0;
     const bool mine = first <= pl.u0 && pl.u0 < upto;
     if (mine) {
         for (;; ++pl.i) {
-            const int e = max(pl.seq0, end_of(p, pl.i));
+            const int e = max(pl.seq0, pl.i == a ? end0 : end_of(p, pl.i));
+            pl.len = pl.i == a ? len0 : len_of(p, pl.i);
             pl.seqs = e - pl.seq0;
-            const uint32_t w =
-                tiles_of(p, pl.seqs) * (uint32_t)p.H * (units_of<UNIT>(len_of(p, pl.i)) + p.lead);
+            const uint32_t w = tiles_of(p, pl.seqs) * (uint32_t)p.H * (units_of<UNIT>(pl.len) + p.lead);
             if (pl.u0 < first + w) break;
             first += w;
             pl.seq0 = e;
@@ -162,8 +169,9 @@ RKV_DEV Place find_place(const Params& p, uint32_t run) {
     pl.i = __shfl_sync(0xffffffffu, pl.i, owner);
     pl.seq0 = __shfl_sync(0xffffffffu, pl.seq0, owner);
     pl.seqs = __shfl_sync(0xffffffffu, pl.seqs, owner);
+    pl.len = __shfl_sync(0xffffffffu, pl.len, owner);
     first = __shfl_sync(0xffffffffu, first, owner);
-    const uint32_t n_s = units_of<UNIT>(len_of(p, pl.i)) + p.lead, tiles = tiles_of(p, pl.seqs);
+    const uint32_t n_s = units_of<UNIT>(pl.len) + p.lead, tiles = tiles_of(p, pl.seqs);
     const uint32_t at = (pl.u0 - first) / n_s;
     pl.h = (int)(at / tiles);
     pl.tile = (int)(at - pl.h * tiles);
@@ -173,20 +181,21 @@ RKV_DEV Place find_place(const Params& p, uint32_t run) {
 
 // A piece of a tile that a block works on.
 struct Piece {
-    int i, seq0, rows, h, row0, len, c0, c1;  // rows of the tile in use, from row0 of the group on
-    uint32_t slot, parts;  // parts: blocks that share the tile, where it begins here
+    // rows of the tile in use (none or less: past the queries), from row0 of the group on
+    int i, seq0, rows, h, row0, len, c0, c1;
+    uint32_t slot, parts;  // parts: runs that share the tile, where it begins here
     bool whole, begins;
 };
 // The next piece of the run (false: none left), which then starts behind it.
 template <int UNIT>
-RKV_DEV bool next_piece(const Params& p, uint32_t run, Place& pl, Piece& c) {
+RKV_DEV bool next_piece(const Params& p, uint32_t run, int member, Place& pl, Piece& c) {
     while (pl.u0 < pl.u1) {
         c.i = pl.i;
         c.seq0 = pl.seq0;
         c.h = pl.h;
-        c.row0 = pl.tile * p.tile;
+        c.row0 = (pl.tile * p.team + member) * p.tile;
         c.rows = min(p.tile, pl.seqs * p.R - c.row0);
-        c.len = len_of(p, pl.i);
+        c.len = pl.len;
         const uint32_t n_s = units_of<UNIT>(c.len), lead = p.lead, n_l = n_s + lead;
         const uint32_t from = pl.u0 - pl.start, to = min(n_l, pl.u1 - pl.start);
         const uint32_t j = from > lead ? from - lead : 0, e = to > lead ? to - lead : 0;
@@ -194,7 +203,7 @@ RKV_DEV bool next_piece(const Params& p, uint32_t run, Place& pl, Piece& c) {
         c.c1 = e == n_s ? c.len : e * UNIT;
         c.whole = j == 0 && e == n_s;
         c.begins = j == 0;
-        c.slot = 2 * run + (j > 0 ? 0 : 1);
+        c.slot = 2 * (run * p.team + member) + (j > 0 ? 0 : 1);
         c.parts = j > 0 || c.whole || e == 0 ? 0 : run_of(pl, pl.start + n_l - 1) - run + 1;
         pl.u0 = pl.start + to;
         if (to == n_l) {
@@ -208,6 +217,7 @@ RKV_DEV bool next_piece(const Params& p, uint32_t run, Place& pl, Piece& c) {
                         ++pl.i;
                         pl.seqs = pl.i <= p.P ? max(pl.seq0, end_of(p, pl.i)) - pl.seq0 : 1;
                     } while (pl.seqs == 0);
+                    if (pl.u0 < pl.u1) pl.len = len_of(p, pl.i);
                 }
             }
         }
@@ -222,6 +232,10 @@ RKV_DEV void place_of_row(const Params& p, int seq0, int h, int row, int& s, int
     tk = x / p.G;
     hd = h * p.G + x - tk * p.G;
 }
+// The rows (up to 256) and parts of a tile that has to be joined; 0: nothing to join.
+RKV_DEV int join_of(int rows, uint32_t parts) { return parts == 0 ? 0 : rows | (int)(parts << 9); }
+RKV_DEV int rows_of(int join) { return join & 511; }
+RKV_DEV int parts_of(int join) { return join >> 9; }
 RKV_DEV bool bad_length(const Params& p, const Piece& c) {
     return c.begins && c.h == 0 && c.row0 == 0 && c.i < p.P && p.lens[c.i] != c.len;
 }
