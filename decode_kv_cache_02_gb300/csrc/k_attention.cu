@@ -1960,8 +1960,9 @@ AttnPlan attn_plan(const AttnArgs& a) {
     // a problem's beginning and end cost about as much as this many units (64
     // ragged sequences of 131 .. 4224 rows, us at 0, 1, 2, 4, 8: bf16 103, 102,
     // 95, 95, 96; 4 bits 64, 60, 56, 58, 62; 8 new tokens, head_dim 64: 72, 70,
-    // 66, 61, 61)
-    pl.lead = a.bits ? 2 : 4;
+    // 66, 61, 61; 8 bits at 1, 2, 4 of their longer ones: 62, 59, 61, 8 new tokens
+    // 64, 60, 57)
+    pl.lead = a.bits == 4 || (a.bits == 8 && pl.rows == 8) ? 2 : 4;
     int64_t runs = (blocks + pl.groups - 1) / pl.groups;
     if (runs > units) runs = units;
     pl.runs = (int)runs;
