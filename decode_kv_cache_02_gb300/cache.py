@@ -619,10 +619,10 @@ def rkv_prefix_attention_workspace_size(q, num_kv_heads: int, max_rows: int, num
     max_rows, max_prefix_rows = int(max_rows), int(max_prefix_rows)
     _prefix_sizes(q, H, max_rows, P, max_prefix_rows)
     S, T, hq, d = q.shape
-    # (blocks of one row are the least that any pool has; the size does not depend on them, and with some cu_seqs the
-    # sequences need not divide)
+    # the size depends neither on the blocks (tables of blocks of one row hold any length) nor
+    # on how the sequences are shared out (some cu_seqs: they need not divide)
     desc = _pack_desc(S, H, hq // H, d, 1, 1, max_rows, _dtype(q))
-    rows = max(max_prefix_rows, 1)
+    rows = max_prefix_rows if P else 1
     n = int(load().rkv_prefix_attention_workspace_size(desc, T, max_rows,
                                                        _pack_prefixes(0, 0, 256, P, rows, rows)))
     if n == 0:
@@ -660,12 +660,14 @@ def rkv_prefix_attention(q, K_pool, V_pool, prefix_table, prefix_lens, block_tab
         raise ValueError("prefix_table must be int32 [num_prefixes, max_blocks]")
     P, pb = prefix_table.shape
     rows = pb * bs if max_prefix_rows is None else int(max_prefix_rows)
+    if not P:
+        rows = pb = 1  # (no prefix: neither is looked at)
     if P and not 0 < rows <= _MAX_ROWS:
         raise ValueError("max_prefix_rows (by default the table's rows) must be 1 .. 2^30")
     S = q.shape[0] if q.dim() == 4 else 0
     if cu_seqs is None and P and S % P:
         raise ValueError("without cu_seqs every prefix has the same number of sequences")
-    prefixes = _pack_prefixes(_ints(prefix_table, "prefix_table", dev, P, pb),
+    prefixes = _pack_prefixes(_ints(prefix_table, "prefix_table", dev, *prefix_table.shape),
                               _ints(prefix_lens, "prefix_lens", dev, P),
                               0 if cu_seqs is None else _ints(cu_seqs, "cu_seqs", dev, P + 1),
                               P, pb, rows)

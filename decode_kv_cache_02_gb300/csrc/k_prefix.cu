@@ -214,9 +214,9 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_kernel(const __grid_consta
 }
 
 // Joins the pieces of the tiles that begin in one run and end in a later one, and the
-// own rows' sums.  A block takes 32 queries (lanes) of a tile and 32 dimensions; its
-// warps share the pieces.
-constexpr int kJoinWarps = 8, kMaxBlocks = 320, kJoinLook = kMaxBlocks / 32;
+// own rows' sums.  A block takes 32 queries (lanes) of a tile and 32 dimensions: up to
+// kFew pieces by a warp for each four of them, more by all warps together.
+constexpr int kJoinWarps = 8, kFew = 16, kMaxBlocks = 320, kJoinLook = kMaxBlocks / 32;
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32, 3) prefix_join_kernel(const __grid_constant__ Params p) {
     __shared__ float4 sh_v[kJoinWarps][8][32];
@@ -258,12 +258,37 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 3) prefix_join_kernel(const _
         const int64_t at = ((int64_t)s * p.T + tk) * p.H * p.G + hd;
         const float2 own = p.own_ml[at];
         const float4 mine = *reinterpret_cast<const float4*>(p.own + at * D + d);
+        const auto slot_of = [&](int i) {
+            return i == 0 ? 2 * (int64_t)from + 1 : 2 * (from + (int64_t)i * p.team);
+        };
+        const auto write = [&](float m, float l, float4 v) {
+            if (r >= rows) return;
+            const Joined j = join_own(m, l, own);
+            store4(static_cast<T*>(p.out) + s * p.o_seq + tk * p.o_tok + hd * p.o_head + d, join4(j, v, mine));
+            if (d == 0 && p.lse) p.lse[at] = j.lse;
+        };
         float m = -INFINITY, l = 0.f;
+        if (parts <= kFew) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int i = 0; i < parts; ++i) {
+                const int64_t slot = slot_of(i);
+                const float2 ml = p.partial_ml[slot * p.tile + r];
+                const float4 y = p.partial[(slot * (D / 4) + d / 4) * p.tile + r];
+                const float mx = fmaxf(m, ml.x);
+                const float f = weight(m, l, mx), g = weight(ml.x, ml.y, mx);
+                m = mx;
+                l = l * f + ml.y * g;
+                v = make_float4(v.x * f + y.x * g, v.y * f + y.y * g, v.z * f + y.z * g, v.w * f + y.w * g);
+            }
+            write(m, l, v);
+            continue;
+        }
         float4 v[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int i = warp; i < parts; i += kJoinWarps) {
-            const int64_t slot = i == 0 ? 2 * from + 1 : 2 * (from + (int64_t)i * p.team);
+            const int64_t slot = slot_of(i);
             const float2 ml = p.partial_ml[slot * p.tile + r];
             float4 y[8];
 #pragma unroll
@@ -277,6 +302,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 3) prefix_join_kernel(const _
                 v[x] = make_float4(v[x].x * f + y[x].x * g, v[x].y * f + y[x].y * g,
                                    v[x].z * f + y[x].z * g, v[x].w * f + y[x].w * g);
         }
+        __syncthreads();  // the shared sums before these have been read
         sh_m[warp][lane] = m;
         sh_l[warp][lane] = l;
 #pragma unroll
@@ -293,12 +319,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 3) prefix_join_kernel(const _
             sum += sh_l[w][lane] * f;
             y.x += x.x * f; y.y += x.y * f; y.z += x.z * f; y.w += x.w * f;
         }
-        if (r < rows) {
-            const Joined j = join_own(mx, sum, own);
-            store4(static_cast<T*>(p.out) + s * p.o_seq + tk * p.o_tok + hd * p.o_head + d, join4(j, y, mine));
-            if (d == 0 && p.lse) p.lse[at] = j.lse;
-        }
-        __syncthreads();
+        write(mx, sum, y);
     }
 }
 

@@ -3,22 +3,35 @@
 // rkv_prefix.cuh for the line of work.
 //
 // The queries of all sequences of a prefix that use a KV head are the rows of two products
-// with the prefix's keys and values: S = Q K^T, O += P V, each 128 queries x 128 rows a
-// step, accumulated in TMEM.  One block an SM, ten warps:
-//   * warp 9: TMA producer, a ring of tiles of 128 rows (K and V in the order in which
-//     they are used) through the prefix's block table, one copy per block (of up to 128
+// with the prefix's keys and values: S = Q K^T, O += P V, each 128 queries x 64 rows a
+// step, accumulated in TMEM.  One block an SM, eleven warps:
+//   * warp 10: TMA producer, a ring of tiles of 64 rows (K and V in the order in which
+//     they are used) through the prefix's block table, one copy per block (of up to 64
 //     rows) and 64 columns, 128-byte swizzle.  Rows past the prefix in its last block are
 //     cleared in V, where they would meet a probability of 0.
-//   * warp 8: issues the MMAs.  S from shared memory; O += P V with P as the operand in
-//     TMEM and V as it lies, its rows being the contracted index (an MN-major operand).
-//   * warps 0-3 and 4-7: softmax, one query a thread, which is a row of TMEM: maxima, sums
-//     and scales take no exchange between threads.  P is
-//     written over S as bf16 (one part, 2^-8 of it: a second would take the tensor cores
-//     half as long again).  O is brought to a new maximum only where a logit passes the old
-//     one by more than 8 (log2), so that hardly ever anybody waits for it.
-// The two softmax groups keep each other's products off the critical path.  With more
-// than 128 queries a prefix they take 128 each, all rows; with fewer (SPLIT) the same
-// queries, every other unit of rows each, and join at a piece's end through shared memory.
+//   * warps 8 and 9: issue the MMAs, one warp for each group of 128 queries.  S from shared
+//     memory; O += P V with P as the operand in TMEM and V as it lies, its rows being the
+//     contracted index (an MN-major operand).
+//   * warps 0-3 and 4-7: softmax of a group, one query a thread, which is a row of TMEM:
+//     maxima, sums and scales take no exchange between threads.  P is written over S as
+//     bf16 (one part, 2^-8 of it: a second would take the tensor cores half as long
+//     again).  O is brought to a new maximum only where a logit passes the old one by more
+//     than 8 (log2), so that hardly ever anybody waits for it.
+// With more than 128 queries a prefix the groups take 128 each, all rows; with fewer
+// (SPLIT) the same queries, every other unit of rows each, and join at a piece's end
+// through shared memory.
+//
+// Why units of 64 rows: at head_dim 128 O takes half of TMEM, and the other half holds two
+// buffers of S for each group only if they are 64 columns wide.  With one buffer of 128 the
+// next S waits until P V is done with it, 340 cycles behind the pipe's own time, and the
+// softmax waits for that S: 241 us for the case below where two buffers take 212, although
+// S in steps of 64 costs the pipe half as much again (48 cycles an MMA, the operands'
+// shared memory, where 128 columns take 64).
+//
+// Measured (one GB300, head_dim 128, 8 KV heads): 128 samples of 131071 rows, G = 4, 275
+// GFLOP: 173 us from the first piece to the last, 1.6 PFLOP/s; about 1600 cycles a step of
+// 2 x 128 queries, of which the products take 1280.  A piece's beginning (its place on the
+// line, queries, first tiles) and end take about 4 us each, which bounds short prefixes.
 // Every wait is bounded; one that runs out records a device error, and all roles end.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -120,8 +133,8 @@ RKV_DEV uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 // One lane of a converged warp.  (The issuing warp stays together around its MMAs, so
-// that what they are given is uniform: an issue by a lane of its own, each operand moved
-// to the uniform registers, takes 100 cycles where the product takes 64.)
+// that what they are given is uniform: issued by a lane of its own they took 100 cycles
+// each where the product takes 64.)
 RKV_DEV bool elect_one() {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
@@ -153,40 +166,40 @@ RKV_DEV bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort_flag) 
     return wait_at(smem_u32(bar), parity, abort_flag);
 }
 
-// Units whose K goes into the ring before V of unit 0 (S has two buffers a group), and
-// the places of K and V of unit u among a piece's tiles.
-template <bool SPLIT> constexpr int kAhead = SPLIT ? 4 : 2;
-template <bool SPLIT> RKV_DEV uint32_t place_k(int u) { return u + max(0, u + 1 - kAhead<SPLIT>); }
-template <bool SPLIT> RKV_DEV uint32_t place_v(int u, int n) { return u + min(u + kAhead<SPLIT>, n); }
+// Whoever waits for a tile has waited for the one that was in its place before: a
+// parity tells a phase that is over from the one before it, not from the one behind it.
+// So with SPLIT each group has a ring of its own (its share of the stages), and without
+// it both issuing warps go through all tiles, those of a piece without queries for the
+// second group as well.
+template <int D, bool SPLIT> constexpr int kRing = Cfg<D>::STAGES / (SPLIT ? 2 : 1);
+// Two units' K go into a ring before V of the first (S has two buffers a group).  The
+// places of K and V of the ring's unit q among its 2 n tiles of a piece.
+RKV_DEV uint32_t place_k(int q) { return q + max(0, q - 1); }
+RKV_DEV uint32_t place_v(int q, int n) { return q + min(q + 2, n); }
 
-// The products of a group's units of a piece of n, by its issuing warp.  (One for each
+// The products of a group's n units of a piece, by its issuing warp.  (One for each
 // group: what a warp does between two MMAs, waits that are over take 100 cycles, is time
 // in which the other's fill the tensor cores; one warp for both: 2090 cycles for 64 rows
 // of 2 x 128 queries.)
 struct Issue {
     uint32_t bars;  // full, empty, .. as in the kernel
     uint32_t s, o;  // TMEM of the group's S and O
-    uint32_t tile;  // tiles of earlier pieces
+    uint32_t tile;  // tiles of earlier pieces in the group's ring
     uint32_t ph;    // phases of p_full and o_done, a bit a buffer
 };
 template <int D, bool SPLIT>
-RKV_DEV bool issue_piece(Issue& w, int x, int n, bool alone, uint64_t q0, uint64_t k0, uint64_t v0,
+RKV_DEV bool issue_piece(Issue& w, int x, int n, uint64_t q0, uint64_t k0, uint64_t v0,
                          volatile int* abort_flag) {
     using C = Cfg<D>;
-    constexpr int STEP = SPLIT ? 2 : 1;
+    constexpr int RING = kRing<D, SPLIT>;
     constexpr uint32_t kIdescS = idesc_bf16(128, kUnit);
     constexpr uint32_t kIdescO = idesc_bf16(128, D) | (1u << 16);  // B by rows
     constexpr uint32_t kEmpty = 8 * C::STAGES, kS = 2 * kEmpty + 16, kP = kS + 32, kO = kP + 32;
-    uint32_t st, ph;
+    uint32_t st;
     const auto find = [&](uint32_t t) {
         t += w.tile;
-        st = t % C::STAGES;
-        ph = (t / C::STAGES) & 1u;
-        return wait_at(w.bars + 8 * st, ph, abort_flag);
-    };
-    const auto release = [&] {
-        commit_to(w.bars + kEmpty + 8 * st);
-        if (!SPLIT && alone) commit_to(w.bars + kEmpty + 8 * st);  // for the other group as well
+        st = (SPLIT ? x * RING : 0) + t % RING;
+        return wait_at(w.bars + 8 * st, (t / RING) & 1u, abort_flag);
     };
     const auto logits = [&](uint32_t b) {  // S into buffer b
         if (elect_one()) {
@@ -196,17 +209,17 @@ RKV_DEV bool issue_piece(Issue& w, int x, int n, bool alone, uint64_t q0, uint64
                 mma_bf16(w.s + b * 64, q0 + (i >> 2) * (kQChunk >> 4) + 2 * (i & 3),
                          k + (i >> 2) * (kChunk >> 4) + 2 * (i & 3), kIdescS, i != 0);
             commit_to(w.bars + kS + 16 * x + 8 * b);
-            release();
+            commit_to(w.bars + kEmpty + 8 * st);
         }
         __syncwarp();
     };
-    for (int u = SPLIT ? x : 0, q = 0; q < 2 && u < n; u += STEP, ++q) {
-        if (!find(place_k<SPLIT>(u))) return false;
+    for (int q = 0; q < 2 && q < n; ++q) {
+        if (!find(place_k(q))) return false;
         logits(q);
     }
-    for (int u = SPLIT ? x : 0, q = 0; u < n; u += STEP, ++q) {
+    for (int q = 0; q < n; ++q) {
         const uint32_t b = q & 1;
-        if (!find(place_v<SPLIT>(u, n))) return false;
+        if (!find(place_v(q, n))) return false;
         if (!wait_at(w.bars + kP + 16 * x + 8 * b, (w.ph >> b) & 1u, abort_flag)) return false;
         tc_fence_after();
         if (elect_one()) {  // O += P V, P from buffer b
@@ -215,12 +228,12 @@ RKV_DEV bool issue_piece(Issue& w, int x, int n, bool alone, uint64_t q0, uint64
             for (int k = 0; k < kUnit / 16; ++k)
                 mma_bf16_ts(w.o, w.s + b * 64 + 8 * k, v + (2048 >> 4) * k, kIdescO, q != 0 || k != 0);
             commit_to(w.bars + kO + 16 * x + 8 * b);
-            release();
+            commit_to(w.bars + kEmpty + 8 * st);
         }
         __syncwarp();
-        if (u + 2 * STEP < n) {
+        if (q + 2 < n) {
             // the S of two units on takes the place of this P, which the product has to be done with
-            if (!find(place_k<SPLIT>(u + 2 * STEP))) return false;
+            if (!find(place_k(q + 2))) return false;
             if (!wait_at(w.bars + kO + 16 * x + 8 * b, (w.ph >> b) & 1u, abort_flag)) return false;
             logits(b);
         }
@@ -270,14 +283,15 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     // O += P V done, by the buffer of P: a phase is then never more than one ahead of who
     // waits for it (the next product from a buffer waits for the group's next P in it)
     uint64_t* o_done = p_full + 4;         // [group][buffer]
-    uint64_t* tail_bar = o_done + 4;
-    uint64_t* drain_bar = tail_bar + 1;  // [group]
-    uint64_t* x_full = drain_bar + 2;  // SPLIT: half of the second group's output is there
+    uint64_t* tail_bar = o_done + 4;       // a tile that has rows to clear
+    uint64_t* drain_bar = tail_bar + 1;    // [group]
+    uint64_t* x_full = drain_bar + 2;      // SPLIT: half of the second group's output is there
     uint64_t* x_empty = x_full + 1;
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(x_empty + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     float2* sh_ml = reinterpret_cast<float2*>(smem + C::ML);
-    float* sh_x = reinterpret_cast<float*>(smem + C::QTILE);  // [D / 2][128] (the second group's queries are the first's)
+    // [D / 2][128], in the place of the second group's queries, which are the first's then
+    float* sh_x = reinterpret_cast<float*>(smem + C::QTILE);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t run = blockIdx.x / p.team;
@@ -289,6 +303,7 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 4);
+            mbar_init(&drain_bar[i], 1);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
@@ -296,8 +311,6 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
             mbar_init(&o_done[i], 1);
         }
         mbar_init(tail_bar, 1);
-        mbar_init(&drain_bar[0], 1);
-        mbar_init(&drain_bar[1], 1);
         mbar_init(x_full, 4);
         mbar_init(x_empty, 4);
         *s_abort = 0;
@@ -326,7 +339,8 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         const int b = lane / C::KC, ch = lane - b * C::KC, own = b << log2box;
         const bool copies = lane < (kUnit >> log2box) * C::KC;  // 16 at most
         const uint32_t to = ch * kChunk + own * 128;
-        uint32_t st = 0, ph = 1, tiles = 0, tails = 0;
+        constexpr int RING = kRing<D, SPLIT>;
+        uint32_t tiles = 0, tiles1 = 0, tails = 0;  // tiles in the (first) ring, SPLIT: in the second
         // the block of the lane's rows of unit u, asked for one tile ahead (-1: rows past the piece)
         auto look_up = [&](int u) {
             const int r = c.c0 + u * kUnit + own;
@@ -334,10 +348,11 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         };
         auto load = [&](const CUtensorMap* map, int u, int block, bool is_v) {
             const int r0 = c.c0 + u * kUnit;
-            const bool there = (unsigned)block < (unsigned)p.num_blocks;
+            const bool there = (unsigned)block < (unsigned)p.num_blocks, second = SPLIT && (u & 1);
+            const uint32_t t = second ? tiles1 : tiles, st = (second ? RING : 0) + t % RING;
             if (copies && !there && !is_v && ch == 0 && r0 + own < c.c1)
                 set_error(p.status, kDevErrIndex, (unsigned)(r0 + own));
-            if (!wait_all(&empty[st], ph, s_abort)) return false;
+            if (!wait_all(&empty[st], ((t / RING) & 1u) ^ 1u, s_abort)) return false;
             uint8_t* dst = ring + st * C::TILE;
             const bool clear = is_v && r0 + kUnit > c.c1 && (c.c1 & (box - 1)) != 0;
             uint64_t* bar = clear ? tail_bar : &full[st];
@@ -359,17 +374,14 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[st]);
             }
-            ++tiles;
-            if (++st == C::STAGES) {
-                st = 0;
-                ph ^= 1u;
-            }
+            tiles += !second;
+            tiles1 += second;
             return true;
         };
         while (ok && next_piece<kUnit>(p, run, member, place, c)) {
             const int n = c.rows > 0 ? units_in(c) : 0;
             int k = 0, next_k = look_up(0), next_v = next_k;
-            for (; ok && k < kAhead<SPLIT> && k < n; ++k) {
+            for (; ok && k < (SPLIT ? 4 : 2) && k < n; ++k) {
                 const int block = next_k;
                 next_k = look_up(k + 1);
                 ok = load(&kmap, k, block, false);
@@ -391,8 +403,10 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         }
         // every copy issued has landed before the block may end
         volatile int never = 0;
-        for (uint32_t u = tiles > (uint32_t)C::STAGES ? tiles - C::STAGES : 0; u < tiles; ++u)
-            mbar_wait(&full[u % C::STAGES], (u / C::STAGES) & 1, &never);
+        for (uint32_t t = tiles > RING ? tiles - RING : 0; t < tiles; ++t)
+            mbar_wait(&full[t % RING], (t / RING) & 1, &never);
+        for (uint32_t t = tiles1 > RING ? tiles1 - RING : 0; t < tiles1; ++t)
+            mbar_wait(&full[RING + t % RING], (t / RING) & 1, &never);
     } else if (warp >= 8) {
         // ---------------------------------------------------- MMA issuers --
         const int x = warp - 8;
@@ -402,12 +416,20 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
                        v0 = sdesc_rows(ring, kChunk);
         while (ok && next_piece<kUnit>(p, run, member, place, c)) {
             const int n = c.rows > 0 ? units_in(c) : 0;
-            if (n > (SPLIT ? x : 0) && (SPLIT || c.rows > 128 * x)) {
+            const int mine = SPLIT ? (n + 1 - x) >> 1 : n;
+            if (SPLIT || c.rows > 128 * x) {
+                if (mine == 0) continue;
                 if (!(ok = wait_all(&q_full[x], asked++ & 1, s_abort))) break;
                 tc_fence_after();
-                ok = issue_piece<D, SPLIT>(w, x, n, c.rows <= 128, q0, k0, v0, s_abort);
+                ok = issue_piece<D, SPLIT>(w, x, mine, q0, k0, v0, s_abort);
+            } else {
+                for (int t = 0; ok && t < 2 * mine; ++t) {
+                    const uint32_t st = (w.tile + t) % C::STAGES;
+                    ok = wait_all(&full[st], ((w.tile + t) / C::STAGES) & 1, s_abort);
+                    if (ok && lane == 0) mbar_arrive(&empty[st]);
+                }
             }
-            w.tile += 2 * n;
+            w.tile += 2 * mine;
         }
         if (!ok) {
             *s_abort = 1;

@@ -348,8 +348,15 @@ struct PrefixCall {
     AttnPlan own;
     rkv::PrefixPlan plan;
     size_t own_bytes() const { return attention_bytes(own); }
+    // what a call of these sizes needs whatever its blocks are
     size_t bytes() const {
-        return own_bytes() + aligned_floats(plan.raw_floats) + aligned_floats(plan.partial_floats);
+        size_t most = 0;
+        for (int tensor = 0; tensor < (args.own.dtype == RKV_DTYPE_BF16 ? 2 : 1); ++tensor) {
+            const rkv::PrefixPlan p = rkv::prefix_plan(args, tensor != 0);
+            const size_t n = own_bytes() + aligned_floats(p.raw_floats) + aligned_floats(p.partial_floats);
+            if (n > most) most = n;
+        }
+        return most;
     }
 };
 
@@ -655,14 +662,7 @@ int rkv_q8_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
 size_t rkv_prefix_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int max_rows,
                                            const rkv_prefixes* prefixes) {
     PrefixCall c;
-    if (check_prefix(desc, nullptr, n_new, max_rows, prefixes, &c)) return 0;
-    // one size serves every block size
-    size_t n = 0;
-    for (int tensor = 0; tensor < (desc->dtype == RKV_DTYPE_BF16 ? 2 : 1); ++tensor) {
-        c.plan = rkv::prefix_plan(c.args, tensor != 0);
-        if (c.bytes() > n) n = c.bytes();
-    }
-    return n;
+    return check_prefix(desc, nullptr, n_new, max_rows, prefixes, &c) ? 0 : c.bytes();
 }
 
 int rkv_prefix_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,

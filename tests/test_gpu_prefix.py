@@ -60,11 +60,12 @@ class Case:
         return pkg.rkv_prefix_attention(q, self.K, self.V, self.ptable.to(DEV), ints(self.plens), self.table.to(DEV),
                                         ints(self.lens), cu_seqs=ints(self.groups) if cu else None, workspace=ws, **kw)
 
-    def compare(self, out, lse, scale=None, q=None):
+    def compare(self, out, lse, scale=None, q=None, seqs=None):
+        """seqs: of the first of the sequences alone."""
         scale = self.d ** -0.5 if scale is None else scale
-        q = self.q if q is None else q
+        q = (self.q if q is None else q)[:seqs]
         pk, pv = (prefix_ref.rows_of(x, self.ptable, self.plens) for x in (self.K, self.V))
-        ok, ov = (prefix_ref.rows_of(x, self.table, self.lens) for x in (self.K, self.V))
+        ok, ov = (prefix_ref.rows_of(x, self.table, self.lens[:seqs]) for x in (self.K, self.V))
         e, el, A, L = prefix_ref.attention(q, pk, pv, self.groups, ok, ov, self.lens, scale)
         rows = max([0] + self.plens) + max(self.lens)
         b, bl = ref.attention_bounds(e, el, A, L, scale, self.d, max(rows, 1), "fp32" if self.dt == FP else "bf16")
@@ -93,6 +94,9 @@ CASES = [
     ([5000], [0, 3], [30, 1, 2], 1, 1, 1, 128, 16),                     # few queries, many runs
     ([2500] * 5, [0, 1, 2, 3, 4, 5], [300, 20, 1, 0, 77], 2, 4, 2, 128, 1024),
     ([20000], [0, 33], [5] * 33, 1, 2, 4, 64, 128),
+    ([400, 70, 9], [0, 90, 95, 96], [6 + i % 9 for i in range(97)], 1, 1, 8, 128, 16),  # teams with members without queries
+    ([300, 900, 40, 700, 65, 129], [0, 4, 70, 73, 139, 200, 203], [i % 4 for i in range(204)], 1, 8, 4, 128, 64),  # one or two groups of queries in turn
+    ([150, 600], [0, 9, 12], [64 + i for i in range(12)], 64, 1, 8, 64, 32),            # 4608 and 1536 queries
     ([1, 2, 3] * 30, list(range(0, 182, 2)) , [1 + i % 3 for i in range(180)], 1, 1, 1, 64, 8),  # many prefixes
 ]
 
@@ -108,6 +112,19 @@ def test_prefix_attention(case, dt):
     again, lse2 = c.call(ws)
     assert torch.equal(again, out) and torch.equal(lse2, lse)
     assert status(ws) == 0
+
+
+@pytest.mark.parametrize("d, bs", [(128, 128), (128, 8), (64, 64), (64, 16)])
+@pytest.mark.parametrize("queries", [70, 200])
+def test_long_pieces(d, bs, queries):
+    """A block's share of a prefix goes through its ring of tiles many times, call after call: the same bits, and
+    those of the definition."""
+    c = Case([60001, 9000], [0, queries - 5, queries], [3 + i % 5 for i in range(queries)], 1, 8, 1, d, bs, BF)
+    ws = [c.ws() for _ in range(2)]
+    first, lse = c.call(ws[0])
+    c.compare(first[:3], lse[:3], seqs=3)
+    again = [c.call(w)[0] for _ in range(20) for w in ws]
+    assert all(torch.equal(x, first) for x in again) and status(ws[0]) == 0 and status(ws[1]) == 0
 
 
 @pytest.mark.parametrize("bs", [1, 2, 4])
