@@ -1,5 +1,5 @@
 // k_attention.cu -- attention of a few new tokens over a paged cache, bf16,
-// fp32 or held in 4 bits: out = softmax(scale * q K^T) V for each KV head's
+// fp32 or held in 4 or 8 bits: out = softmax(scale * q K^T) V for each KV head's
 // group of query heads.
 //
 // One pass over the cache with a running maximum and sum.  The rows of all
@@ -35,6 +35,9 @@
 // elements below 2^-27 of its row's largest are off by up to 2^-35 of that.  What
 // the fp16 steps are relative to is the query's own (kSpread).
 //
+// 8 bits: codes become bf16 numbers exactly (bytes_as_bf16), K's scale meets the logit and
+// V's the probability in fp32; the rest is the bf16 cache's.
+//
 // The running maximum moves only when a logit passes it by more than 8 (log2):
 // p stays below 2^8 and the rescaling almost never runs.  (4 bits: by more than 4.)
 //
@@ -45,7 +48,10 @@
 // of 131071, G = 5: 47.0 us, 3.6 TB/s.  In steady state a warp spends 379 instructions
 // and an SM quarter 592 cycles on 16 rows, where HBM's rate would allow 435: no pipe is
 // above 55 in a hundred of them (logic; issue slots 64), the twelve warps of an SM
-// wait for their own last instructions.
+// wait for their own last instructions.  8 bits: the same 64 sequences 59.1 us, 5.0 TB/s;
+// one of 131071, G = 8: 54.0 us, 5.1 TB/s: 432 instructions for 16 rows, 240 of them
+// codes to bf16 and both operands' order, where HBM's rate would allow 720 cycles: logic 54
+// in a hundred, issue slots 52 (three stages at two blocks an SM: 62.6 and 53.3).
 #include <cuda_fp16.h>
 #include <float.h>
 
@@ -968,11 +974,12 @@ RKV_DEV void store4(__nv_bfloat16* p, float4 v) {
 }
 
 // Four values of a query's output from its sums v relative to 2^mx, and the log of its
-// sum (or, where they are to be joined with others', v and mx and the sum as they are).
-template <typename T, int D>
+// sum (RAW: or, where they are to be joined with others', v and mx and the sum as they
+// are; packed caches have no such calls).
+template <typename T, int D, bool RAW>
 RKV_DEV void emit(const Params& p, int64_t s, int tk, int hd, int d, float4 v, float mx, float sum) {
     const int64_t at = (s * p.T + tk) * (int64_t)p.H * p.G + hd;
-    if (p.raw) {
+    if (RAW && p.raw) {
         store4(p.raw + at * D + d, v);
         if (d == 0) *reinterpret_cast<float2*>(p.raw_ml + 2 * at) = make_float2(mx, sum);
         return;
@@ -985,7 +992,7 @@ RKV_DEV void emit(const Params& p, int64_t s, int tk, int hd, int d, float4 v, f
 
 // Joins the warps' weighted sums in acc [kWarps][ROWS][D] and writes the rows:
 // the output where the chunk is the whole sequence, else its part.
-template <typename T, int D, int ROWS>
+template <typename T, int D, int ROWS, bool RAW>
 RKV_DEV void finish(const Params& p, const float* acc, const float (&sh_m)[kWarps][ROWS],
                     const float (&sh_l)[kWarps][ROWS], int64_t s, int h, int row_first,
                     int64_t slot, bool whole) {
@@ -1004,7 +1011,7 @@ RKV_DEV void finish(const Params& p, const float* acc, const float (&sh_m)[kWarp
         }
         if (whole) {
             const int tk = row / p.G, hd = h * p.G + row - tk * p.G;
-            emit<T, D>(p, s, tk, hd, d, v, mx, sum);
+            emit<T, D, RAW>(p, s, tk, hd, d, v, mx, sum);
         } else {
             *reinterpret_cast<float4*>(p.partial + (slot * ROWS + r) * D + d) = v;
             if (d == 0) {
@@ -1047,7 +1054,7 @@ RKV_DEV float2 remote2(uint32_t at) {
 // warps, then takes its part of the problem's output over all blocks.  No second
 // launch and no scratch.
 constexpr int kCluster = 8;
-template <typename T, int D, int ROWS>
+template <typename T, int D, int ROWS, bool RAW>
 RKV_DEV void finish_cluster(const Params& p, float* acc, const float (&sh_m)[kWarps][ROWS],
                             const float (&sh_l)[kWarps][ROWS], float2 (&sh_ml)[ROWS], int s, int h,
                             int row_first, uint32_t rank) {
@@ -1097,7 +1104,7 @@ RKV_DEV void finish_cluster(const Params& p, float* acc, const float (&sh_m)[kWa
             v.x += x[i].x * f; v.y += x[i].y * f; v.z += x[i].z * f; v.w += x[i].w * f;
         }
         const int tk = row / p.G, hd = h * p.G + row - tk * p.G;
-        emit<T, D>(p, s, tk, hd, d, v, mx, sum);
+        emit<T, D, RAW>(p, s, tk, hd, d, v, mx, sum);
     }
     cluster_sync();  // nobody leaves while its shared memory is read
 }
@@ -1566,10 +1573,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && BITS ? 3 : 2) attn_ker
             }
         __syncthreads();
         if (p.cluster) {
-            finish_cluster<__nv_bfloat16, D, ROWS>(p, acc, sh_m, sh_l, sh_ml, s, h, row_first, rank);
+            finish_cluster<__nv_bfloat16, D, ROWS, BITS == 0>(p, acc, sh_m, sh_l, sh_ml, s, h, row_first, rank);
             return;
         }
-        finish<__nv_bfloat16, D, ROWS>(p, acc, sh_m, sh_l, s, h, row_first,
+        finish<__nv_bfloat16, D, ROWS, BITS == 0>(p, acc, sh_m, sh_l, s, h, row_first,
                                        (int64_t)c.slot * p.groups + group, c.whole);
         __syncthreads();  // the next piece's copies overwrite what was just read
     }
@@ -1754,7 +1761,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
                     make_float4(o[r][0] * f, o[r][1] * f, o[r][2] * f, o[r][3] * f);
         }
         __syncthreads();
-        finish<float, D, ROWS>(p, acc, sh_m, sh_l, c.s, c.h, row_first, (int64_t)c.slot * p.groups + group,
+        finish<float, D, ROWS, true>(p, acc, sh_m, sh_l, c.s, c.h, row_first, (int64_t)c.slot * p.groups + group,
                                c.whole);
         __syncthreads();
     }
@@ -1767,7 +1774,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
 // A warp takes a query; where the pieces are many (few long sequences), the
 // block's eight warps share a query's pieces.
 constexpr int kJoinWarps = 8;
-template <typename T, int D>
+template <typename T, int D, bool RAW>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
     const __grid_constant__ Params p, int rows) {
     constexpr int LANES = D / 4;
@@ -1776,7 +1783,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = blockIdx.x % p.groups;
     const int run = blockIdx.x / p.groups;
-    if (p.raw) let_next_begin();  // (the pass over the prefixes waits where it takes these sums)
+    if (RAW) let_next_begin();  // (the pass over the prefixes waits where it takes these sums)
     wait_for_last();  // the pieces are written
     const int4 job = p.joins[blockIdx.x];
     const int s = job.x, h = job.y, parts = job.z;
@@ -1805,7 +1812,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
     auto write = [&](int r, float m, float l, float4 v) {
         const int row = group * rows + r;
         const int tk = row / p.G, hd = h * p.G + row - tk * p.G;
-        if (lane < LANES) emit<T, D>(p, s, tk, hd, lane * 4, v, m, l);
+        if (lane < LANES) emit<T, D, RAW>(p, s, tk, hd, lane * 4, v, m, l);
     };
     float m, l;
     float4 v;
@@ -1991,8 +1998,8 @@ cudaError_t go_join(const Params& p, const AttnPlan& pl, cudaStream_t s) {
     const bool few = (int64_t)p.num_seqs * p.H * 8 >= pl.runs;
     const int y = few ? (used + kJoinWarps - 1) / kJoinWarps : used;
     // begins while the pieces are still being written and waits for them itself
-    return launch_early(attn_combine_kernel<T, D>, dim3((unsigned)blocks, (unsigned)y), kJoinWarps * 32,
-                        0, s, p, pl.rows);
+    return launch_early(p.raw ? attn_combine_kernel<T, D, true> : attn_combine_kernel<T, D, false>,
+                        dim3((unsigned)blocks, (unsigned)y), kJoinWarps * 32, 0, s, p, pl.rows);
 }
 
 cudaError_t launch_attention_combine(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {
