@@ -30,7 +30,7 @@
 // 8 bits: the same four lanes own a row and find its largest magnitude with two
 // shuffles; codes are rounded as above, and a lane's eight of a group are one
 // store of 8 bytes, the row's four lanes together a sector.  16.8 thousand tokens of 48
-// heads, rotated, written and read back, 502 MB: 84 us, 6.0 TB/s.
+// heads, rotated, written and read back, 502 MB: 81 us, 6.2 TB/s.
 #include <float.h>
 
 #include "rkv_common.cuh"
@@ -741,10 +741,11 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const __grid_constant
 
 // ------------------------------------------------------------- q8 read --
 
-// Sixteen values of four rows a thread (a warp: neighbouring rows at a time), so that what
+// Sixteen values of two rows a thread (a warp: neighbouring rows at a time), so that what
 // has to be known before a row can be read, its length and its block, is waited for once
-// for all of them (16.8 thousand tokens' K and V: 28 us with a row a thread).
-constexpr int kReadRows = 4;
+// for both (16.8 thousand tokens written and read back: 92.4 us with a row a thread, 81.4,
+// with four 83.9, with eight 86.4).
+constexpr int kReadRows = 2;
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) q8_read_kernel(const __grid_constant__ Q8ReadArgs a,
                                                            int64_t total, int both, Div by_groups,
