@@ -385,3 +385,113 @@ def test_python_refusals():
     assert e.value.code == 3
     with pytest.raises(ValueError):
         pkg.rkv_prefix_attention_workspace_size(c.q, 1, 0, 1, 10)
+
+
+def test_prefixes_that_share_blocks():
+    """Two prefixes over the same blocks, at other lengths, a block twice in one of them, and own rows
+    in a prefix's blocks: rows are read, so any may be named again."""
+    c = Case([90, 64, 33], [0, 4, 7, 9], [9, 1, 0, 5, 16, 3, 8, 2, 1], 1, 2, 4, 128, 16, BF, seed=11)
+    c.ptable[1] = c.ptable[0]
+    c.ptable[2, 1] = c.ptable[2, 0]
+    c.table[4] = c.ptable[0, 0]
+    ws = c.ws()
+    out, lse = c.call(ws)
+    assert status(ws) == 0
+    c.compare(out, lse)
+
+
+@pytest.mark.parametrize("bits", [0, 8])
+def test_queries_written_just_before(bits):
+    """Captured with an append on one stream that writes the prefix's rows and the queries right before
+    (kernels begin while those before them end), the two calls of a graph on one workspace: replayed with
+    new inputs, the bits of calls with a synchronize between them."""
+    N, H, G, d, bs, n = 6, 2, 4, 128, 16, 200
+    pb = -(-n // bs)
+    ptable = torch.arange(pb, dtype=torch.int32, device=DEV).view(1, pb)
+    table = (pb + torch.arange(N, dtype=torch.int32, device=DEV)).view(N, 1)
+    K = torch.zeros(pb + N, H, bs, d, dtype=BF, device=DEV)
+    V = torch.zeros_like(K)
+    plens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    lens = torch.full((N,), 3, dtype=torch.int32, device=DEV)
+    plan = pkg.RopePlan(d)
+    pk, pv = (torch.zeros(1, n, H, d, dtype=BF, device=DEV) for _ in range(2))
+    nk, nv = (torch.zeros(N, 3, H, d, dtype=BF, device=DEV) for _ in range(2))
+    q = torch.zeros(N, 3, H * G, d, dtype=BF, device=DEV)
+    rq, one, two = torch.zeros_like(q), torch.zeros_like(q), torch.zeros_like(q)
+    ws = pkg.alloc_prefix_attention_workspace(q, H, bs, 1, pb * bs)
+    cache = pkg.alloc_q8_cache(pb + N, H, bs, d, device=DEV)
+    aws = pkg.alloc_attention_workspace(q, H, bs)
+
+    def fill(seed):
+        for i, x in enumerate((pk, pv, nk, nv, q)):
+            x.copy_(rnd(x.shape, BF, 100 * seed + i))
+
+    def run(wait):
+        pause = torch.cuda.synchronize if wait else lambda: None
+        if bits:
+            pkg.rkv_q8_append(cache, nk, nv, table, lens, rope=plan, q=q, out_q=rq)
+            pause()
+            pkg.rkv_q8_attention(rq, cache, table, lens, out=one, workspace=aws)
+            pause()
+            K8, V8 = pkg.rkv_q8_read(cache, table, lens, 3)
+            two[:, :, :H].copy_(K8.view(N, H, 3, d).transpose(1, 2))
+            two[:, :, H:2 * H].copy_(V8.view(N, H, 3, d).transpose(1, 2))
+            return
+        pkg.rkv_paged_append(K, V, pk, pv, ptable, plens, rope=plan)
+        pause()
+        pkg.rkv_paged_append(K, V, nk, nv, table, lens, rope=plan, q=q, out_q=rq)
+        pause()
+        pkg.rkv_prefix_attention(rq, K, V, ptable, plens, table, lens, out=one, workspace=ws)
+        pause()
+        pkg.rkv_prefix_attention(one, K, V, ptable, plens, table, lens, out=two, workspace=ws)
+
+    fill(0)
+    run(True)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run(False)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(False)
+    for seed in range(1, 9):
+        fill(seed)
+        run(True)
+        torch.cuda.synchronize()
+        want = [x.clone() for x in (one, two)]
+        for x in (one, two, rq, K, V):
+            x.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(one, want[0]) and torch.equal(two, want[1])
+
+
+def test_two_graphs_on_one_workspace():
+    """Two captured calls of other sizes share a workspace and are replayed in turn on one stream, without a
+    wait between them: each call writes what it reads there."""
+    a = Case([700], [0, 40], [12] * 40, 1, 2, 4, 128, 16, BF, seed=21)
+    b = Case([130, 90], [0, 9, 20], [40] * 20, 2, 2, 4, 64, 32, BF, seed=22)
+    cs = (a, b)
+    plain = [c.call(c.ws())[0] for c in cs]
+    ws = max((c.ws() for c in cs), key=lambda x: x.numel())
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    graphs, outs, held = [], [], []
+    for c in cs:
+        out = torch.zeros_like(c.q)
+        args = (c.q, c.K, c.V, c.ptable.to(DEV), ints(c.plens), c.table.to(DEV), ints(c.lens))
+        kw = dict(cu_seqs=ints(c.groups), out=out, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pkg.rkv_prefix_attention(*args, **kw)
+        graphs.append(g)
+        outs.append(out)
+        held.append((args, kw))
+    for _ in range(20):
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], plain[0]) and torch.equal(outs[1], plain[1])
