@@ -48,8 +48,8 @@
 // of 131071, G = 5: 47.0 us, 3.6 TB/s.  In steady state a warp spends 379 instructions
 // and an SM quarter 592 cycles on 16 rows, where HBM's rate would allow 435: no pipe is
 // above 55 in a hundred of them (logic; issue slots 64), the twelve warps of an SM
-// wait for their own last instructions.  8 bits: the same 64 sequences 58.9 us, 5.0 TB/s;
-// one of 131071, G = 8: 53.5 us, 5.2 TB/s: 432 instructions for 16 rows, some 240 of them, counted by hand,
+// wait for their own last instructions.  8 bits: the same 64 sequences 59.0 us, 5.0 TB/s;
+// one of 131071, G = 8: 53.8 us, 5.2 TB/s: 432 instructions for 16 rows, some 240 of them, counted by hand,
 // codes to bf16 and both operands' order, where HBM's rate would allow 720 cycles: logic 54
 // in a hundred, issue slots 52 (three stages at two blocks an SM: 62.6 and 53.3).
 #include <cuda_fp16.h>

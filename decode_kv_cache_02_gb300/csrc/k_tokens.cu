@@ -30,7 +30,7 @@
 // 8 bits: the same four lanes own a row and find its largest magnitude with two
 // shuffles; codes are rounded as above, and a lane's eight of a group are one
 // store of 8 bytes, the row's four lanes together a sector.  16.8 thousand tokens of 48
-// heads, rotated, written and read back, 502 MB: 81 us, 6.2 TB/s.
+// heads, rotated, written and read back, 502 MB: 82 us, 6.1 TB/s.
 #include <float.h>
 
 #include "rkv_common.cuh"
