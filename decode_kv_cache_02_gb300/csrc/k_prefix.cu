@@ -12,6 +12,11 @@
 // thread holds 8 queries x 4 rows of the logits (rows tx, tx + 16, ..: reads of 8
 // neighbouring rows of 528 bytes meet no bank twice) and 8 queries x D / 16 of the
 // output, so four FMAs stand against each word that is read.
+//
+// Measured (one GB300, under the profiler, cold): fp32, 2 prefixes to 2049 rows, 24 sequences,
+// 4 KV heads, head_dim 128: the pass 28 us (255 registers, two blocks an SM, one wave; issue
+// slots 43 in a hundred), its join 15; FMAs alone would take 5.  The join waits for
+// memory and for its first warp's look at what the blocks left.
 #include <atomic>
 
 #include "rkv_prefix.cuh"
