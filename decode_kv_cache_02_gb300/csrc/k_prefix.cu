@@ -73,7 +73,9 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_kernel(const __grid_consta
     while (next_piece<kUnit>(p, run, 0, place, c)) {
         if (tid == 0 && bad_length(p, c)) set_error(p.status, kDevErrIndex, (unsigned)c.i);
         __syncthreads();  // the piece before has been read
-        for (int e = tid; e < kTile * (D / 4); e += kThreads) {
+        // Only where rows follow: the copies are waited for with the first unit's, and copies of
+        // a piece without rows (an empty prefix) could land behind those of the next one.
+        for (int e = c.c0 < c.c1 ? tid : kTile * (D / 4); e < kTile * (D / 4); e += kThreads) {
             const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
             const bool ok = r < c.rows;
             int s = 0, tk = 0, hd = 0;

@@ -495,3 +495,27 @@ def test_two_graphs_on_one_workspace():
             g.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], plain[0]) and torch.equal(outs[1], plain[1])
+
+
+@pytest.mark.parametrize("dt, bs", [(FP, 16), (BF, 4), (BF, 16)], ids=["fp32", "bf16-b4", "bf16"])
+@pytest.mark.parametrize("every", [2, 5])
+def test_empty_prefixes_between_others(dt, bs, every):
+    """Empty prefixes in turn with others, several of each a block, whose queries take one another's place in shared
+    memory: call after call the bits of the first, and those of the definition."""
+    P, S = 1200, 2400
+    plens = [0 if p % every else 1 + p % 70 for p in range(P)]
+    c = Case(plens, list(range(0, S + 1, 2)), [1 + s % 3 for s in range(S)], 1, 1, 2, 64, bs, dt, seed=31)
+    ws = c.ws()
+    out, lse = c.call(ws)
+    for _ in range(10):
+        again, lse2 = c.call(ws)
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
+    assert status(ws) == 0
+    c.K, c.V = c.K.cpu(), c.V.cpu()
+    c.groups = list(range(0, 401, 2))
+    for first in (0, P - 200):  # 200 prefixes at either end
+        part = Case.__new__(Case)
+        part.__dict__.update(c.__dict__)
+        a, b = slice(first, first + 200), slice(2 * first, 2 * first + 400)
+        part.plens, part.ptable, part.lens, part.table, part.q = c.plens[a], c.ptable[a], c.lens[b], c.table[b], c.q[b]
+        part.compare(out[b], lse[b])
