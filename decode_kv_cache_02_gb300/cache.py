@@ -480,7 +480,8 @@ def rkv_q8_read(cache: Q8Cache, block_table, lens, n_rows: int, first=None, out_
 
 def rkv_attention_workspace_size(q, num_kv_heads: int, max_rows: int) -> int:
     """Workspace bytes of rkv_paged_attention, rkv_q4_attention and rkv_q8_attention for q [S,
-    n_new, heads, d] over at most max_rows rows a sequence, on q's device."""
+    n_new, heads, d] over at most max_rows rows a sequence, or for fewer sequences, tokens or
+    rows, on q's device."""
     if q.is_cuda and q.get_device() != _current_device():
         with torch.cuda.device(q.device):
             return rkv_attention_workspace_size(q, num_kv_heads, max_rows)

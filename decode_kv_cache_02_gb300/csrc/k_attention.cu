@@ -1940,6 +1940,12 @@ bool is_f32(const AttnArgs& a) { return !a.bits && a.dtype == RKV_DTYPE_FP32; }
 // 4096 18.1 / 16.6; at 4 bits one of 1152 9.2 / 7.4, of 4096 10.5 / 9.7.
 constexpr int kClusterUnits = 64;
 
+// Blocks that an SM holds at once: shared memory for two (one with fp32 rows of 128), with
+// packed rows and 8 queries registers for three.
+static int resident(const AttnArgs& a, int rows) {
+    return is_f32(a) && a.d == 128 ? 1 : (a.bits && rows == 8 ? 3 : 2);
+}
+
 AttnPlan attn_plan(const AttnArgs& a) {
     AttnPlan pl;
     const int R = a.n_new * a.G;
@@ -1952,10 +1958,7 @@ AttnPlan attn_plan(const AttnArgs& a) {
     pl.unit = kWarps * (is_f32(a) ? 16 : (a.bits ? Stage<128, 4>::KEYS
                                                : (a.d == 128 ? Stage<128, 0>::KEYS
                                                              : Stage<64, 0>::KEYS)));
-    // as many blocks as the device's SMs hold at once: shared memory for two (one with
-    // fp32 rows of 128), with 4-bit rows registers for three
-    const int sms = tc::sm_count();
-    const int blocks = sms * (is_f32(a) && a.d == 128 ? 1 : (a.bits && pl.rows == 8 ? 3 : 2));
+    const int sms = tc::sm_count(), blocks = sms * resident(a, pl.rows);
     const int64_t per = ((int64_t)a.max_rows + pl.unit - 1) / pl.unit, problems = a.num_seqs * a.pg.H;
     // a few short sequences: a cluster for each problem, one launch
     if (!is_f32(a) && per > 1 && per <= kClusterUnits && problems * pl.groups * kCluster <= 2 * sms) {
@@ -1978,6 +1981,18 @@ AttnPlan attn_plan(const AttnArgs& a) {
     pl.partial_floats =
         pl.join ? (size_t)pl.runs * pl.groups * (2 * pl.rows * (a.d + 2) + 4) : 0;
     return pl;
+}
+
+// Runs are rounded up to whole groups, so a plan with fewer groups may have more blocks
+// (7 queries a KV head, head_dim 128: 306 with 6 new tokens, 304 with 8).  This is at least
+// that of every plan for fewer sequences, tokens or rows: rows and groups grow with the
+// queries, units with everything, and 16 queries take more than 8 of three blocks an SM.
+size_t attn_most_floats(const AttnArgs& a) {
+    const AttnPlan pl = attn_plan(a);
+    if (!pl.join) return 0;
+    const int64_t units = a.num_seqs * a.pg.H * (((int64_t)a.max_rows + pl.unit - 1) / pl.unit) * pl.groups;
+    const int64_t blocks = (int64_t)tc::sm_count() * resident(a, pl.rows) + pl.groups - 1;
+    return (size_t)(units < blocks ? units : blocks) * (2 * pl.rows * (a.d + 2) + 4);
 }
 
 cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& pl, cudaStream_t s) {

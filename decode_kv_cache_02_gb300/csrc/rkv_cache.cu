@@ -263,9 +263,8 @@ cudaError_t run_combine(const void* x, cudaStream_t s) {
     return rkv::launch_attention_combine(c.args, c.plan, s);
 }
 
-size_t attention_bytes(const AttnPlan& p) {
-    return kAlign + (p.partial_floats * sizeof(float) + kAlign - 1) / kAlign * kAlign;
-}
+size_t aligned_floats(size_t n) { return (n * sizeof(float) + kAlign - 1) / kAlign * kAlign; }
+size_t attention_bytes(size_t scratch_floats) { return kAlign + aligned_floats(scratch_floats); }
 
 // The parts of an attention call that do not depend on its workspace: pools, tables and
 // rows.
@@ -329,7 +328,7 @@ int attend(const rkv_paged_desc* desc, int n_new, const rkv_rows* q, const void*
     if (!isfinite(scale)) return RKV_ERR_INVALID_ARG;
     call.plan = rkv::attn_plan(a);
     if (!countable(desc, a, call.plan)) return RKV_ERR_UNSUPPORTED;
-    if (!workspace || !aligned_ws(workspace) || workspace_bytes < attention_bytes(call.plan))
+    if (!workspace || !aligned_ws(workspace) || workspace_bytes < attention_bytes(call.plan.partial_floats))
         return RKV_ERR_WORKSPACE;
     if (desc->num_seqs == 0) return RKV_OK;
     if ((rc = check_attend(desc, n_new, q, K_pool, V_pool, four, eight, table, lens, scale, out, lse, bits, &a)))
@@ -341,13 +340,11 @@ int attend(const rkv_paged_desc* desc, int n_new, const rkv_rows* q, const void*
 
 // --------------------------------------------------------------- prefixes --
 
-size_t aligned_floats(size_t n) { return (n * sizeof(float) + kAlign - 1) / kAlign * kAlign; }
-
 struct PrefixCall {
     rkv::PrefixArgs args;
     AttnPlan own;
     rkv::PrefixPlan plan;
-    size_t own_bytes() const { return attention_bytes(own); }
+    size_t own_bytes() const { return attention_bytes(own.partial_floats); }
     // what a call of these sizes needs whatever its blocks are
     size_t bytes() const {
         size_t most = 0;
@@ -625,11 +622,11 @@ size_t rkv_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int m
     // one size serves the pool and the packed caches
     AttnArgs a;
     if (check_attention(desc, nullptr, n_new, max_rows, 0, &a)) return 0;
-    size_t n = attention_bytes(rkv::attn_plan(a));
+    size_t n = attention_bytes(rkv::attn_most_floats(a));
     if (desc->dtype == RKV_DTYPE_BF16)
         for (const int bits : {4, 8}) {
             a.bits = bits;
-            const size_t m = attention_bytes(rkv::attn_plan(a));
+            const size_t m = attention_bytes(rkv::attn_most_floats(a));
             if (m > n) n = m;
         }
     return n;

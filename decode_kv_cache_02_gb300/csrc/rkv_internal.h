@@ -309,6 +309,8 @@ struct AttnPlan {
     size_t partial_floats = 0;
 };
 AttnPlan attn_plan(const AttnArgs& a);
+// The most scratch of a call with these sizes or smaller ones.
+size_t attn_most_floats(const AttnArgs& a);
 cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
 cudaError_t launch_attention_combine(const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
 

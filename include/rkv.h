@@ -496,8 +496,8 @@ int rkv_q8_read(const rkv_paged_desc* desc, const rkv_q8_cache* cache,
  * probabilities times V, before they are divided, are up to 2^8 sum |V| (fp32).
  * q, out: rkv_rows by sequence and token (bf16 for 4-bit caches). */
 #define RKV_MAX_NEW_TOKENS 64
-/* Bytes for the current device (the work is cut for its SMs) and any of the caches;
- * 0: invalid sizes. */
+/* Bytes for the current device (the work is cut for its SMs) and any of the caches, of
+ * these sizes or smaller ones (num_seqs, n_new, max_rows); 0: invalid sizes. */
 size_t rkv_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int max_rows);
 int rkv_paged_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
                         const void* K_pool, const void* V_pool, const int32_t* block_table,
