@@ -611,7 +611,8 @@ def rkv_prefix_attention_workspace_size(q, num_kv_heads: int, max_rows: int, num
                                         max_prefix_rows: int) -> int:
     """Workspace bytes of rkv_prefix_attention for q [S, n_new, heads, d] over at
     most max_rows own rows a sequence and num_prefixes prefixes of at most
-    max_prefix_rows rows, however the sequences are shared out, on q's device."""
+    max_prefix_rows rows, however the sequences are shared out, or for fewer of any of
+    them, on q's device."""
     if q.is_cuda and q.get_device() != _current_device():
         with torch.cuda.device(q.device):
             return rkv_prefix_attention_workspace_size(q, num_kv_heads, max_rows, num_prefixes,

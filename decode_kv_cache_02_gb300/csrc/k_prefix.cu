@@ -27,6 +27,8 @@ namespace {
 
 constexpr int kTile = 64, kUnit = 64, kThreads = 128;
 constexpr int kMaxTeam = 8;
+// Scratch of a block: two pieces of a tile, and what it leaves to join (4 words).
+constexpr size_t block_floats(int tile, int d) { return 2 * (size_t)tile * (d + 2) + 4; }
 
 RKV_DEV uint32_t smem_at(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -391,8 +393,9 @@ cudaError_t go_join(const Params& p, int64_t tiles, cudaStream_t s) {
 }  // namespace
 }  // namespace prefix
 
-PrefixPlan prefix_plan(const PrefixArgs& a, bool tensor) {
+PrefixPlan prefix_plan(const PrefixArgs& a) {
     using namespace prefix;
+    const bool tensor = tc_takes(a);
     PrefixPlan pl;
     const AttnArgs& w = a.own;
     const int64_t R = (int64_t)w.G * w.n_new;
@@ -421,10 +424,33 @@ PrefixPlan prefix_plan(const PrefixArgs& a, bool tensor) {
     if (runs < 1) runs = 1;
     pl.runs = (int)runs;
     pl.raw_floats = (size_t)w.num_seqs * R * w.pg.H * (w.d + 2);
-    pl.partial_floats = (size_t)pl.runs * pl.team * (2 * pl.tile * (w.d + 2) + 4);
+    pl.partial_floats = (size_t)pl.runs * pl.team * block_floats(pl.tile, w.d);
     return pl;
 }
-PrefixPlan prefix_plan(const PrefixArgs& a) { return prefix_plan(a, prefix::tc_takes(a)); }
+
+// A call with fewer sequences or prefixes may take larger tiles and more blocks (64 sequences:
+// tiles of 128 queries with two prefixes, of 256 with one), so this follows no one plan: as
+// many blocks as a plan of these sizes could have units, in the largest tile and team that any
+// number of prefixes leads to.
+size_t prefix_most_floats(const PrefixArgs& a) {
+    using namespace prefix;
+    const AttnArgs& w = a.own;
+    const int64_t rows = w.num_seqs * (int64_t)w.G * w.n_new, sms = tc::sm_count();
+    const int64_t per = ((int64_t)a.max_rows + kUnit - 1) / kUnit, groups = (int64_t)a.num_prefixes + 1;
+    const auto most = [&](int64_t resident, int64_t tile, int64_t least, int64_t team) {
+        const int64_t units = (rows / least + groups * team) * w.pg.H * per;
+        const int64_t blocks = resident > team ? resident : team;
+        return (size_t)(units < blocks ? units : blocks) * block_floats((int)tile, w.d);
+    };
+    size_t n = most(2 * sms, kTile, kTile, 1);
+    if (w.dtype == RKV_DTYPE_BF16) {
+        const int64_t teams = (rows + 255) / 256;
+        const size_t m = rows <= 128 ? most(sms, 128, 128, 1)
+                                     : most(sms, 256, 128, teams > kMaxTeam ? kMaxTeam : teams);
+        if (m > n) n = m;
+    }
+    return n;
+}
 
 cudaError_t launch_prefix(const PrefixArgs& a, const PrefixPlan& pl, cudaStream_t s) {
     const prefix::Params p = prefix::params(a, pl);

@@ -345,15 +345,10 @@ struct PrefixCall {
     AttnPlan own;
     rkv::PrefixPlan plan;
     size_t own_bytes() const { return attention_bytes(own.partial_floats); }
-    // what a call of these sizes needs whatever its blocks are
+    // of calls with these sizes or smaller ones, whatever their blocks are
     size_t bytes() const {
-        size_t most = 0;
-        for (int tensor = 0; tensor < (args.own.dtype == RKV_DTYPE_BF16 ? 2 : 1); ++tensor) {
-            const rkv::PrefixPlan p = rkv::prefix_plan(args, tensor != 0);
-            const size_t n = own_bytes() + aligned_floats(p.raw_floats) + aligned_floats(p.partial_floats);
-            if (n > most) most = n;
-        }
-        return most;
+        return attention_bytes(rkv::attn_most_floats(args.own)) + aligned_floats(plan.raw_floats) +
+               aligned_floats(rkv::prefix_most_floats(args));
     }
 };
 

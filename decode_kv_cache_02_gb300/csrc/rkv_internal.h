@@ -333,8 +333,9 @@ struct PrefixPlan {
     int64_t tiles = 0;
     size_t raw_floats = 0, partial_floats = 0;
 };
-PrefixPlan prefix_plan(const PrefixArgs& a);  // what a call takes
-PrefixPlan prefix_plan(const PrefixArgs& a, bool tensor);
+PrefixPlan prefix_plan(const PrefixArgs& a);
+// The most scratch for pieces of a call with these sizes or smaller ones, over pools of any blocks.
+size_t prefix_most_floats(const PrefixArgs& a);
 cudaError_t launch_prefix(const PrefixArgs& a, const PrefixPlan& p, cudaStream_t s);
 cudaError_t launch_prefix_join(const PrefixArgs& a, const PrefixPlan& p, cudaStream_t s);
 

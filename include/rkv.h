@@ -539,7 +539,8 @@ typedef struct {
     int32_t max_rows;   /* bounds lens (>= 1), at most 2^30 and the table's rows */
 } rkv_prefixes;
 
-/* Bytes for the current device; 0: invalid sizes. */
+/* Bytes for the current device, of these sizes or smaller ones (num_seqs, n_new, the
+ * max_rows of both, num_prefixes), over blocks of any size; 0: invalid sizes. */
 size_t rkv_prefix_attention_workspace_size(const rkv_paged_desc* desc, int n_new, int max_rows,
                                            const rkv_prefixes* prefixes);
 

@@ -519,3 +519,25 @@ def test_empty_prefixes_between_others(dt, bs, every):
         a, b = slice(first, first + 200), slice(2 * first, 2 * first + 400)
         part.plens, part.ptable, part.lens, part.table, part.q = c.plens[a], c.ptable[a], c.lens[b], c.table[b], c.q[b]
         part.compare(out[b], lse[b])
+
+
+@pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "fp32"])
+def test_one_workspace_while_sequences_end(dt):
+    """A workspace made for the largest batch serves the batches after it: sequences and whole prefixes leave, and
+    tiles and teams are chosen anew. The bits of calls with a workspace of their own; nothing behind it is written."""
+    most = Case([700, 90, 400], [0, 100, 180, 257], [4 + s % 7 for s in range(257)], 2, 2, 4, 128, 16, dt, seed=41)
+    n = most.ws().numel()
+    room = torch.full((n + (1 << 20),), 0xa5, dtype=torch.uint8, device=DEV)
+    for sizes in ([100, 80, 77], [100, 80, 76], [129], [128], [65, 0, 64], [64], [33], [32], [17, 16], [16], [5, 3, 2], [1]):
+        c = Case.__new__(Case)
+        c.__dict__.update(most.__dict__)
+        S = sum(sizes)
+        c.plens, c.ptable = most.plens[:len(sizes)], most.ptable[:len(sizes)]
+        c.groups = [sum(sizes[:i]) for i in range(len(sizes) + 1)]
+        c.lens, c.table, c.q = most.lens[:S], most.table[:S], most.q[:S].contiguous()
+        room[:256] = 0
+        out, lse = c.call(room[:n])
+        assert status(room[:n]) == 0 and (room[n:] == 0xa5).all()
+        own, lse2 = c.call()
+        assert torch.equal(out, own) and torch.equal(lse, lse2)
+        c.compare(out[:3], lse[:3], seqs=min(S, 3))
