@@ -1524,6 +1524,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 && BITS ? 3 : 2) attn_ker
             st = st == ring + (S::DEPTH - 1) * S::BYTES ? ring : st + S::BYTES;
         }
         cp_wait<0>();
+        // (behind this block's wait: the pass over shared prefixes relies on that, see launch_early)
         if (place.u0 >= place.u1) let_next_begin();
 
         // sums over the lanes that share a query; from here on m is the base-2 logit that they are
@@ -1606,7 +1607,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const __grid_cons
     const float* q32 = reinterpret_cast<const float*>(p.q);
     const float sign = p.flip ? -1.f : 1.f;
     uint8_t* ring = smem + warp * (S::DEPTH * S::BYTES);
-    wait_for_last();
+    wait_for_last();  // (first, as in attn_kernel: see launch_early)
 
     Place place = find_place<kWarps * 32>(p, UNIT, run);
     Piece c{};
@@ -1783,7 +1784,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_combine_kernel(
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = blockIdx.x % p.groups;
     const int run = blockIdx.x / p.groups;
-    if (RAW) let_next_begin();  // (the pass over the prefixes waits where it takes these sums)
+    // before the wait: the pass over the prefixes waits itself where it takes these sums, and what
+    // it reads before that is there, since the pass in front of this join has waited for it
+    if (RAW) let_next_begin();
     wait_for_last();  // the pieces are written
     const int4 job = p.joins[blockIdx.x];
     const int s = job.x, h = job.y, parts = job.z;

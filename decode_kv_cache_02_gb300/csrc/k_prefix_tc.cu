@@ -326,8 +326,9 @@ prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
-    // (Begins while the own rows' pass ends: that pass began behind everything before it, so
-    // queries, pools and tables are there; its sums are waited for where they are read.)
+    // (Begins while the own rows' pass ends, every block of which has waited for everything before
+    // it, so queries, pools and tables are there; its sums are waited for where they are read.
+    // See launch_early.)
     Place place = find_place<kUnit>(p, run);
     Piece c{};
     bool ok = true;

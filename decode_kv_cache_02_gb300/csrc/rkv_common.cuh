@@ -79,8 +79,17 @@ RKV_DEV float warp_max(float v) {
 // behind it begin, which waits in turn.  Call after call on a stream this takes
 // 2 us off each (16384 tokens rotated: 53.8 -> 51.2 us, appended 64.9 -> 62.6);
 // captured, an append and an attention of one sequence of 1152 take 9.4 us
-// instead of 10.2.  The join of an attention lets nothing begin: what began there
+// instead of 10.2.  The join of a plain attention lets nothing begin: what began there
 // would hold its SMs up (16 sequences of 16384 at 4 bits 57.4 -> 58.4 us).
+//
+// One kernel looks before it waits: the pass over shared prefixes on the tensor cores
+// reads its tables, queries and pools at once and waits where it takes the sums over the
+// own rows.  What came before the call is over by then, because of what stands between:
+// it begins once every block of the attention over the own rows has let it (or the join
+// between, which passes that on before its own wait) or has ended, and those blocks
+// have waited before either.  So in attn_kernel and attn_f32_kernel wait_for_last()
+// stays first and let_next_begin() behind it, and no kernel that lets the next begin
+// before its own wait (as the token kernels do) may come in place of them.
 RKV_DEV void wait_for_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 RKV_DEV void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <typename... P, typename... A>

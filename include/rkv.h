@@ -320,8 +320,9 @@ int rkv_paged_compress(const rkv_paged_desc* desc, void* K_pool, void* V_pool,
  * slice of a fused projection is taken as it is.
  *
  * The launches of these calls may begin while the stream's last kernel ends
- * (programmatic dependent launch) and wait for it before they read or write
- * anything: results are in stream order as ever, also in captured graphs. */
+ * (programmatic dependent launch), and a call reads and writes nothing before
+ * everything in front of it is over: results are in stream order as ever, also in
+ * captured graphs. */
 typedef struct {
     void* data;
     int64_t seq_stride;   /* unused where tokens are numbered through */
