@@ -225,9 +225,9 @@ __global__ void __launch_bounds__(kThreads, 2) prefix_kernel(const __grid_consta
 // Joins the pieces of the tiles that begin in one run and end in a later one, and the
 // own rows' sums.  A block takes 32 queries (lanes) of a tile and 32 dimensions: up to
 // kFew pieces by a warp for each four of them, more by all warps together.
-constexpr int kJoinWarps = 8, kFew = 16, kMaxBlocks = 320, kJoinLook = kMaxBlocks / 32;
+constexpr int kJoinWarps = 8, kJoinResident = 3, kFew = 16, kMaxBlocks = 320, kJoinLook = kMaxBlocks / 32;
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32, 3) prefix_join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, kJoinResident) prefix_join_kernel(const __grid_constant__ Params p) {
     __shared__ float4 sh_v[kJoinWarps][8][32];
     __shared__ float sh_m[kJoinWarps][32], sh_l[kJoinWarps][32];
     __shared__ int4 sh_job[kMaxBlocks];  // p.joins of the blocks that left something, and which they are
@@ -382,10 +382,12 @@ cudaError_t go(const Params& p, cudaStream_t s) {
 }
 template <typename T, int D>
 cudaError_t go_join(const Params& p, int64_t tiles, cudaStream_t s) {
-    // a block for every 32 queries and 32 dimensions of a tile, for as many tiles at a time
-    // as six such blocks an SM take
+    // a block for every 32 queries and 32 dimensions of a tile, for as many tiles at a time as the
+    // SMs hold such blocks (registers for kJoinResident): those of a second wave would each look up
+    // again what there is to join (us a call with one and with two waves, two runs each: 64 samples
+    // of 8192 rows 64.3, 65.0 and 65.3, 65.9; 8 new tokens 46.4, 46.5 and 47.8, 47.6)
     const int y = p.tile / 32 * (D / 32);
-    int64_t x = 6 * tc::sm_count() / y;
+    int64_t x = kJoinResident * tc::sm_count() / y;
     if (x > tiles) x = tiles;
     return launch_early(prefix_join_kernel<T, D>, dim3((unsigned)(x < 1 ? 1 : x), (unsigned)y), kJoinWarps * 32, 0, s, p);
 }
