@@ -14,9 +14,11 @@
 // output, so four FMAs stand against each word that is read.
 //
 // Measured (one GB300, under the profiler, cold): fp32, 2 prefixes to 2049 rows, 24 sequences,
-// 4 KV heads, head_dim 128: the pass 28 us (255 registers, two blocks an SM, one wave; issue
-// slots 43 in a hundred), its join 15; FMAs alone would take 5.  The join waits for
-// memory and for its first warp's look at what the blocks left.
+// 4 KV heads, head_dim 128: the pass 28 us (253 registers, two blocks an SM, one wave), its join
+// 15; FMAs alone would take 5.  What bounds the pass: a step waits for all of its copies before
+// it multiplies (one buffer, so every 64 rows pay a trip to memory, which only the SM's other
+// block fills), and with 48 queries a prefix and head a quarter of each tile is empty.  The join
+// waits for memory and for its first warp's look at what the blocks left.
 #include <atomic>
 
 #include "rkv_prefix.cuh"
@@ -404,8 +406,13 @@ PrefixPlan prefix_plan(const PrefixArgs& a) {
     const int sms = tc::sm_count();
     pl.tensor = tensor;
     if (tensor) {
-        // two groups of 128 queries a block, or, where a prefix has 128 or fewer (on
-        // average: how they are shared out is the device's), two shares of its rows
+        // Two groups of 128 queries a block, or, where a prefix has 128 or fewer, two shares of
+        // its rows.  On average: how the sequences are shared out is known on the device alone, and
+        // those without a prefix count too.  Groups far from the average cost time, not values: 8 of
+        // 512 sequences on 16384 rows 181 us (teams of eight blocks, seven without queries) where
+        // those 8 by themselves take 35 and the others 69; two prefixes of 16384 with 2 and 126
+        // sequences 82, with 64 each 72; one with 113 of 128 sequences beside 15 with one each
+        // 189, with 8 each 197 (8 KV heads, G = 4, to 64 own rows).
         const int64_t groups = a.num_prefixes > 0 ? a.num_prefixes : 1, each = w.num_seqs * R / groups;
         pl.tile = each <= 128 ? 128 : 256;
         const int64_t tiles = (each + pl.tile - 1) / pl.tile;

@@ -24,14 +24,16 @@
 // Why units of 64 rows: at head_dim 128 O takes half of TMEM, and the other half holds two
 // buffers of S for each group only if they are 64 columns wide.  With one buffer of 128 the
 // next S waits until P V is done with it, 340 cycles behind the pipe's own time, and the
-// softmax waits for that S: 241 us for the case below where two buffers take 212, although
-// S in steps of 64 costs the pipe half as much again (48 cycles an MMA, the operands'
-// shared memory, where 128 columns take 64).
+// softmax waits for that S: 241 us for the case below where two buffers took 212 when the
+// step was measured by itself, although S in steps of 64 costs the pipe half as much again
+// (48 cycles an MMA, the operands' shared memory, where 128 columns take 64).
 //
 // Measured (one GB300, head_dim 128, 8 KV heads): 128 samples of 131071 rows, G = 4, 275
 // GFLOP: 173 us from the first piece to the last, 1.6 PFLOP/s; about 1600 cycles a step of
-// 2 x 128 queries, of which the products take 1280.  A piece's beginning (its place on the
-// line, queries, first tiles) and end take about 4 us each, which bounds short prefixes.
+// 2 x 128 queries, of which the products take 1280.  The whole call takes 220 us over many
+// calls on the same inputs, 227 with inputs that change from call to call.  A piece's beginning
+// (its place on the line, queries, first tiles) and end take about 4 us each, which bounds short
+// prefixes.
 // Every wait is bounded; one that runs out records a device error, and all roles end.
 #include <cuda.h>
 #include <cuda_runtime.h>

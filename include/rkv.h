@@ -512,7 +512,8 @@ int rkv_q4_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
  * bf16 numbers, exactly; K's scale meets the logit and V's the probability in
  * fp32, and the probability times the scale goes on as a bf16 cache's
  * probabilities do (two bf16 parts, one where n_new * gqa_group is above 16).
- * What a hidden row holds, codes or scale, reaches no query. */
+ * What a hidden row holds, codes or scale, reaches no query.  Rows of V count in full where
+ * their largest magnitude is 2^-100 or more, queries below 2^112 (q . code stays finite). */
 int rkv_q8_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
                      const rkv_q8_cache* cache, const int32_t* block_table,
                      const int32_t* lens, int max_rows, float scale, const rkv_rows* out,
@@ -552,7 +553,9 @@ size_t rkv_prefix_attention_workspace_size(const rkv_paged_desc* desc, int n_new
  * tables; a cu_seqs that descends or passes the last sequence is recorded and cut.
  * The probabilities of a prefix's rows meet a bf16 V as one bf16 part (2^-8 of
  * them).  Prefixes are read by tensor-core kernels where the pools are bf16 with
- * blocks of 8 rows or more, else on the CUDA cores. */
+ * blocks of 8 rows or more, else on the CUDA cores.  The work is cut for num_seqs /
+ * num_prefixes sequences a prefix: sequences without one are better off in a call of their
+ * own where they are many (results are the same). */
 int rkv_prefix_attention(const rkv_paged_desc* desc, int n_new, const rkv_rows* q,
                          const void* K_pool, const void* V_pool, const rkv_prefixes* prefixes,
                          const int32_t* block_table, const int32_t* lens, int max_rows, float scale,
